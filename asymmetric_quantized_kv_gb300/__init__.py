@@ -6,4 +6,4 @@ Importing the binding fails when the library has not been built.
 """
 from . import _binding as binding  # noqa: F401
 from ._binding import *  # noqa: F401,F403
-from .cache import PagedKVCache, make_config, src_torch_dtype  # noqa: F401
+from .cache import PagedKVCache, make_config, make_rope, src_torch_dtype  # noqa: F401

@@ -17,11 +17,14 @@ LIB_PATH = os.path.join(HERE, "libkvq.so")
 KVQ_OK, KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED, KVQ_ERR_CUDA, KVQ_ERR_CAPACITY, KVQ_ERR_WORKSPACE = range(6)
 KVQ_INT2, KVQ_INT4, KVQ_INT8, KVQ_FP8_E4M3, KVQ_FP8_E5M2 = 2, 4, 8, 9, 10
 KVQ_SYM_ABSMAX, KVQ_ASYM_MINMAX = 0, 1
-KVQ_PER_TENSOR, KVQ_PER_TOKEN, KVQ_PER_CHANNEL = 0, 1, 2
+KVQ_PER_TENSOR, KVQ_PER_TOKEN, KVQ_PER_CHANNEL, KVQ_PER_BLOCK = 0, 1, 2, 3
 KVQ_F32, KVQ_BF16, KVQ_F16 = 0, 1, 2
 KVQ_DEV_BAD_PAGE, KVQ_DEV_OVERFLOW, KVQ_DEV_TIMEOUT, KVQ_DEV_BAD_LENGTH = 1, 2, 4, 8
 KVQ_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 KVQ_KERNEL_GENERIC, KVQ_KERNEL_ROPE_I8I4, KVQ_KERNEL_FP8, KVQ_KERNEL_INT2 = 0, 1, 2, 3
+KVQ_KERNEL_BLOCK8 = 4
+KVQ_ROPE_INTERLEAVED, KVQ_ROPE_HALVES = 0, 1
+KVQ_MASK_NONE, KVQ_MASK_CAUSAL = 0, 1
 
 
 class kvq_qspec(ctypes.Structure):
@@ -40,6 +43,10 @@ class kvq_cache(ctypes.Structure):
                 ("k_win", c_void_p), ("v_win", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
                 ("batch", c_int32), ("max_pages_per_seq", c_int32), ("n_pages", c_int32),
                 ("status", c_void_p), ("rope_table", c_void_p), ("rope_positions", c_int32)]
+
+
+class kvq_rope(ctypes.Structure):
+    _fields_ = [("cos_sin", c_void_p), ("positions", c_int32), ("rot_dim", c_int32), ("pairing", c_int32)]
 
 
 class KvqError(RuntimeError):
@@ -71,6 +78,11 @@ def _load():
                                                    c_void_p]),
         "kvq_dequantize": (c_int32, [P(kvq_config), P(kvq_cache), c_int32, c_int32, c_int32, c_void_p,
                                      c_void_p, c_void_p]),
+        "kvq_rope_append": (c_int32, [P(kvq_config), P(kvq_cache), P(kvq_rope), c_void_p, c_void_p, c_void_p, c_int64,
+                                      c_int64, c_int64, c_int32, c_void_p, c_void_p, c_void_p]),
+        "kvq_query_workspace_bytes": (c_size_t, [P(kvq_config), c_int32, c_int32]),
+        "kvq_query_attention": (c_int32, [P(kvq_config), P(kvq_cache), c_void_p, c_int32, c_void_p, c_int32, c_void_p,
+                                          c_float, c_void_p, c_size_t, c_void_p]),
         "kvq_decode_kernel": (c_int32, [P(kvq_config), P(kvq_cache), P(c_int32)]),
         "kvq_selftest_bounded_wait": (c_int32, [c_void_p, c_void_p]),
         "kvq_status_string": (ctypes.c_char_p, [c_int32]),
@@ -145,6 +157,27 @@ def kvq_quantize_append(cfg, cache: kvq_cache, k_new, v_new, n_new, n_new_per_se
     _check("kvq_quantize_append",
            LIB.kvq_quantize_append(ctypes.byref(cfg), ctypes.byref(cache), _ptr(k_new), _ptr(v_new), int(n_new),
                                    _ptr(n_new_per_seq), _stream(stream)))
+
+
+def kvq_rope_append(cfg, cache: kvq_cache, rope: kvq_rope, q, k_new, v_new, n_new, n_new_per_seq=None, q_out=None,
+                    q_stride=0, k_stride=0, v_stride=0, stream=None):
+    """kvq_quantize_append with q and the keys rotated to their positions; strides in elements between rows."""
+    _check("kvq_rope_append",
+           LIB.kvq_rope_append(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(rope), _ptr(q), _ptr(k_new),
+                               _ptr(v_new), int(q_stride), int(k_stride), int(v_stride), int(n_new),
+                               _ptr(n_new_per_seq), _ptr(q_out), _stream(stream)))
+
+
+def kvq_query_workspace_bytes(cfg: kvq_config, batch: int, n_q: int) -> int:
+    return LIB.kvq_query_workspace_bytes(ctypes.byref(cfg), batch, n_q)
+
+
+def kvq_query_attention(cfg, cache: kvq_cache, q, n_q, n_q_per_seq, mask, out, softmax_scale, workspace, stream=None):
+    nbytes = workspace.numel() * workspace.element_size()
+    _check("kvq_query_attention",
+           LIB.kvq_query_attention(ctypes.byref(cfg), ctypes.byref(cache), _ptr(q), int(n_q), _ptr(n_q_per_seq),
+                                   int(mask), _ptr(out), float(softmax_scale), _ptr(workspace), nbytes,
+                                   _stream(stream)))
 
 
 def kvq_decode_attention(cfg, cache: kvq_cache, q, out, softmax_scale, workspace, stream=None):

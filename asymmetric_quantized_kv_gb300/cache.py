@@ -20,6 +20,16 @@ def make_config(num_q_heads, num_kv_heads, head_dim, k, v, residual, page_size, 
     return cfg
 
 
+def make_rope(cos_sin, rot_dim, pairing=B.KVQ_ROPE_INTERLEAVED) -> B.kvq_rope:
+    """The position rotation of append_rope.  cos_sin: [positions, rot_dim] float32 device tensor, the cosines of the
+    rot_dim / 2 pairs, then their sines; the caller keeps it alive."""
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != rot_dim or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous float32 tensor of [positions, rot_dim]")
+    rope = B.kvq_rope(cos_sin.data_ptr(), cos_sin.shape[0], rot_dim, pairing)
+    rope.tensor = cos_sin  # the table outlives the struct
+    return rope
+
+
 def src_torch_dtype(cfg) -> torch.dtype:
     return torch.bfloat16 if cfg.src_dtype == B.KVQ_BF16 else torch.float32
 
@@ -34,27 +44,57 @@ class PagedKVCache:
         pages can hold (rounded up to a multiple of 32, as the kernel reads whole
         32-position tables), False leaves the decode kernel to compute the cos/sin,
         and a (tensor, positions) pair shares a table built by kvq_rope_table_init."""
+        n_pages = n_pages if n_pages is not None else batch * max_pages_per_seq
+        dev = torch.device(device)
+        pages = torch.zeros(n_pages * B.kvq_page_bytes(cfg), dtype=torch.uint8, device=dev)
+        if block_table is None:
+            block_table = torch.arange(batch * max_pages_per_seq, dtype=torch.int32).reshape(batch, -1)
+        block_table = torch.as_tensor(block_table, dtype=torch.int32).reshape(batch, max_pages_per_seq).to(dev)
+        seq_lens = torch.zeros(batch, dtype=torch.int32, device=dev)
+        R, H, D = cfg.residual, cfg.num_kv_heads, cfg.head_dim
+        dt = src_torch_dtype(cfg)
+        k_win = torch.zeros(batch, max(R, 1), H, D, dtype=dt, device=dev) if R else None
+        v_win = torch.zeros(batch, max(R, 1), H, D, dtype=dt, device=dev) if R else None
+        self._bind(cfg, pages, block_table, seq_lens, k_win, v_win, rope_table)
+
+    @classmethod
+    def over(cls, cfg, pages, block_table, seq_lens, k_win=None, v_win=None, rope_table=False):
+        """A cache over buffers that the caller owns: pages (n_pages * kvq_page_bytes bytes), block_table
+        [batch, max_pages_per_seq] and seq_lens [batch] int32, and the residual windows [batch, R, Hkv, D] in
+        the source dtype (None when R is 0).  All contiguous, on one device."""
+        page = B.kvq_page_bytes(cfg)
+        if pages.dtype != torch.uint8 or not pages.is_contiguous() or pages.numel() == 0 or pages.numel() % page:
+            raise ValueError(f"pages must be contiguous uint8 of a multiple of {page} bytes")
+        batch = seq_lens.numel()
+        for name, t, shape, dt in (("block_table", block_table, (batch, block_table.shape[-1]), torch.int32),
+                                   ("seq_lens", seq_lens, (batch,), torch.int32),
+                                   ("k_win", k_win, (batch, cfg.residual, cfg.num_kv_heads, cfg.head_dim), None),
+                                   ("v_win", v_win, (batch, cfg.residual, cfg.num_kv_heads, cfg.head_dim), None)):
+            if t is None and dt is None and cfg.residual == 0:
+                continue
+            if (t is None or tuple(t.shape) != shape or t.dtype != (dt or src_torch_dtype(cfg))
+                    or not t.is_contiguous() or t.device != pages.device):
+                raise ValueError(f"{name} must be contiguous {dt or src_torch_dtype(cfg)} of shape {shape} beside the pages")
+        self = cls.__new__(cls)
+        self._bind(cfg, pages, block_table, seq_lens, k_win, v_win, rope_table)
+        return self
+
+    def _bind(self, cfg, pages, block_table, seq_lens, k_win, v_win, rope_table):
+        batch, max_pages_per_seq = block_table.shape
         self.cfg = cfg
         self.batch = batch
         self.max_pages = max_pages_per_seq
-        self.n_pages = n_pages if n_pages is not None else batch * max_pages_per_seq
         self.page_bytes = B.kvq_page_bytes(cfg)
-        dev = torch.device(device)
-        self.pages = torch.zeros(self.n_pages * self.page_bytes, dtype=torch.uint8, device=dev)
-        if block_table is None:
-            block_table = torch.arange(batch * max_pages_per_seq, dtype=torch.int32).reshape(batch, -1)
-        self.block_table = torch.as_tensor(block_table, dtype=torch.int32).reshape(batch, max_pages_per_seq).to(dev)
-        self.seq_lens = torch.zeros(batch, dtype=torch.int32, device=dev)
-        R, H, D = cfg.residual, cfg.num_kv_heads, cfg.head_dim
-        dt = src_torch_dtype(cfg)
-        self.k_win = torch.zeros(batch, max(R, 1), H, D, dtype=dt, device=dev) if R else None
-        self.v_win = torch.zeros(batch, max(R, 1), H, D, dtype=dt, device=dev) if R else None
+        self.n_pages = pages.numel() // self.page_bytes
+        self.pages, self.block_table, self.seq_lens, self.k_win, self.v_win = pages, block_table, seq_lens, k_win, v_win
+        dev, H = pages.device, cfg.num_kv_heads
         self.k_scale = torch.zeros(H, dtype=torch.float32, device=dev)
         self.v_scale = torch.zeros(H, dtype=torch.float32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.workspace = torch.empty(
             max(B.kvq_workspace_bytes(cfg, batch, max_pages_per_seq * cfg.page_size), 256),
             dtype=torch.uint8, device=dev)
+        self._outgrown = []
         self.rope_table, self.rope_positions = None, 0
         if cfg.rope_pre and rope_table is not False:
             if rope_table is True:
@@ -78,6 +118,68 @@ class PagedKVCache:
         if out is None:
             out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
         B.kvq_decode_attention(self.cfg, self.c, q, out, softmax_scale, self.workspace, stream)
+        return out
+
+    def _beside(self, name, t):
+        """The library launches on the current device, over the cache's memory."""
+        if t.device != self.pages.device or (t.is_cuda and t.device.index != torch.cuda.current_device()):
+            raise ValueError(f"{name} must be on the cache's device ({self.pages.device}), which must be the current one")
+
+    def _counts(self, name, t):
+        self._beside(name, t)
+        if tuple(t.shape) != (self.batch,) or t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous int32 of shape {(self.batch,)}")
+
+    def append_rope(self, rope, q, k_new, v_new, n_new_per_seq=None, q_out=None, stream=None):
+        """append() with the position rotation on the way: k_new, v_new [batch, n_new, Hkv, D] and q
+        [batch, n_new, Hq, D] (or None) may be slices of one fused projection (rows of one token contiguous,
+        tokens evenly spaced).  Returns the rotated queries."""
+        n = k_new.shape[1]
+        strides = []
+        for name, t, heads in (("q", q, self.cfg.num_q_heads), ("k_new", k_new, self.cfg.num_kv_heads),
+                               ("v_new", v_new, self.cfg.num_kv_heads)):
+            if t is None and name == "q":
+                strides.append(0)
+                continue
+            D = self.cfg.head_dim
+            if tuple(t.shape) != (self.batch, n, heads, D) or t.dtype != src_torch_dtype(self.cfg):
+                raise ValueError(f"{name} must be {src_torch_dtype(self.cfg)} of shape {(self.batch, n, heads, D)}")
+            self._beside(name, t)
+            row = t.stride(1) if n > 1 else t.stride(0) if self.batch > 1 else heads * D
+            if (D > 1 and t.stride(3) != 1) or (heads > 1 and t.stride(2) != D) or (
+                    self.batch > 1 and n > 1 and t.stride(0) != n * row):
+                raise ValueError(f"{name}: a token's row must be contiguous and the tokens evenly spaced")
+            strides.append(row)
+        if n_new_per_seq is not None:
+            self._counts("n_new_per_seq", n_new_per_seq)
+        if q is not None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+            if q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
+                raise ValueError("q_out must be contiguous, of q's shape and dtype")
+        B.kvq_rope_append(self.cfg, self.c, rope, q, k_new, v_new, n, n_new_per_seq, q_out, *strides, stream=stream)
+        return q_out
+
+    def query_attention(self, q, causal=True, n_q_per_seq=None, out=None, softmax_scale=0.0, stream=None):
+        """Attention of n_q queries per sequence, q [batch, n_q, Hq, D]: the sequence's newest n_q tokens over its
+        own cache (causal), or a decoder's tokens over an encoder's states (causal=False).  The workspace grows
+        with n_q on first use and is kept; calls on several streams at once need a cache object each."""
+        n = q.shape[1]
+        shape = (self.batch, n, self.cfg.num_q_heads, self.cfg.head_dim)
+        if tuple(q.shape) != shape or q.dtype != src_torch_dtype(self.cfg) or not q.is_contiguous():
+            raise ValueError(f"q must be contiguous {src_torch_dtype(self.cfg)} of shape {shape}")
+        self._beside("q", q)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+            raise ValueError("out must be contiguous, of q's shape and dtype")
+        if n_q_per_seq is not None:
+            self._counts("n_q_per_seq", n_q_per_seq)
+        need = B.kvq_query_workspace_bytes(self.cfg, self.batch, max(n, 1))
+        if self.workspace.numel() < need:
+            self._outgrown.append(self.workspace)  # a captured graph may still use it
+            self.workspace = torch.empty(need, dtype=torch.uint8, device=self.pages.device)
+        B.kvq_query_attention(self.cfg, self.c, q, n, n_q_per_seq, B.KVQ_MASK_CAUSAL if causal else B.KVQ_MASK_NONE,
+                              out, softmax_scale, self.workspace, stream)
         return out
 
     def decode_kernel(self) -> int:

@@ -25,8 +25,14 @@ int n_meta(const kvq_qspec& s) {
 kvq_status check_spec(const kvq_qspec& s, int D, bool is_key) {
   if (!fmt_ok(s.fmt)) return KVQ_ERR_INVALID_ARG;
   if (s.mode != KVQ_SYM_ABSMAX && s.mode != KVQ_ASYM_MINMAX) return KVQ_ERR_INVALID_ARG;
-  if (s.axis != KVQ_PER_TENSOR && s.axis != KVQ_PER_TOKEN && s.axis != KVQ_PER_CHANNEL)
+  if (s.axis != KVQ_PER_TENSOR && s.axis != KVQ_PER_TOKEN && s.axis != KVQ_PER_CHANNEL &&
+      s.axis != KVQ_PER_BLOCK)
     return KVQ_ERR_INVALID_ARG;
+  if (s.axis == KVQ_PER_BLOCK) {
+    if (bits_of(s.fmt) != 8) return KVQ_ERR_UNSUPPORTED;
+    if (!fmt_is_fp8(s.fmt) && s.mode != KVQ_SYM_ABSMAX) return KVQ_ERR_UNSUPPORTED;
+    return s.group < 16 || s.group % 16 ? KVQ_ERR_INVALID_ARG : KVQ_OK;
+  }
   if (fmt_is_fp8(s.fmt)) return s.axis == KVQ_PER_TENSOR ? KVQ_OK : KVQ_ERR_UNSUPPORTED;
   if (s.axis == KVQ_PER_TENSOR) return s.mode == KVQ_SYM_ABSMAX ? KVQ_OK : KVQ_ERR_UNSUPPORTED;
   if (s.axis == KVQ_PER_CHANNEL) {
@@ -54,6 +60,9 @@ bool layout_of(const kvq_config* c, Layout* L) {
   L->vm = align16(L->vc + P * L->vrow);
   size_t vm_bytes = 0;
   if (c->v.axis == KVQ_PER_TOKEN) vm_bytes = P * (D / tok_group(c->v, D)) * n_meta(c->v) * mb;
+  const bool block = c->k.axis == KVQ_PER_BLOCK;  // keys and values alike (kvq_validate)
+  const size_t nb = block && P >= (size_t)c->k.group ? P / c->k.group : 1;  // block scales a page holds
+  if (block) vm_bytes = nb * mb;
   L->km = align16(L->vm + vm_bytes);
   size_t km_bytes = 0;
   if (c->k.axis == KVQ_PER_CHANNEL) {
@@ -61,8 +70,13 @@ bool layout_of(const kvq_config* c, Layout* L) {
     km_bytes = (P >= G ? P / G : 1) * D * n_meta(c->k) * mb;
   } else if (c->k.axis == KVQ_PER_TOKEN) {
     km_bytes = P * (D / tok_group(c->k, D)) * n_meta(c->k) * mb;
+  } else if (block) {
+    km_bytes = nb * mb;
   }
   L->head = align16(L->km + km_bytes);
+  // PER_BLOCK: every head block starts on a 128-byte row of the pool, so that its codes are whole
+  // rows of one 2-D tensor map
+  if (block) L->head = (L->head + 127) & ~size_t(127);
   L->page = L->head * c->num_kv_heads;
   return true;
 }
@@ -75,6 +89,9 @@ kvq_status check_cache(const kvq_config* c, const kvq_cache* k) {
   if ((c->k.axis == KVQ_PER_TENSOR) && !k->k_scale) return KVQ_ERR_INVALID_ARG;
   if ((c->v.axis == KVQ_PER_TENSOR) && !k->v_scale) return KVQ_ERR_INVALID_ARG;
   if ((long long)k->max_pages_per_seq * c->page_size > (1LL << 30)) return KVQ_ERR_CAPACITY;
+  if (c->k.axis == KVQ_PER_BLOCK &&
+      ((reinterpret_cast<uintptr_t>(k->k_win) | reinterpret_cast<uintptr_t>(k->v_win)) & 15))
+    return KVQ_ERR_INVALID_ARG;
   if (k->rope_table) {
     if (!c->rope_pre || k->rope_positions < 1 || (reinterpret_cast<uintptr_t>(k->rope_table) & 15))
       return KVQ_ERR_INVALID_ARG;
@@ -97,12 +114,13 @@ bool make_view(const kvq_config* c, const kvq_cache* k, KvqView* v) {
   v->kfmt = c->k.fmt;
   v->kmode = fmt_is_fp8(c->k.fmt) ? KVQ_SYM_ABSMAX : c->k.mode;
   v->kaxis = c->k.axis;
-  v->kgroup = c->k.axis == KVQ_PER_CHANNEL ? c->k.group
+  v->kgroup = c->k.axis == KVQ_PER_CHANNEL || c->k.axis == KVQ_PER_BLOCK ? c->k.group
               : c->k.axis == KVQ_PER_TOKEN ? tok_group(c->k, c->head_dim) : 0;
   v->vfmt = c->v.fmt;
   v->vmode = fmt_is_fp8(c->v.fmt) ? KVQ_SYM_ABSMAX : c->v.mode;
   v->vaxis = c->v.axis;
-  v->vgroup = c->v.axis == KVQ_PER_TOKEN ? tok_group(c->v, c->head_dim) : 0;
+  v->vgroup = c->v.axis == KVQ_PER_TOKEN ? tok_group(c->v, c->head_dim)
+              : c->v.axis == KVQ_PER_BLOCK ? c->v.group : 0;
   v->kbits = bits_of(c->k.fmt);
   v->vbits = bits_of(c->v.fmt);
   v->R = c->residual;
@@ -173,7 +191,9 @@ kvq_status kvq_validate(const kvq_config* c) {
   s = check_spec(c->v, c->head_dim, false);
   if (s != KVQ_OK) return s;
   if (c->residual < 0 || c->page_size < 16 || c->page_size % 16) return KVQ_ERR_INVALID_ARG;
-  if (c->k.axis == KVQ_PER_CHANNEL) {
+  if ((c->k.axis == KVQ_PER_BLOCK) != (c->v.axis == KVQ_PER_BLOCK)) return KVQ_ERR_UNSUPPORTED;
+  if (c->k.axis == KVQ_PER_BLOCK && c->k.group != c->v.group) return KVQ_ERR_UNSUPPORTED;
+  if (c->k.axis == KVQ_PER_CHANNEL || c->k.axis == KVQ_PER_BLOCK) {
     const int G = c->k.group;
     if (c->residual == 0 || c->residual % G) return KVQ_ERR_INVALID_ARG;
     if (c->page_size % G && G % c->page_size) return KVQ_ERR_INVALID_ARG;
@@ -234,7 +254,88 @@ kvq_status kvq_quantize_append(const kvq_config* c, const kvq_cache* cache, cons
   if ((long long)n_new > (long long)cache->max_pages_per_seq * c->page_size) return KVQ_ERR_CAPACITY;
   if (n_new == 0) return KVQ_OK;
   if (!k_new || !v_new) return KVQ_ERR_INVALID_ARG;
+  if (c->k.axis == KVQ_PER_BLOCK) {
+    if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15) return KVQ_ERR_INVALID_ARG;
+    const long long row = (long long)v.Hkv * v.D;
+    return kvq::launch_block_append(v, kvq::RopeView{}, nullptr, k_new, v_new, 0, row, row, n_new, n_new_per_seq,
+                                    nullptr, (cudaStream_t)stream);
+  }
   return kvq::launch_append(v, k_new, v_new, n_new, n_new_per_seq, (cudaStream_t)stream);
+}
+
+kvq_status kvq_rope_append(const kvq_config* c, const kvq_cache* cache, const kvq_rope* rope, const void* q,
+                           const void* k_new, const void* v_new, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, int32_t n_new, const int32_t* n_new_per_seq, void* q_out,
+                           void* stream) {
+  const kvq::NvtxRange range("kvq_rope_append");
+  kvq::KvqView v;
+  if (!kvq::make_view(c, cache, &v)) return kvq_validate(c);
+  kvq_status s = check_cache(c, cache);
+  if (s != KVQ_OK) return s;
+  if (!rope || !rope->cos_sin || (reinterpret_cast<uintptr_t>(rope->cos_sin) & 15) || rope->positions < 1 ||
+      rope->rot_dim < 16 || rope->rot_dim % 16 || rope->rot_dim > c->head_dim ||
+      (rope->pairing != KVQ_ROPE_INTERLEAVED && rope->pairing != KVQ_ROPE_HALVES))
+    return KVQ_ERR_INVALID_ARG;
+  if (n_new < 0) return KVQ_ERR_INVALID_ARG;
+  if ((long long)n_new > (long long)cache->max_pages_per_seq * c->page_size) return KVQ_ERR_CAPACITY;
+  const long long qrow = (long long)v.Hq * v.D, kvrow = (long long)v.Hkv * v.D;
+  const int esz = v.src_bf16 ? 2 : 4;
+  const int64_t strides[3] = {q_stride, k_stride, v_stride};
+  const long long rows[3] = {qrow, kvrow, kvrow};
+  for (int i = 0; i < 3; ++i)
+    if (strides[i] != 0 && (strides[i] < rows[i] || strides[i] > (1LL << 40) || strides[i] * esz % 16))
+      return KVQ_ERR_INVALID_ARG;
+  if (n_new == 0) return KVQ_OK;
+  if (!k_new || !v_new || (q && !q_out)) return KVQ_ERR_INVALID_ARG;
+  const uintptr_t al = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_new) |
+                       reinterpret_cast<uintptr_t>(v_new) | (q ? reinterpret_cast<uintptr_t>(q_out) : 0);
+  if (al & 15) return KVQ_ERR_INVALID_ARG;
+  const long long qs = q_stride ? q_stride : qrow, ks = k_stride ? k_stride : kvrow, vs = v_stride ? v_stride : kvrow;
+  if (q && q == q_out && qs != qrow) return KVQ_ERR_INVALID_ARG;
+  kvq::RopeView r;
+  r.cs = rope->cos_sin;
+  r.positions = rope->positions;
+  r.rot = rope->rot_dim;
+  r.halves = rope->pairing == KVQ_ROPE_HALVES;
+  if (c->k.axis == KVQ_PER_BLOCK)
+    return kvq::launch_block_append(v, r, q, k_new, v_new, qs, ks, vs, n_new, n_new_per_seq, q_out,
+                                    (cudaStream_t)stream);
+  return kvq::launch_rope_append(v, r, q, k_new, v_new, qs, ks, vs, n_new, n_new_per_seq, q_out,
+                                 (cudaStream_t)stream);
+}
+
+size_t kvq_query_workspace_bytes(const kvq_config* c, int32_t batch, int32_t n_q) {
+  kvq::KvqView v;
+  if (batch < 1 || n_q < 1 || !kvq::make_view(c, nullptr, &v)) return 0;
+  return kvq::query_workspace_bytes(v, batch, n_q);
+}
+
+kvq_status kvq_query_attention(const kvq_config* c, const kvq_cache* cache, const void* q, int32_t n_q,
+                               const int32_t* n_q_per_seq, int32_t mask, void* out, float softmax_scale,
+                               void* workspace, size_t ws_bytes, void* stream) {
+  const kvq::NvtxRange range("kvq_query_attention");
+  kvq::KvqView v;
+  if (!kvq::make_view(c, cache, &v)) return kvq_validate(c);
+  kvq_status s = check_cache(c, cache);
+  if (s != KVQ_OK) return s;
+  if (n_q < 0 || (mask != KVQ_MASK_NONE && mask != KVQ_MASK_CAUSAL) || !(softmax_scale >= 0.f) ||
+      !isfinite(softmax_scale))
+    return KVQ_ERR_INVALID_ARG;
+  if (n_q > (1 << 24)) return KVQ_ERR_CAPACITY;
+  if (n_q == 0) return KVQ_OK;
+  if (!q || !out || ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15))
+    return KVQ_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return KVQ_ERR_WORKSPACE;
+  if (ws_bytes < kvq::query_workspace_bytes(v, cache->batch, n_q)) return KVQ_ERR_WORKSPACE;
+  kvq::QueryArgs a;
+  a.q = q;
+  a.out = out;
+  a.n_q = n_q;
+  a.n_per_seq = n_q_per_seq;
+  a.causal = mask == KVQ_MASK_CAUSAL;
+  a.out_f32 = !v.src_bf16;
+  a.scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)c->head_dim);
+  return kvq::launch_query(v, a, workspace, (cudaStream_t)stream);
 }
 
 kvq_status kvq_decode_attention(const kvq_config* c, const kvq_cache* cache, const void* q,

@@ -13,8 +13,10 @@
 // quantizes every window that fills (reading the old window and the new rows);
 // then one CTA per sequence writes the remaining new tokens into the window and
 // advances seq_lens, so window slots are never read and overwritten out of order.
+#include "kvq_dequant.cuh"
 #include "kvq_host.h"
 #include "kvq_internal.cuh"
+#include "kvq_rope.cuh"
 
 namespace kvq {
 namespace {
@@ -42,15 +44,38 @@ struct AppendCtx {
   int b, h, T0, wbase, n_stride, st_t0;
 };
 
+// The new rows of a call.  kvq_quantize_append: dense, unrotated (an empty struct, so its kernels
+// are the same code as before the rotation existed); kvq_rope_append: rows k_tok / v_tok elements
+// apart, keys rotated on their way in unless the cache holds pre-RoPE keys.
+template <bool kRope>
+struct Fresh {
+  __device__ __forceinline__ long long tok(const KvqView& v, bool) const { return (long long)v.Hkv * v.D; }
+  __device__ __forceinline__ bool fits(long long) const { return true; }
+};
+template <>
+struct Fresh<true> {
+  RopeView r;
+  long long k_tok, v_tok;
+  int rotate_keys;
+  __device__ __forceinline__ long long tok(const KvqView&, bool key) const { return key ? k_tok : v_tok; }
+  __device__ __forceinline__ bool fits(long long end) const { return end <= r.positions; }
+};
+
+template <bool kRope>
 __device__ __forceinline__ float src_value(const KvqView& v, const Src& s, const AppendCtx& a,
-                                           int t, int c) {
+                                           const Fresh<kRope>& f, bool key, int t, int c) {
   if (s.staged) return load_src(s.staged, (long long)(t - a.st_t0) * v.D + c, v.src_bf16);
   if (t < a.T0) {
     const long long i = (((long long)a.b * v.R + (t - a.wbase)) * v.Hkv + a.h) * v.D + c;
     return load_src(s.win, i, v.src_bf16);
   }
-  const long long i = (((long long)a.b * a.n_stride + (t - a.T0)) * v.Hkv + a.h) * v.D + c;
-  return load_src(s.fresh, i, v.src_bf16);
+  const long long i = ((long long)a.b * a.n_stride + (t - a.T0)) * f.tok(v, key) + (long long)a.h * v.D;
+  const float x = load_src(s.fresh, i + c, v.src_bf16);
+  if constexpr (kRope) {
+    if (key && f.rotate_keys && c < f.r.rot)
+      return rope_channel(f.r, t, c, x, load_src(s.fresh, i + rope_partner(f.r, c), v.src_bf16), v.src_bf16);
+  }
+  return x;
 }
 
 struct Smem {
@@ -103,15 +128,16 @@ __device__ void clear_stage(Smem& sm, const TQ& q, int n) {
 
 // Tokens [t_begin, t_begin + count) of one tensor, quantized along a per-token,
 // per-tensor or FP8 axis.  D and the group sizes are powers of two.
-__device__ void quantize_rows(const KvqView& v, const Src& s, const AppendCtx& a, const TQ& q,
-                              Smem& sm, int t_begin, int count) {
+template <bool kRope>
+__device__ void quantize_rows(const KvqView& v, const Src& s, const AppendCtx& a, const Fresh<kRope>& f, bool key,
+                              const TQ& q, Smem& sm, int t_begin, int count) {
   const int D = v.D, lD = log2i(D);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int sub = 0; sub < count; sub += kSub) {
     const int n = min(kSub, count - sub);
     const int t0 = t_begin + sub;
     for (int e = threadIdx.x; e < (n << lD); e += kThreads)
-      sm.xs[e >> lD][e & (D - 1)] = src_value(v, s, a, t0 + (e >> lD), e & (D - 1));
+      sm.xs[e >> lD][e & (D - 1)] = src_value(v, s, a, f, key, t0 + (e >> lD), e & (D - 1));
     clear_stage(sm, q, n);
     load_rows(v, a, sm, t0, n);
     __syncthreads();
@@ -181,15 +207,16 @@ __device__ void quantize_rows(const KvqView& v, const Src& s, const AppendCtx& a
 
 // Keys of tokens [t_begin, t_begin + count), count a multiple of G, quantized per
 // channel over groups of G tokens aligned to multiples of G.
+template <bool kRope>
 __device__ void quantize_key_channels(const KvqView& v, const Src& s, const AppendCtx& a,
-                                      const TQ& q, Smem& sm, int t_begin, int count) {
+                                      const Fresh<kRope>& f, const TQ& q, Smem& sm, int t_begin, int count) {
   const int D = v.D, G = q.group, lD = log2i(D);
   const int lanes = kThreads >> lD;
   const int c = threadIdx.x & (D - 1), lane = threadIdx.x >> lD;
   for (int g0 = t_begin; g0 < t_begin + count; g0 += G) {
     float mn = INFINITY, mx = -INFINITY;
     for (int t = g0 + lane; t < g0 + G; t += lanes) {
-      const float x = src_value(v, s, a, t, c);
+      const float x = src_value(v, s, a, f, true, t, c);
       mn = fminf(mn, x);
       mx = fmaxf(mx, x);
     }
@@ -223,7 +250,7 @@ __device__ void quantize_key_channels(const KvqView& v, const Src& s, const Appe
       __syncthreads();
       for (int e = threadIdx.x; e < (n << lD); e += kThreads) {
         const int r = e >> lD, cc = e & (D - 1);
-        const float x = src_value(v, s, a, t0 + r, cc);
+        const float x = src_value(v, s, a, f, true, t0 + r, cc);
         const int code = q.mode == KVQ_ASYM_MINMAX
                              ? asym_code_r(x, sm.ch_m[cc], sm.ch_s[cc], sm.ch_r[cc], q.bits)
                              : sym_code_r(x, sm.ch_s[cc], sm.ch_r[cc], q.bits);
@@ -252,15 +279,16 @@ __device__ TQ value_q(const KvqView& v) {
   return q;
 }
 
+template <bool kRope>
 __device__ void quantize_block(const KvqView& v, const Src& ks, const Src& vs, const AppendCtx& a,
-                               Smem& sm, int t_begin, int count) {
+                               const Fresh<kRope>& f, Smem& sm, int t_begin, int count) {
   const TQ kq = key_q(v), vq = value_q(v);
   if (kq.axis == KVQ_PER_CHANNEL) {
-    quantize_key_channels(v, ks, a, kq, sm, t_begin, count);
+    quantize_key_channels(v, ks, a, f, kq, sm, t_begin, count);
   } else {
-    quantize_rows(v, ks, a, kq, sm, t_begin, count);
+    quantize_rows(v, ks, a, f, true, kq, sm, t_begin, count);
   }
-  quantize_rows(v, vs, a, vq, sm, t_begin, count);
+  quantize_rows(v, vs, a, f, false, vq, sm, t_begin, count);
 }
 
 // 16-byte global -> shared copy that completes asynchronously (cp.async, sm_80+);
@@ -276,8 +304,9 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 // rows.  `between` runs while the copies are in flight, so the global reads it
 // makes overlap theirs.  The loop stays rolled: a launch runs this code once, so
 // its size, not its instruction count, sets its cost.
-template <typename Between>
-__device__ void stage_block(const KvqView& v, const AppendCtx& a, const void* k_new, const void* v_new,
+template <bool kRope, typename Between>
+__device__ void stage_block(const KvqView& v, const AppendCtx& a, const Fresh<kRope>& f, const void* k_new,
+                            const void* v_new,
                             int t_begin, int count, unsigned char* dst, Between&& between) {
   const int row = v.D * (v.src_bf16 ? 2 : 4);
   const int lp = log2i(row >> 4);  // 16-byte pieces per row: 2^lp
@@ -294,14 +323,29 @@ __device__ void stage_block(const KvqView& v, const AppendCtx& a, const void* k_
       const long long i = (((long long)a.b * v.R + (t - a.wbase)) * v.Hkv + a.h) * row;
       src = static_cast<const unsigned char*>(tensor ? v.v_win : v.k_win) + i;
     } else {
-      const long long i = (((long long)a.b * a.n_stride + (t - a.T0)) * v.Hkv + a.h) * row;
-      src = static_cast<const unsigned char*>(tensor ? v_new : k_new) + i;
+      const long long i = ((long long)a.b * a.n_stride + (t - a.T0)) * f.tok(v, !tensor) + (long long)a.h * v.D;
+      src = static_cast<const unsigned char*>(tensor ? v_new : k_new) + i * (v.src_bf16 ? 2 : 4);
     }
     cp_async16(dst + 16 * e, src + 16 * k);  // piece e of the block sits at byte 16 e
   }
   between();
   cp_async_wait_all();
   __syncthreads();
+  if constexpr (kRope) {
+    if (f.rotate_keys) {  // the new rows' pairs, in place: a thread owns both channels of a pair
+      const int half = f.r.rot / 2, first = max(t_begin, a.T0);
+#pragma unroll 1
+      for (int e = threadIdx.x; e < (t_begin + count - first) * half; e += kThreads) {
+        const int t = first + e / half, i = e % half;
+        const int c = f.r.halves ? i : 2 * i, p = rope_partner(f.r, c);
+        const long long o = (long long)(t - t_begin) * v.D;
+        const float x = load_src(dst, o + c, v.src_bf16), y = load_src(dst, o + p, v.src_bf16);
+        store_src(dst, o + c, rope_channel(f.r, t, c, x, y, v.src_bf16), v.src_bf16);
+        store_src(dst, o + p, rope_channel(f.r, t, p, y, x, v.src_bf16), v.src_bf16);
+      }
+      __syncthreads();
+    }
+  }
 }
 
 // ---- parallel fold of one R-token block of one kv-head (R <= kMaxFold)
@@ -587,11 +631,11 @@ __device__ __forceinline__ void fold_key_channels_t(const KvqView& v, const TQ& 
 }
 
 // Stage the block, look up its pages meanwhile, then fold keys and values.
-template <bool BF16>
-__device__ __forceinline__ void fold_block(const KvqView& v, const AppendCtx& a, const void* k_new,
+template <bool BF16, bool kRope>
+__device__ __forceinline__ void fold_block(const KvqView& v, const AppendCtx& a, const Fresh<kRope>& f, const void* k_new,
                                            const void* v_new, int tb, unsigned char* staged, FoldSmem& fs) {
   const int R = v.R;
-  stage_block(v, a, k_new, v_new, tb, R, staged, [&] {
+  stage_block(v, a, f, k_new, v_new, tb, R, staged, [&] {
     if (threadIdx.x < R) {
       const int t = tb + threadIdx.x;
       uint8_t* page = page_of(v, a.b, t);
@@ -617,9 +661,11 @@ __device__ __forceinline__ void fold_block(const KvqView& v, const AppendCtx& a,
     fold_rows<BF16>(v, tensor ? vq : kq, staged + tensor * R * row, fs, R);
 }
 
+template <bool kRope>
 __global__ void __launch_bounds__(kThreads) append_kernel(KvqView v, const void* k_new,
                                                            const void* v_new, int n_stride,
-                                                           const int32_t* n_per_seq, int stage_ok) {
+                                                           const int32_t* n_per_seq, int stage_ok,
+                                                           Fresh<kRope> f) {
   __shared__ Smem sm;
   extern __shared__ __align__(16) unsigned char staged[];
   const int unit = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
@@ -627,7 +673,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvqView v, const void*
   const int n = n_per_seq ? n_per_seq[b] : n_stride;
   if (n <= 0) return;
   const long long cap = (long long)v.max_pages * v.P;
-  if (T0 < 0 || n > n_stride || (long long)T0 + n > cap) {
+  if (T0 < 0 || n > n_stride || (long long)T0 + n > cap || !f.fits((long long)T0 + n)) {
     if (unit == 0 && h == 0 && threadIdx.x == 0) atomicOr(v.status, KVQ_DEV_OVERFLOW);
     return;
   }
@@ -650,38 +696,41 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvqView v, const void*
         if (v.R <= kMaxFold) {
           __shared__ FoldSmem fs;
           if (v.src_bf16) {
-            fold_block<true>(v, a, k_new, v_new, tb, staged, fs);
+            fold_block<true>(v, a, f, k_new, v_new, tb, staged, fs);
           } else {
-            fold_block<false>(v, a, k_new, v_new, tb, staged, fs);
+            fold_block<false>(v, a, f, k_new, v_new, tb, staged, fs);
           }
         } else {
-          stage_block(v, a, k_new, v_new, tb, v.R, staged, [] {});
+          stage_block(v, a, f, k_new, v_new, tb, v.R, staged, [] {});
           a.st_t0 = tb;
           const int row = v.D * (v.src_bf16 ? 2 : 4);
           const Src kss{v.k_win, k_new, staged}, vss{v.v_win, v_new, staged + (long long)v.R * row};
-          quantize_block(v, kss, vss, a, sm, tb, v.R);
+          quantize_block(v, kss, vss, a, f, sm, tb, v.R);
         }
       } else {
-        quantize_block(v, ks, vs, a, sm, tb, v.R);
+        quantize_block(v, ks, vs, a, f, sm, tb, v.R);
       }
     }
   } else {
     a.wbase = 0;
     const int t_lo = T0 + unit * kUnitTok;
-    if (t_lo < T1) quantize_block(v, ks, vs, a, sm, t_lo, min(kUnitTok, T1 - t_lo));
+    if (t_lo < T1) quantize_block(v, ks, vs, a, f, sm, t_lo, min(kUnitTok, T1 - t_lo));
   }
 }
 
 // After the folds: write each sequence's remaining new tokens into its window
 // (slots from the last fold boundary) and advance seq_lens.  One CTA per
 // sequence, so the CTA that updates seq_lens[b] is the only one that reads it.
+template <bool kRope>
 __global__ void __launch_bounds__(kThreads) window_lengths_kernel(KvqView v, const void* k_new,
                                                                    const void* v_new, int n_stride,
-                                                                   const int32_t* n_per_seq) {
+                                                                   const int32_t* n_per_seq, Fresh<kRope> f) {
   const int b = blockIdx.x;
   const int T0 = v.seq_lens[b];
   const int n = n_per_seq ? n_per_seq[b] : n_stride;
-  if (n <= 0 || T0 < 0 || n > n_stride || (long long)T0 + n > (long long)v.max_pages * v.P) return;
+  if (n <= 0 || T0 < 0 || n > n_stride || (long long)T0 + n > (long long)v.max_pages * v.P ||
+      !f.fits((long long)T0 + n))
+    return;
   const int T1 = T0 + n;
   if (v.R > 0) {
     const int base = (T1 / v.R) * v.R;
@@ -690,7 +739,7 @@ __global__ void __launch_bounds__(kThreads) window_lengths_kernel(KvqView v, con
     const int esz = v.src_bf16 ? 2 : 4;
     const uintptr_t al = reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new) |
                          reinterpret_cast<uintptr_t>(v.k_win) | reinterpret_cast<uintptr_t>(v.v_win);
-    if ((al & 15) == 0 && (row * esz) % 16 == 0) {
+    if (!kRope && (al & 15) == 0 && (row * esz) % 16 == 0) {
       // 16-byte chunks: a token's row of all heads is contiguous in both tensors
       const int cpr = row * esz / 16;
       for (int e = threadIdx.x; e < (T1 - t_lo) * cpr; e += kThreads) {
@@ -705,10 +754,17 @@ __global__ void __launch_bounds__(kThreads) window_lengths_kernel(KvqView v, con
     } else {
       for (int e = threadIdx.x; e < (T1 - t_lo) * row; e += kThreads) {
         const int t = t_lo + e / row, c = e % row;
-        const long long si = ((long long)b * n_stride + (t - T0)) * row + c;
+        const long long si = ((long long)b * n_stride + (t - T0)) * f.tok(v, true) + c;
+        const long long vi = ((long long)b * n_stride + (t - T0)) * f.tok(v, false) + c;
         const long long di = ((long long)b * v.R + (t - base)) * row + c;
-        store_src(v.k_win, di, load_src(k_new, si, v.src_bf16), v.src_bf16);
-        store_src(v.v_win, di, load_src(v_new, si, v.src_bf16), v.src_bf16);
+        float x = load_src(k_new, si, v.src_bf16);
+        if constexpr (kRope) {
+          const int ch = c % v.D;
+          if (f.rotate_keys && ch < f.r.rot)
+            x = rope_channel(f.r, t, ch, x, load_src(k_new, si - ch + rope_partner(f.r, ch), v.src_bf16), v.src_bf16);
+        }
+        store_src(v.k_win, di, x, v.src_bf16);
+        store_src(v.v_win, di, load_src(v_new, vi, v.src_bf16), v.src_bf16);
       }
     }
   }
@@ -724,58 +780,9 @@ __global__ void dequantize_kernel(KvqView v, int seq, int t0, float* k_out, floa
   const int nq = n_quantized(T, v.R);
   for (int c = threadIdx.x; c < v.D; c += blockDim.x) {
     const long long o = ((long long)blockIdx.x * v.Hkv + h) * v.D + c;
-    float kx = 0.f, vx = 0.f;
-    if (t < T && t >= nq) {
-      const long long wi = (((long long)seq * v.R + (t - nq)) * v.Hkv + h) * v.D + c;
-      kx = load_src(v.k_win, wi, v.src_bf16);
-      vx = load_src(v.v_win, wi, v.src_bf16);
-    } else if (t < T) {
-      const uint8_t* page = page_of(v, seq, t);
-      if (page) {
-        const uint8_t* hb = page + (long long)h * v.head_bytes;
-        const int slot = t % v.P;
-        const unsigned ku = get_code(hb + slot * v.krow, c, v.kbits);
-        if (is_fp8(v.kfmt)) {
-          kx = __fmul_rn(fp8_to_float(ku, v.kfmt), v.k_scale[h]);
-        } else if (v.kaxis == KVQ_PER_TENSOR) {
-          kx = dequant_sym(signed_code(ku, v.kbits, KVQ_SYM_ABSMAX), v.k_scale[h]);
-        } else {
-          const uint8_t* meta;
-          float s, mn = 0.f;
-          if (v.kaxis == KVQ_PER_TOKEN) {
-            meta = hb + v.off_km + slot * v.k_ng * v.k_nmeta * v.mb;
-            const int grp = c / v.kgroup;
-            s = load_meta(meta, grp, v.meta16);
-            if (v.k_nmeta == 2) mn = load_meta(meta, v.k_ng + grp, v.meta16);
-          } else {
-            const int g0 = (t / v.kgroup) * v.kgroup;
-            const uint8_t* gp = page_of(v, seq, g0);
-            meta = gp ? gp + (long long)h * v.head_bytes + v.off_km +
-                            (long long)((g0 % v.P) / v.kgroup) * v.D * v.k_nmeta * v.mb
-                      : nullptr;
-            s = meta ? load_meta(meta, c, v.meta16) : 0.f;
-            if (meta && v.k_nmeta == 2) mn = load_meta(meta, v.D + c, v.meta16);
-          }
-          const int code = signed_code(ku, v.kbits, v.kmode);
-          kx = v.kmode == KVQ_ASYM_MINMAX ? dequant_asym(code, s, mn) : dequant_sym(code, s);
-        }
-        const unsigned vu = get_code(hb + v.off_vc + slot * v.vrow, c, v.vbits);
-        if (is_fp8(v.vfmt)) {
-          vx = __fmul_rn(fp8_to_float(vu, v.vfmt), v.v_scale[h]);
-        } else if (v.vaxis == KVQ_PER_TENSOR) {
-          vx = dequant_sym(signed_code(vu, v.vbits, KVQ_SYM_ABSMAX), v.v_scale[h]);
-        } else {
-          const uint8_t* meta = hb + v.off_vm + slot * v.v_ng * v.v_nmeta * v.mb;
-          const int grp = c / v.vgroup;
-          const int code = signed_code(vu, v.vbits, v.vmode);
-          const float vs = load_meta(meta, grp, v.meta16);
-          vx = v.vmode == KVQ_ASYM_MINMAX ? dequant_asym(code, vs, load_meta(meta, v.v_ng + grp, v.meta16))
-                                          : dequant_sym(code, vs);
-        }
-      }
-    }
-    k_out[o] = kx;
-    v_out[o] = vx;
+    bool ok = true;
+    k_out[o] = t < T ? cache_key(v, seq, h, t, c, nq, &ok) : 0.f;
+    v_out[o] = t < T ? cache_value(v, seq, h, t, c, nq) : 0.f;
   }
 }
 
@@ -809,8 +816,11 @@ __global__ void scale_finalize_kernel(float* scale, int Hkv, float qmax) {
 
 }  // namespace
 
-kvq_status launch_append(const KvqView& v, const void* k_new, const void* v_new, int n_new,
-                         const int32_t* n_new_per_seq, cudaStream_t st) {
+namespace {
+
+template <bool kRope>
+kvq_status launch_append_t(const KvqView& v, const void* k_new, const void* v_new, int n_new,
+                           const int32_t* n_new_per_seq, const Fresh<kRope>& f, cudaStream_t st) {
   const int units = v.R > 0 ? n_new / v.R + 1 : (n_new + kUnitTok - 1) / kUnitTok;
   dim3 grid(units, v.Hkv, v.batch);
   const size_t stage_bytes = v.R > 0 ? 2ull * v.R * v.D * (v.src_bf16 ? 2 : 4) : 0;
@@ -818,13 +828,35 @@ kvq_status launch_append(const KvqView& v, const void* k_new, const void* v_new,
                                reinterpret_cast<uintptr_t>(v.k_win) | reinterpret_cast<uintptr_t>(v.v_win);
   const int stage_ok = stage_bytes > 0 && stage_bytes <= kStageMax && (align_bits & 15) == 0;
   if (stage_ok) {
-    const kvq_status ss = ensure_dynamic_smem(kSlotAppend, append_kernel, kStageMax);
+    const kvq_status ss = ensure_dynamic_smem(kRope ? kSlotRopeAppend : kSlotAppend, append_kernel<kRope>, kStageMax);
     if (ss != KVQ_OK) return ss == KVQ_ERR_CAPACITY ? KVQ_ERR_CUDA : ss;
   }
-  append_kernel<<<grid, kThreads, stage_ok ? stage_bytes : 0, st>>>(v, k_new, v_new, n_new, n_new_per_seq,
-                                                                    stage_ok);
-  window_lengths_kernel<<<v.batch, kThreads, 0, st>>>(v, k_new, v_new, n_new, n_new_per_seq);
+  append_kernel<kRope><<<grid, kThreads, stage_ok ? stage_bytes : 0, st>>>(v, k_new, v_new, n_new, n_new_per_seq,
+                                                                           stage_ok, f);
+  window_lengths_kernel<kRope><<<v.batch, kThreads, 0, st>>>(v, k_new, v_new, n_new, n_new_per_seq, f);
   return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+}  // namespace
+
+kvq_status launch_append(const KvqView& v, const void* k_new, const void* v_new, int n_new,
+                         const int32_t* n_new_per_seq, cudaStream_t st) {
+  return launch_append_t<false>(v, k_new, v_new, n_new, n_new_per_seq, Fresh<false>{}, st);
+}
+
+kvq_status launch_rope_append(const KvqView& v, const RopeView& r, const void* q, const void* k_new,
+                              const void* v_new, long long qs, long long ks, long long vs, int n_new,
+                              const int32_t* n_new_per_seq, void* q_out, cudaStream_t st) {
+  if (q) {  // before the lengths advance
+    const kvq_status s = launch_rope_queries(v, r, q, qs, n_new, n_new_per_seq, q_out, st);
+    if (s != KVQ_OK) return s;
+  }
+  Fresh<true> f;
+  f.r = r;
+  f.k_tok = ks;
+  f.v_tok = vs;
+  f.rotate_keys = !v.rope_pre;
+  return launch_append_t<true>(v, k_new, v_new, n_new, n_new_per_seq, f, st);
 }
 
 kvq_status launch_dequantize(const KvqView& v, int seq, int t0, int t1, float* k_out, float* v_out,

@@ -670,6 +670,7 @@ __global__ void __launch_bounds__(128) combine_kernel(KvqView v, float* ws, floa
 }
 
 size_t attention_workspace_bytes(const KvqView& v, int batch) {
+  if (v.kaxis == KVQ_PER_BLOCK) return query_workspace_bytes(v, batch, 1);
   const int HB = (v.n_rep + kHB - 1) / kHB;
   const long long items = kTargetItems + 2LL * batch * v.Hkv * HB;
   const size_t generic = plan_header_bytes(batch) + (size_t)items * kHB * generic_rec(v.D) * sizeof(float);
@@ -680,6 +681,7 @@ size_t attention_workspace_bytes(const KvqView& v, int batch) {
 }
 
 int pick_decode_kernel(const KvqView& v) {
+  if (v.kaxis == KVQ_PER_BLOCK) return KVQ_KERNEL_BLOCK8;
   if (fast_eligible(v)) return KVQ_KERNEL_ROPE_I8I4;
   if (fp8_eligible(v)) return KVQ_KERNEL_FP8;
   if (int2_eligible(v)) return KVQ_KERNEL_INT2;
@@ -693,6 +695,10 @@ kvq_status launch_attention(const KvqView& v, const void* q, float* out, float s
     case KVQ_KERNEL_ROPE_I8I4: return launch_fast(v, q, out, scale, ws, st);
     case KVQ_KERNEL_FP8: return launch_fp8(v, q, out, scale, ws, st);
     case KVQ_KERNEL_INT2: return launch_int2(v, q, out, scale, ws, st);
+    case KVQ_KERNEL_BLOCK8: {
+      const QueryArgs a{q, out, nullptr, 1, 0, 1, scale};
+      return launch_query(v, a, ws, st);
+    }
     default: break;
   }
   // dynamic shared memory grows with the batch (the plan prefix) and D: raise the

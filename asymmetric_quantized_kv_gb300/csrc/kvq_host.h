@@ -34,7 +34,10 @@ enum SetupSlot {
   kSlotFast = kSlotGenericOcc + 12,     // pre-RoPE tensor-core kernel, 4 instances: CTAs per SM
   kSlotFp8 = kSlotFast + 4,       // FP8 tensor-core kernel, 2 instances
   kSlotInt2 = kSlotFp8 + 2,       // 2-bit tensor-core kernel, 2 instances
-  kSlotCount = kSlotInt2 + 2
+  kSlotRopeAppend = kSlotInt2 + 2,  // append kernel of kvq_rope_append
+  kSlotQueryFew,                    // few-row attention kernel, 36 instances: CTAs per SM
+  kSlotQueryTc = kSlotQueryFew + 36,  // many-row attention kernel, 6 instances
+  kSlotCount = kSlotQueryTc + 6
 };
 
 inline std::mutex& setup_mutex() {

@@ -48,12 +48,42 @@ struct KvqView {
   int rope_positions;
 };
 
+// Position rotation of kvq_rope_append (kvq_rope, checked); cs == nullptr: none.
+struct RopeView {
+  const float* cs = nullptr;
+  int positions = 0, rot = 0, halves = 0;
+};
+
+// One kvq_query_attention call (or a decode call over a PER_BLOCK cache: n_q = 1,
+// not causal, fp32 output), checked.
+struct QueryArgs {
+  const void* q;
+  void* out;
+  const int32_t* n_per_seq;
+  int n_q, causal, out_f32;
+  float scale;
+};
+
 // Host: resolve a validated config + cache into a view (false when invalid).
 bool make_view(const kvq_config* cfg, const kvq_cache* cache, KvqView* out);
 
 // Host launchers (each returns KVQ_OK or KVQ_ERR_CUDA).
 kvq_status launch_append(const KvqView& v, const void* k_new, const void* v_new, int n_new,
                          const int32_t* n_new_per_seq, cudaStream_t st);
+// kvq_rope_append: caches with another axis (the fold of launch_append with the rotation on its loads)
+// and PER_BLOCK caches (q may be null; r.cs null: no rotation, kvq_quantize_append).
+kvq_status launch_rope_append(const KvqView& v, const RopeView& r, const void* q, const void* k_new,
+                              const void* v_new, long long qs, long long ks, long long vs, int n_new,
+                              const int32_t* n_new_per_seq, void* q_out, cudaStream_t st);
+kvq_status launch_block_append(const KvqView& v, const RopeView& r, const void* q, const void* k_new,
+                               const void* v_new, long long qs, long long ks, long long vs, int n_new,
+                               const int32_t* n_new_per_seq, void* q_out, cudaStream_t st);
+// The rotation of the queries alone (every sequence that the append will take).
+kvq_status launch_rope_queries(const KvqView& v, const RopeView& r, const void* q, long long qs, int n_new,
+                               const int32_t* n_new_per_seq, void* q_out, cudaStream_t st);
+// Attention of n_q queries per sequence.
+size_t query_workspace_bytes(const KvqView& v, int batch, int n_q);
+kvq_status launch_query(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st);
 kvq_status launch_dequantize(const KvqView& v, int seq, int t0, int t1, float* k_out,
                              float* v_out, cudaStream_t st);
 kvq_status launch_calibrate(const KvqView& v, const void* src, long long n_tokens, float qmax,

@@ -1,0 +1,163 @@
+// kvq_query_attention: the choice of kernel, and the plain kernel that takes every
+// configuration (any axis, format, window, pre-RoPE keys, head_dim, fp32 sources).
+//
+// The plain kernel: a CTA takes 8 rows (query, head) of one (sequence, kv-head) and walks
+// the tokens in tiles of 32, dequantized into shared memory as fp32 by the rules of
+// include/kvq.h, with the softmax's running maximum and sum in base 2.  It is bound by the
+// per-element dequantization and by its one pass per 8 rows; it is what is right, not what
+// is fast.
+#include <math.h>
+
+#include "kvq_dequant.cuh"
+#include "kvq_query.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kPT = 128;    // threads
+constexpr int kPRows = 8;   // rows of a CTA
+constexpr int kPTile = 32;  // tokens of a tile
+constexpr float kLog2eP = 1.4426950408889634f;
+
+__global__ void __launch_bounds__(kPT) query_plain_kernel(KvqView v, QueryArgs a, int row_blocks) {
+  __shared__ float qs[kPRows][kMaxHeadDim];
+  __shared__ float kv[kPTile][kMaxHeadDim + 1];
+  __shared__ float ps[kPRows][kPTile];
+  __shared__ float ms[kPRows], ls[kPRows], al[kPRows];
+  __shared__ float w_hi[kMaxHeadDim / 2], w_lo[kMaxHeadDim / 2];
+  __shared__ int ends[kPRows];
+  __shared__ unsigned char okt[kPTile];
+  const int rb = blockIdx.x % row_blocks, x = blockIdx.x / row_blocks, h = x % v.Hkv, b = x / v.Hkv;
+  const int D = v.D, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = query_count(v, a, b), T = seq_tokens(v, b), nq = n_quantized(T, v.R);
+  const int rows = min(kPRows, n * v.n_rep - rb * kPRows);
+  if (rows <= 0) return;
+  // element offset of row r: query i = row / n_rep, head h * n_rep + row % n_rep
+  auto row_elem = [&](int r) {
+    const int row = rb * kPRows + r, i = row / v.n_rep;
+    return (((long long)b * a.n_q + i) * v.Hq + h * v.n_rep + row % v.n_rep) * D;
+  };
+  if (threadIdx.x < kPRows) {
+    ends[threadIdx.x] =
+        threadIdx.x < rows ? query_end(a, T, n, (rb * kPRows + threadIdx.x) / v.n_rep) : 0;
+    ms[threadIdx.x] = -INFINITY;
+    ls[threadIdx.x] = 0.f;
+  }
+  for (int e = threadIdx.x; e < kPRows * D; e += kPT) {
+    const int r = e / D, c = e % D;
+    qs[r][c] = r < rows ? load_src(a.q, row_elem(r) + c, v.src_bf16) * a.scale * kLog2eP : 0.f;
+  }
+  if (v.rope_pre)
+    for (int i = threadIdx.x; i < D / 2; i += kPT) rope_split(v, i, &w_hi[i], &w_lo[i]);
+  float o[kPRows][kMaxHeadDim / kPT];
+#pragma unroll
+  for (int r = 0; r < kPRows; ++r)
+#pragma unroll
+    for (int j = 0; j < kMaxHeadDim / kPT; ++j) o[r][j] = 0.f;
+  __syncthreads();
+  int end = 0;
+  for (int r = 0; r < kPRows; ++r) end = max(end, ends[r]);
+  for (int t0 = 0; t0 < end; t0 += kPTile) {
+    const int nt = min(kPTile, end - t0);
+    if (threadIdx.x < kPTile) okt[threadIdx.x] = 1;
+    __syncthreads();
+    for (int e = threadIdx.x; e < nt * D; e += kPT) {
+      const int tt = e / D, c = e % D;
+      bool ok = true;
+      kv[tt][c] = cache_key(v, b, h, t0 + tt, c, nq, &ok);
+      if (!ok) okt[tt] = 0;  // every writer writes the same
+    }
+    __syncthreads();
+    if (v.rope_pre) {
+      for (int e = threadIdx.x; e < nt * (D / 2); e += kPT) {
+        const int tt = e / (D / 2), i = e % (D / 2);
+        float sn, cs;
+        sincospif(2.f * rope_turns(t0 + tt, w_hi[i], w_lo[i]), &sn, &cs);
+        const float kx = kv[tt][2 * i], ky = kv[tt][2 * i + 1];
+        kv[tt][2 * i] = kx * cs - ky * sn;
+        kv[tt][2 * i + 1] = kx * sn + ky * cs;
+      }
+      __syncthreads();
+    }
+    for (int e = threadIdx.x; e < kPRows * kPTile; e += kPT) {
+      const int r = e / kPTile, tt = e % kPTile;
+      float s = -INFINITY;
+      if (tt < nt && okt[tt] && t0 + tt < ends[r]) {
+        s = 0.f;
+        for (int c = 0; c < D; ++c) s = fmaf(qs[r][c], kv[tt][c], s);
+      }
+      ps[r][tt] = s;
+    }
+    __syncthreads();
+    for (int r = warp; r < kPRows; r += kPT / 32) {
+      const float s = ps[r][lane];
+      float mx = s;
+      for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+      const float m = fmaxf(ms[r], mx);
+      const float p = s == -INFINITY ? 0.f : exp2f(s - m);
+      float sum = p;
+      for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+      const float alpha = m == -INFINITY ? 1.f : exp2f(ms[r] - m);
+      __syncwarp();
+      ps[r][lane] = p;
+      if (lane == 0) {
+        al[r] = alpha;
+        ls[r] = ls[r] * alpha + sum;
+        ms[r] = m;
+      }
+      __syncwarp();
+    }
+    for (int e = threadIdx.x; e < nt * D; e += kPT) kv[e / D][e % D] = cache_value(v, b, h, t0 + e / D, e % D, nq);
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kPRows; ++r) {
+      const float alpha = al[r];
+#pragma unroll
+      for (int j = 0; j < kMaxHeadDim / kPT; ++j) {
+        const int c = threadIdx.x + j * kPT;
+        if (c >= D) continue;
+        float s = o[r][j] * alpha;
+        for (int tt = 0; tt < nt; ++tt) {
+          const float p = ps[r][tt];
+          if (p != 0.f) s = fmaf(p, kv[tt][c], s);  // a token without weight adds nothing, whatever it holds
+        }
+        o[r][j] = s;
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int r = 0; r < kPRows; ++r) {
+    if (r >= rows) break;
+    const float inv = ls[r] > 0.f ? 1.f / ls[r] : 0.f;
+#pragma unroll
+    for (int j = 0; j < kMaxHeadDim / kPT; ++j) {
+      const int c = threadIdx.x + j * kPT;
+      if (c >= D) continue;
+      const float y = o[r][j] * inv;
+      if (a.out_f32) {
+        static_cast<float*>(a.out)[row_elem(r) + c] = y;
+      } else {
+        static_cast<__nv_bfloat16*>(a.out)[row_elem(r) + c] = __float2bfloat16_rn(y);
+      }
+    }
+  }
+}
+
+kvq_status launch_query_plain(const KvqView& v, const QueryArgs& a, cudaStream_t st) {
+  const long long row_blocks = ((long long)a.n_q * v.n_rep + kPRows - 1) / kPRows;
+  const long long grid = row_blocks * v.Hkv * v.batch;
+  if (grid > 0x7FFFFFFFLL) return KVQ_ERR_CAPACITY;
+  query_plain_kernel<<<(unsigned)grid, kPT, 0, st>>>(v, a, (int)row_blocks);
+  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t query_workspace_bytes(const KvqView& v, int batch, int n_q) { return 256; }
+
+kvq_status launch_query(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st) {
+  return launch_query_plain(v, a, st);
+}
+
+}  // namespace kvq

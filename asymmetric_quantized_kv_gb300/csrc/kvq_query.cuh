@@ -1,0 +1,42 @@
+// What the kernels of kvq_query_attention share: the queries of a call as rows of a
+// (sequence, kv-head), and the choice of kernel.
+//
+// The n queries of a sequence and the n_rep query heads of a kv-head read the same keys,
+// so they are rows of one matrix product: row i * n_rep + r is query i, head
+// kvh * n_rep + r.  Row i sees the tokens [0, end): all T, or T - n + i + 1 of them under
+// the causal mask.
+#pragma once
+
+#include "kvq_attn_plan.cuh"
+#include "kvq_ptx.cuh"
+
+namespace kvq {
+
+// Queries of sequence b in this call.
+__device__ __forceinline__ int query_count(const KvqView& v, const QueryArgs& a, int b) {
+  if (!a.n_per_seq) return a.n_q;
+  const int n = a.n_per_seq[b];
+  if (n < 0 || n > a.n_q) {
+    atomicOr(v.status, KVQ_DEV_BAD_LENGTH);
+    return 0;
+  }
+  return n;
+}
+
+// Tokens that query i of n sees of T.
+__device__ __forceinline__ int query_end(const QueryArgs& a, int T, int n, int i) {
+  return a.causal ? max(0, T - n + i + 1) : T;
+}
+
+// Kernels of kvq_query_attention.
+enum QueryKernel { kQueryPlain, kQueryFew, kQueryMany };
+constexpr int kFewRows = 8;  // rows of the few-row kernel: one column block of its products
+
+bool query_tc_shape(const KvqView& v);      // config only: the tensor-core kernels take it
+bool query_tc_eligible(const KvqView& v);   // and the cache's pool
+size_t query_few_workspace_bytes(const KvqView& v, int batch);
+size_t query_many_workspace_bytes(const KvqView& v, int batch, int n_q);
+kvq_status launch_query_few(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st);
+kvq_status launch_query_many(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st);
+
+}  // namespace kvq

@@ -42,7 +42,8 @@
  *     that timed out) set bits in the caller's `*status` word with atomicOr
  *     and skip the affected work; kernels never trap and never spin without
  *     an iteration limit.  Read the word when convenient.
- *   - Every call that enqueues work (calibrate, append, decode, dequantize)
+ *   - Every call that enqueues work (calibrate, append, decode,
+ *     query attention, dequantize)
  *     opens an NVTX range named after itself in the "libkvq" domain, so a
  *     profiler can attribute the kernels to the call; with no profiler
  *     attached a range costs a pointer test.
@@ -81,6 +82,17 @@
  *               group 0 means head_dim.
  *   PER_TENSOR: the static per-head scale k_scale[h] / v_scale[h]
  *               (symmetric INT-b or FP8 only).
+ *   PER_BLOCK:  one scale per (kv-head, block of `group` tokens), over all
+ *               head_dim channels, blocks aligned to absolute token index
+ *               multiples of `group` (a multiple of 16).  Formats of 8 bits
+ *               only: sym INT8 (s = a/127, the sym INT-b rule over the block)
+ *               and FP8 (s = a/448 for E4M3, a/57344 for E5M2, a = max|x| over
+ *               the block; y = x/s and the encoding as above).  Keys and values
+ *               are PER_BLOCK together, with one `group`; their formats may
+ *               differ.  Source tensors and windows are 16-byte aligned.
+ *               A non-finite key or value makes its block's scale, and with it
+ *               the outputs of the queries that see the block, meaningless; the
+ *               queries of the same call that do not see it may be affected too.
  *
  * Residual window (`residual` = R tokens, per sequence and kv-head): new
  * tokens are written unquantized (source dtype) into the window; when an
@@ -88,7 +100,8 @@
  * key groups, R value rows) and the window empties.  So after T tokens,
  * n_q = R*floor(T/R) tokens are quantized and T - n_q sit in the window.
  * Appending n tokens in one call gives the same bytes as n single appends.
- * R = 0 quantizes every token on append (not allowed with PER_CHANNEL keys).
+ * R = 0 quantizes every token on append (not allowed with PER_CHANNEL keys or
+ * PER_BLOCK tensors, whose R is a multiple of G).
  *
  * Page layout (stable; version KVQ_LAYOUT_VERSION).  Tokens of sequence b
  * live in pages block_table[b][t / P] at slot t % P (P = page_size).  A page
@@ -96,11 +109,15 @@
  * Each head block holds, each section starting on a 16-byte boundary:
  *   K codes  [P][D*bk/8]   bk = bits (8 for FP8)
  *   V codes  [P][D*bv/8]
- *   V meta   [P][ {D/gv scales} {D/gv mins (asym only)} ]  PER_TOKEN V
+ *   V meta   [P][ {D/gv scales} {D/gv mins (asym only)} ]  PER_TOKEN V;
+ *            [max(1, P/G)] scales  PER_BLOCK V (placed like the K scales below)
  *   K meta   PER_CHANNEL: [max(1, P/G)][ {D scales} {D mins (asym)} ];
  *            key group j is stored in the page holding token j*G, in slot
  *            (j*G % P) / G;
  *            PER_TOKEN:   [P][ {D/gk scales} {D/gk mins (asym)} ]
+ *            PER_BLOCK:   [max(1, P/G)] scales; block j's is stored like key
+ *            group j's of PER_CHANNEL.  The head block is then padded to a
+ *            multiple of 128 bytes.
  *            (scales and minima: fp32, or binary16 with meta_dtype = KVQ_F16)
  * Codes are packed along D: channel c's code occupies bits (c*b) % 8 ..
  * of byte (c*b)/8 of the token's row (little-endian bit order).  Code values:
@@ -133,7 +150,7 @@ typedef enum {
 
 typedef enum { KVQ_INT2 = 2, KVQ_INT4 = 4, KVQ_INT8 = 8, KVQ_FP8_E4M3 = 9, KVQ_FP8_E5M2 = 10 } kvq_format;
 typedef enum { KVQ_SYM_ABSMAX = 0, KVQ_ASYM_MINMAX = 1 } kvq_mode; /* ignored for FP8 */
-typedef enum { KVQ_PER_TENSOR = 0, KVQ_PER_TOKEN = 1, KVQ_PER_CHANNEL = 2 } kvq_axis;
+typedef enum { KVQ_PER_TENSOR = 0, KVQ_PER_TOKEN = 1, KVQ_PER_CHANNEL = 2, KVQ_PER_BLOCK = 3 } kvq_axis;
 typedef enum { KVQ_F32 = 0, KVQ_BF16 = 1, KVQ_F16 = 2 } kvq_dtype; /* source/window/q: F32, BF16;
                                                                  stored scales/minima: F32, F16 */
 
@@ -147,7 +164,7 @@ typedef struct {
   int32_t fmt;   /* kvq_format */
   int32_t mode;  /* kvq_mode   */
   int32_t axis;  /* kvq_axis   */
-  int32_t group; /* PER_CHANNEL: G tokens; PER_TOKEN: g channels (0 = D); else 0 */
+  int32_t group; /* PER_CHANNEL, PER_BLOCK: G tokens; PER_TOKEN: g channels (0 = D); else 0 */
 } kvq_qspec;
 
 typedef struct {
@@ -155,7 +172,7 @@ typedef struct {
   int32_t num_kv_heads; /* Hkv; query head h reads kv-head h / (Hq/Hkv) (GQA)    */
   int32_t head_dim;     /* D in {64, 128, 256}                                    */
   kvq_qspec k, v;       /* key and value quantization                              */
-  int32_t residual;     /* R: window tokens; R % G == 0 when keys are PER_CHANNEL  */
+  int32_t residual;     /* R: window tokens; R % G == 0 with PER_CHANNEL or PER_BLOCK */
   int32_t page_size;    /* P tokens per page, a multiple of 16; P % G == 0 or G % P == 0 */
   int32_t rope_pre;     /* 1: the cache holds pre-RoPE keys, rotated after dequant */
   float rope_theta;     /* RoPE base; angle of pair i at position p = p*theta^(-2i/D) */
@@ -246,6 +263,77 @@ kvq_status kvq_quantize_append(const kvq_config* cfg, const kvq_cache* cache, co
                                const void* v_new, int32_t n_new, const int32_t* n_new_per_seq,
                                void* stream);
 
+/* Position rotation of queries and keys (RoPE): channels [0, rot_dim) of every
+ * head, in pairs, by the angle of the token's absolute position; the other
+ * channels pass unchanged. */
+typedef enum {
+  KVQ_ROPE_INTERLEAVED = 0, /* pair i = channels (2i, 2i+1)             */
+  KVQ_ROPE_HALVES = 1       /* pair i = channels (i, i + rot_dim/2)     */
+} kvq_rope_pairing;
+
+typedef struct {
+  const float* cos_sin; /* [positions][rot_dim] device fp32, 16-byte aligned: the cosines of the
+                         * rot_dim/2 pairs, then their sines (any frequency scaling is the caller's) */
+  int32_t positions;    /* rows of the table                                                        */
+  int32_t rot_dim;      /* rotated channels: a multiple of 16, 16 .. head_dim                       */
+  int32_t pairing;      /* kvq_rope_pairing                                                         */
+} kvq_rope;
+
+/* kvq_quantize_append with the position rotation on the way, of the keys and of
+ * the queries that come with them: row i of sequence b has the position
+ * seq_lens[b] + i (its token index), and a pair (x, y) becomes
+ *   (x*c - y*s, x*s + y*c)   c, s = the table's cosine and sine,
+ * in fp32, each product and sum rounded to nearest (no fused multiply-add), then
+ * rounded to the source dtype (nearest even).  The rotated keys enter the window
+ * and the pages exactly as kvq_quantize_append would store them; q_out gets the
+ * rotated queries, which the attention entry points take.  With a pre-RoPE cache
+ * (rope_pre = 1) the keys are stored as given, since the cache rotates them when
+ * it is read; q is rotated all the same.
+ * q: [batch][n_new] rows of Hq*D, or NULL (then q_out is ignored); k_new, v_new:
+ * rows of Hkv*D; src dtype.  Consecutive rows of a tensor lie q_stride, k_stride,
+ * v_stride elements apart (the rows of a sequence, and sequence b+1's first row
+ * after sequence b's n_new rows; 0 = dense), so the three may be slices of one
+ * fused projection.  Pointers are 16-byte aligned, strides multiples of 16 bytes
+ * and no smaller than a row.  q_out: [batch][n_new][Hq][D] dense; it may be q
+ * itself when q is dense, and must not overlap it otherwise.  Rows of q_out at or
+ * beyond n_new_per_seq[b] are left as they were.
+ * A sequence that would exceed its pages, or whose positions exceed the table, is
+ * left unchanged (its q_out rows too) and sets KVQ_DEV_OVERFLOW. */
+kvq_status kvq_rope_append(const kvq_config* cfg, const kvq_cache* cache, const kvq_rope* rope,
+                           const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, int32_t n_new,
+                           const int32_t* n_new_per_seq, void* q_out, void* stream);
+
+/* Which cache tokens a query sees (kvq_query_attention). */
+typedef enum {
+  KVQ_MASK_NONE = 0,  /* all of them: cross attention to a sequence of another length         */
+  KVQ_MASK_CAUSAL = 1 /* those up to its own: the n queries of a sequence are its newest n
+                       * tokens, query i the token seq_lens[b] - n + i                        */
+} kvq_mask;
+
+/* Workspace bytes kvq_query_attention needs for `batch` sequences of at most n_q
+ * queries (0 when cfg is invalid or a size is < 1). */
+size_t kvq_query_workspace_bytes(const kvq_config* cfg, int32_t batch, int32_t n_q);
+
+/* Attention of several queries per sequence over the cache: a prompt's chunk or
+ * drafted tokens over the sequence's own tokens (KVQ_MASK_CAUSAL, after the
+ * append of those tokens), or a decoder's tokens over an encoder's cached states
+ * (KVQ_MASK_NONE).  Logits, softmax and output are those of kvq_decode_attention.
+ * q: [batch][n_q][Hq][D] device, src dtype, 16-byte aligned; sequence b uses its
+ * first n_q_per_seq[b] rows ([batch] device int32, values in [0, n_q]; NULL: n_q
+ * each; a value outside sets KVQ_DEV_BAD_LENGTH and counts as 0).
+ * out: [batch][n_q][Hq][D] device, src dtype (rounded once, to nearest even);
+ * rows at or beyond n_q_per_seq[b] are left as they were.  A query that sees no
+ * token (an empty cache, or more queries than tokens under the causal mask) gets
+ * zeros.  softmax_scale: 0 means 1/sqrt(D).  workspace: as for
+ * kvq_decode_attention, kvq_query_workspace_bytes(cfg, batch, n_q) bytes.
+ * Every configuration is taken.  PER_BLOCK caches with bf16 sources run on
+ * tensor cores; every other configuration runs on a plain kernel of fp32
+ * arithmetic, which suits small calls only. */
+kvq_status kvq_query_attention(const kvq_config* cfg, const kvq_cache* cache, const void* q,
+                               int32_t n_q, const int32_t* n_q_per_seq, int32_t mask, void* out,
+                               float softmax_scale, void* workspace, size_t ws_bytes, void* stream);
+
 /* Decode attention for one query per (sequence, query head).
  * q: [batch][Hq][D] device, src dtype, already rotated to its own position
  * (post-RoPE q).  out: [batch][Hq][D] device fp32.  softmax_scale: logit
@@ -271,8 +359,9 @@ typedef enum {
   KVQ_KERNEL_ROPE_I8I4 = 1, /* sym INT8 per-channel pre-RoPE K + asym INT4 per-token V,
                                8 kv-heads x 4 query heads, power-of-two G and P */
   KVQ_KERNEL_FP8 = 2,       /* FP8 (E4M3 or E5M2) K and V, 8 query heads per kv-head */
-  KVQ_KERNEL_INT2 = 3       /* asym 2-bit per-channel K + asym 2-bit per-token V (g = 32),
+  KVQ_KERNEL_INT2 = 3,      /* asym 2-bit per-channel K + asym 2-bit per-token V (g = 32),
                                4 query heads per kv-head, bf16 or fp32 window */
+  KVQ_KERNEL_BLOCK8 = 4     /* every PER_BLOCK cache: kvq_query_attention's kernels, one query each */
 } kvq_kernel;
 
 /* Which kvq_kernel kvq_decode_attention launches for these arguments.  Host

@@ -38,6 +38,11 @@ Everything here is the plain definition, written for a reader to check by eye:
   Reading: the asymmetric range is taken from the stored (rounded-down) minimum,
   d = max(mx - mn16, 1e-8), so the top code never clips.  Values beyond the
   binary16 range saturate (scale 65504, minimum -65504).
+* Block scales (axis PER_BLOCK; 8-bit formats): one scale per block of G tokens and
+  kv-head, over all channels: sym INT8 by the absmax rule above, FP8 with
+  s = absmax / (448 or 57344) and the byte of x/s.
+* Position rotation on append (rope_rows): the table's cosine and sine, one fp32
+  operation per product and sum, then one rounding to the source dtype.
 * Axes: K per channel over G-token groups, V per token ("Why Keys Are More
   Sensitive Than Values in INT8 KV Cache Quantization", section "Outlier
   Distribution in Key Channels"; fourth page, "What should I actually turn on
@@ -63,7 +68,7 @@ import numpy as np
 
 INT2, INT4, INT8, FP8_E4M3, FP8_E5M2 = 2, 4, 8, 9, 10
 SYM, ASYM = 0, 1
-PER_TENSOR, PER_TOKEN, PER_CHANNEL = 0, 1, 2
+PER_TENSOR, PER_TOKEN, PER_CHANNEL, PER_BLOCK = 0, 1, 2, 3
 F32, BF16, F16 = 0, 1, 2  # source dtypes; F16 also names fp16 scale/min storage
 
 FL32_1EM8 = float(np.float32(1e-8))
@@ -354,6 +359,8 @@ def layout(cfg: Config) -> dict:
     vm = _align16(vc + P * vrow)
     mb = meta_bytes(cfg)
     vm_bytes = P * (D // _tok_group(cfg.v, D)) * _n_meta(cfg.v) * mb if cfg.v.axis == PER_TOKEN else 0
+    if cfg.v.axis == PER_BLOCK:
+        vm_bytes = max(1, P // cfg.v.group) * mb
     km = _align16(vm + vm_bytes)
     if cfg.k.axis == PER_CHANNEL:
         km_bytes = max(1, P // cfg.k.group) * D * _n_meta(cfg.k) * mb
@@ -361,7 +368,11 @@ def layout(cfg: Config) -> dict:
         km_bytes = P * (D // _tok_group(cfg.k, D)) * _n_meta(cfg.k) * mb
     else:
         km_bytes = 0
+    if cfg.k.axis == PER_BLOCK:
+        km_bytes = max(1, P // cfg.k.group) * mb
     head = _align16(km + km_bytes)
+    if cfg.k.axis == PER_BLOCK:
+        head = (head + 127) // 128 * 128
     return dict(krow=krow, vrow=vrow, kc=kc, vc=vc, vm=vm, km=km, head=head,
                 page=head * cfg.num_kv_heads)
 
@@ -414,13 +425,37 @@ def _quant_k_channel(x, spec: QSpec, meta16=False):
     return c.reshape(n, D), s[:, 0, :], m[:, 0, :]
 
 
+def _quant_block(x, spec: QSpec, meta16=False):
+    """One scale per block of G consecutive tokens: x [n, D], n % G == 0.
+
+    Returns (codes [n, D] (FP8: bytes), scales [n/G], None)."""
+    n, D = x.shape
+    xg = x.reshape(n // spec.group, spec.group * D)
+    a = np.max(np.abs(xg), axis=1, keepdims=True) if n else np.zeros((0, 1))
+    if is_fp8(spec.fmt):
+        s = fl32(a / fp8_max(spec.fmt))
+        if meta16:
+            s = f16_up(s)
+        c = quant_fp8(xg, s, spec.fmt)
+    else:
+        c, s = (quant_sym16 if meta16 else quant_sym)(xg, a, 8)
+    return c.reshape(n, D), s[:, 0], None
+
+
+def _dequant_block(c, s, spec: QSpec):
+    n, D = c.shape
+    cg = c.reshape(n // spec.group, spec.group * D)
+    deq = (lambda b, sc: dequant_fp8(b, sc, spec.fmt)) if is_fp8(spec.fmt) else dequant_sym
+    return deq(cg, s[:, None]).reshape(n, D)
+
+
 @dataclass
 class HeadState:
     """Quantized state of one (sequence, kv-head) stream after T tokens."""
     T: int
     n_q: int
     kc: np.ndarray  # [n_q, D] int64 signed codes (FP8: bytes)
-    ks: np.ndarray | None  # PER_CHANNEL [n_q/G, D]; PER_TOKEN [n_q, D/g]
+    ks: np.ndarray | None  # PER_CHANNEL [n_q/G, D]; PER_TOKEN [n_q, D/g]; PER_BLOCK [n_q/G]
     km: np.ndarray | None
     vc: np.ndarray
     vs: np.ndarray | None
@@ -443,6 +478,10 @@ def quantize_stream(cfg: Config, K, V, k_scale=0.0, v_scale=0.0) -> HeadState:
     m16 = cfg.meta_dtype == F16
     if cfg.k.axis == PER_CHANNEL:
         kc, ks, km = _quant_k_channel(K[:nq], cfg.k, m16)
+    elif cfg.k.axis == PER_BLOCK:
+        kc, ks, km = _quant_block(K[:nq], cfg.k, m16)
+        vc, vs, vm = _quant_block(V[:nq], cfg.v, m16)
+        return HeadState(T, nq, kc, ks, km, vc, vs, vm, K[nq:].copy(), V[nq:].copy())
     else:
         kc, ks, km = _quant_tokens(K[:nq], cfg.k, k_scale, D, m16)
     vc, vs, vm = _quant_tokens(V[:nq], cfg.v, v_scale, D, m16)
@@ -504,6 +543,9 @@ def dequantize_stream(cfg: Config, st: HeadState, k_scale=0.0, v_scale=0.0):
     """Dequantized K, V [T, D] (float64 holding fp32 values); window rows are the
     stored source values.  Keys are as stored (pre-RoPE when rope_pre)."""
     D = cfg.head_dim
+    if cfg.k.axis == PER_BLOCK:
+        return (np.concatenate([_dequant_block(st.kc, st.ks, cfg.k), st.k_win]),
+                np.concatenate([_dequant_block(st.vc, st.vs, cfg.v), st.v_win]))
     if cfg.k.axis == PER_CHANNEL:
         G = cfg.k.group
         n = st.n_q
@@ -536,6 +578,46 @@ def rope(x, positions, theta: float):
     out[:, 0::2] = x[:, 0::2] * c - x[:, 1::2] * s
     out[:, 1::2] = x[:, 0::2] * s + x[:, 1::2] * c
     return out
+
+
+def bf16(x):
+    """Round fp32-exact values to the nearest bf16 (ties to even), as float64."""
+    u = np.asarray(x, dtype=np.float64).astype(np.float32).view(np.uint32).astype(np.uint64)
+    u = (u + 0x7FFF + ((u >> 16) & 1)) & 0xFFFF0000
+    return u.astype(np.uint32).view(np.float32).astype(np.float64)
+
+
+def rope_rows(x, positions, cos_sin, rot: int, halves: bool, src_dtype: int = F32):
+    """Channels [0, rot) of each row of x [n, D] rotated by its position's row of the
+    table cos_sin [positions, rot] (cosines, then sines, fp32 values); pairs are
+    (2i, 2i+1), or (i, i + rot/2) with `halves`."""
+    x = np.asarray(x, dtype=np.float64)
+    half = rot // 2
+    t = np.asarray(cos_sin, dtype=np.float64)[np.asarray(positions)]
+    c, s = t[:, :half], t[:, half:]
+    first, second = (slice(0, half), slice(half, rot)) if halves else (slice(0, rot, 2), slice(1, rot, 2))
+    out = x.copy()
+    u, w = x[:, first], x[:, second]
+    out[:, first] = fl32(fl32(u * c) - fl32(w * s))
+    out[:, second] = fl32(fl32(u * s) + fl32(w * c))
+    return bf16(out) if src_dtype == BF16 else out
+
+
+def query_attention(q, K, V, causal: bool, scale=None):
+    """Attention of the rows of q [n, H, D] over K, V [T, D]: every token, or, causal,
+    the first T - n + i + 1 for row i.  Rows that see none get 0.  Returns the output
+    and the weighted mean of |V| (the size of the sums behind it)."""
+    n, H, D = q.shape
+    T = K.shape[0]
+    out, size = np.zeros((2, n, H, V.shape[1]))
+    scale = 1.0 / np.sqrt(D) if scale is None else scale
+    for i in range(n):
+        end = max(0, T - n + i + 1) if causal else T
+        if end == 0:
+            continue
+        p = softmax((np.asarray(q[i], np.float64) @ K[:end].T) * scale)
+        out[i], size[i] = p @ V[:end], p @ np.abs(V[:end])
+    return out, size
 
 
 def attention(q, K, V, scale=None):
@@ -650,6 +732,12 @@ def write_head_pages(cfg: Config, pages: np.ndarray, defined: np.ndarray, block_
             ng = D // _tok_group(cfg.k, D)
             row = [st.ks[t]] + ([st.km[t]] if _n_meta(cfg.k) == 2 else [])
             put(page, L["km"] + slot * ng * _n_meta(cfg.k) * mb, f32(np.concatenate(row)))
+    if cfg.k.axis == PER_BLOCK:
+        G = cfg.k.group
+        for j in range(st.n_q // G):
+            page, slot = int(block_table[b][j * G // P]), (j * G % P) // G
+            put(page, L["vm"] + slot * mb, f32([st.vs[j]]))
+            put(page, L["km"] + slot * mb, f32([st.ks[j]]))
     if cfg.k.axis == PER_CHANNEL:
         G = cfg.k.group
         for j in range(st.n_q // G):

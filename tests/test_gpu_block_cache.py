@@ -1,0 +1,435 @@
+"""Block-scaled 8-bit caches, rotated append and query attention on the GPU against the
+oracle.  Bit-exact: page bytes, windows, lengths, rotated queries, kvq_dequantize.
+Attention: against 64 bits on the dequantized cache, element by element.
+
+Tolerance of an output x (bf16 sources): the final rounding is off by at most
+2^-8 |x|.  The weights enter the tensor cores in f16, each off by at most 2^-11 of
+itself (weights below 2^-14 of the running maximum by an absolute 2^-25), so the sum
+by 2^-11 A with A = sum p |v| / sum p; the logits are fp32 sums of exact products, off
+by under 2^-22 sum |q k| scale, which for these streams (sum |q k| scale < 2^10) is
+2^-12 relative on a weight, at most 2^-11 A on the output after normalisation.
+fp32 sources (plain kernel): the final rounding 2^-24 |x|, the logits' fp32 sum of D
+products (at most D 2^-24 sum |q k| scale, under 2^-9 on a weight for the outlier
+channels here; measured sums err far less), so 2^-10 A covers both.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from oracle import kvq_oracle as O  # noqa: E402
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from kvq_testlib import Case, torch_src  # noqa: E402
+
+S, BLK = O.SYM, O.PER_BLOCK
+I8, E4, E5 = O.INT8, O.FP8_E4M3, O.FP8_E5M2
+
+
+def cfg_of(Hq, H, D, kf, vf, G, R, P, **kw):
+    return O.Config(Hq, H, D, O.QSpec(kf, S, BLK, G), O.QSpec(vf, S, BLK, G), R, P, 0, 1e4, kw.pop("src", O.BF16), **kw)
+
+
+# name: (config, sequence lengths)
+CASES = {
+    "e4m3_p64": (cfg_of(32, 8, 128, E4, E4, 64, 64, 64), [0, 1, 63, 64, 65, 300, 1000]),
+    "int8_p16": (cfg_of(8, 2, 128, I8, I8, 64, 64, 16), [1, 64, 130, 700, 2100]),
+    "e5m2_p256": (cfg_of(16, 2, 128, E5, E5, 64, 128, 256), [127, 128, 129, 900]),
+    "mixed_formats": (cfg_of(8, 2, 128, E4, I8, 32, 64, 64), [5, 64, 333]),
+    "g16_p16": (cfg_of(4, 4, 128, I8, I8, 16, 16, 16), [3, 16, 17, 250]),
+    "g128_p32": (cfg_of(8, 1, 128, E4, E4, 128, 256, 32), [255, 256, 700]),
+    "d64": (cfg_of(16, 16, 64, E4, E4, 64, 64, 64), [5, 64, 200, 1500]),
+    "d64_int8_nrep4": (cfg_of(8, 2, 64, I8, I8, 32, 64, 16), [1, 31, 64, 500]),
+    "d256": (cfg_of(8, 2, 256, E4, E4, 64, 64, 64), [7, 64, 260]),
+    "d256_int8": (cfg_of(4, 4, 256, I8, I8, 32, 32, 32), [32, 100]),
+    "nrep7": (cfg_of(14, 2, 128, E4, E4, 64, 64, 64), [65, 400]),
+    "nrep16": (cfg_of(16, 1, 128, I8, I8, 64, 64, 64), [65, 400]),
+    "nrep40": (cfg_of(40, 1, 64, E5, E5, 64, 64, 64), [100, 64]),
+    "meta16": (cfg_of(8, 2, 128, E4, E4, 64, 64, 64, meta_dtype=O.F16), [1, 64, 300]),
+    "meta16_int8_p16": (cfg_of(8, 8, 64, I8, I8, 32, 32, 16, meta_dtype=O.F16), [40, 33, 0]),
+    "f32": (cfg_of(8, 2, 128, E4, E4, 64, 64, 64, src=O.F32), [1, 64, 130]),
+    "f32_int8_d64": (cfg_of(4, 4, 64, I8, I8, 16, 48, 16, src=O.F32), [47, 48, 100]),
+    "group_512": (cfg_of(8, 2, 128, I8, I8, 512, 512, 64), [511, 512, 1300]),  # more than registers hold
+}
+
+
+@pytest.fixture(scope="module", params=sorted(CASES))
+def case(request):
+    cfg, lens = CASES[request.param]
+    c = Case(cfg, lens, seed=100 + sorted(CASES).index(request.param))
+    c.name = request.param
+    return c
+
+
+def test_pages_bit_exact(case):
+    case.check_pages()
+
+
+def test_lengths_and_window(case):
+    case.check_lengths_and_window()
+
+
+def test_dequantize_bit_exact(case):
+    case.check_dequantize()
+
+
+def test_decode_attention(case):
+    import asymmetric_quantized_kv_gb300 as K
+    assert case.cache.decode_kernel() == K.KVQ_KERNEL_BLOCK8
+    case.check_attention()
+    case.check_attention(scale=0.05)
+
+
+def check_queries(case, n, causal, per_seq=None, scale=0.0, seed=7, q=None):
+    """kvq_query_attention of n queries a sequence against the oracle; rows past a sequence's count keep
+    what they held."""
+    cfg = case.cfg
+    Bn, D = len(case.lens), cfg.head_dim
+    g = np.random.default_rng(seed)
+    if q is None:
+        q = g.standard_normal((Bn, n, cfg.num_q_heads, D)).astype(np.float32)
+        q = O.bf16(q).astype(np.float32) if cfg.src_dtype == O.BF16 else q
+    counts = [n] * Bn if per_seq is None else list(per_seq)
+    tq = torch_src(q, cfg)
+    for b, c in enumerate(counts):  # rows that are not to be read
+        tq[b, c:] = float("nan")
+    out = torch.full_like(tq, 7.25)
+    per = None if per_seq is None else torch.tensor(counts, dtype=torch.int32, device="cuda")
+    case.cache.query_attention(tq, causal=causal, n_q_per_seq=per, out=out, softmax_scale=scale)
+    got = out.double().cpu().numpy()
+    half = 2.0 ** -8 if cfg.src_dtype == O.BF16 else 2.0 ** -24
+    worst = 0.0
+    for b in range(Bn):
+        assert np.all(got[b, counts[b]:] == 7.25)
+        for h in range(cfg.num_kv_heads):
+            Kd, Vd = O.dequantize_stream(cfg, case.states[b][h], case.k_scale[h], case.v_scale[h])
+            if cfg.rope_pre:
+                Kd = O.rope(Kd, np.arange(Kd.shape[0]), cfg.rope_theta)
+            heads = slice(h * cfg.n_rep, (h + 1) * cfg.n_rep)
+            ref, size = O.query_attention(q[b, :counts[b], heads].astype(np.float64), Kd, Vd, causal, scale or None)
+            err = np.abs(got[b, :counts[b], heads] - ref)
+            lim = half * np.abs(ref) + 2.0 ** -10 * size
+            assert np.all(err <= lim), (case.name, b, h, float((err - lim).max()))
+            worst = max(worst, float(np.max(err / np.maximum(size, 1e-30), initial=0)))
+    assert int(case.cache.status.item()) == 0
+    return worst
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n", [1, 2, 5, 33])
+def test_query_attention(case, n, causal):
+    check_queries(case, n, causal)
+
+
+def test_query_attention_ragged_counts(case):
+    Bn = len(case.lens)
+    check_queries(case, 9, True, [(3 * b) % 10 for b in range(Bn)])
+    check_queries(case, 9, False, [9 - (4 * b) % 10 for b in range(Bn)], scale=0.03)
+
+
+@pytest.mark.parametrize("name,n", [("e4m3_p64", 129), ("int8_p16", 300), ("d64", 257), ("nrep40", 64), ("nrep7", 100)])
+def test_query_attention_many_rows(name, n):
+    """Several row tiles, cut ones among them; more queries than some sequences have tokens."""
+    cfg, lens = CASES[name]
+    c = Case(cfg, lens, seed=3)
+    c.name = name
+    check_queries(c, n, True)
+    check_queries(c, n, False, [n - 17 * (b % 3) for b in range(len(lens))])
+
+
+# ------------------------------------------------------------------------ other caches
+
+OTHER = {
+    "rope_pre_i8i4": (O.Config(32, 8, 128, O.QSpec(O.INT8, S, O.PER_CHANNEL, 64), O.QSpec(O.INT4, O.ASYM, O.PER_TOKEN, 0),
+                               64, 16, 1, 5e5, O.BF16), [1, 64, 200]),
+    "kivi2": (O.Config(8, 2, 128, O.QSpec(O.INT2, O.ASYM, O.PER_CHANNEL, 32), O.QSpec(O.INT2, O.ASYM, O.PER_TOKEN, 32),
+                       128, 64, 0, 1e4, O.BF16), [5, 128, 300]),
+    "fp8_static": (O.Config(16, 2, 128, O.QSpec(E4, S, O.PER_TENSOR), O.QSpec(E4, S, O.PER_TENSOR), 0, 16, 0, 1e4, O.F32),
+                   [1, 17, 130]),
+    "int8_token_d256": (O.Config(2, 2, 256, O.QSpec(I8, S, O.PER_TOKEN, 64), O.QSpec(I8, O.ASYM, O.PER_TOKEN, 128), 32, 32,
+                                 0, 1e4, O.BF16, meta_dtype=O.F16), [31, 32, 90]),
+    "int4_channel_r512": (O.Config(8, 1, 64, O.QSpec(O.INT4, O.ASYM, O.PER_CHANNEL, 512),
+                                   O.QSpec(O.INT4, O.ASYM, O.PER_TOKEN, 0), 512, 512, 0, 1e4, O.F32), [512, 700]),
+    "block_rope_pre": (O.Config(8, 2, 128, O.QSpec(E4, S, BLK, 64), O.QSpec(E4, S, BLK, 64), 64, 64, 1, 1e4, O.BF16),
+                       [1, 64, 200]),
+}
+
+
+@pytest.mark.parametrize("name", sorted(OTHER))
+def test_query_attention_of_every_axis(name):
+    cfg, lens = OTHER[name]
+    c = Case(cfg, lens, seed=11)
+    c.name = name
+    for n, causal in ((1, True), (3, True), (4, False)):
+        check_queries(c, n, causal)
+
+
+# ------------------------------------------------------------------------ rotated append
+
+def rope_setup(positions, rot, theta=1e4):
+    ang = np.arange(positions)[:, None] * theta ** (-2 * np.arange(rot // 2) / rot)
+    table = np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)
+    return table, torch.from_numpy(table).cuda()
+
+
+def rotated_case(cfg, lens, rot, halves, chunks, seed=0, fused=True, positions=None):
+    """Fill an empty cache through append_rope in the given chunk sizes; returns a Case-like object
+    whose oracle streams hold the oracle's rotated keys."""
+    import asymmetric_quantized_kv_gb300 as K
+    Bn, H, Hq, D = len(lens), cfg.num_kv_heads, cfg.num_q_heads, cfg.head_dim
+    c = Case.__new__(Case)
+    base = Case(cfg, [0] * Bn, seed=seed, extra_pages=-(-max(max(lens), max(chunks)) // cfg.page_size) + 1)
+    c.__dict__.update(base.__dict__)
+    c.lens, c.name = list(lens), "rotated"
+    g = np.random.default_rng(seed)
+    rnd = (lambda x: O.bf16(x)) if cfg.src_dtype == O.BF16 else (lambda x: O.fl32(x))
+    x = rnd(g.standard_normal((Bn, max(lens), Hq + 2 * H, D))).astype(np.float32)
+    x[:, :, Hq:Hq + H, 3::29] *= 8
+    table, tt = rope_setup(positions or c.maxp * cfg.page_size, rot)
+    rope = K.make_rope(tt, rot, K.KVQ_ROPE_HALVES if halves else K.KVQ_ROPE_INTERLEAVED)
+    if O.is_fp8(cfg.k.fmt) and cfg.k.axis == O.PER_TENSOR:
+        c.k_scale, c.v_scale = [0.25] * H, [0.125] * H
+        c.cache.k_scale.fill_(0.25)
+        c.cache.v_scale.fill_(0.125)
+    done, qs = [0] * Bn, []
+    step = 0
+    while any(done[b] < lens[b] for b in range(Bn)):
+        n = chunks[step % len(chunks)]
+        step += 1
+        take = [min(n - (b % 2 if n > 2 else 0), lens[b] - done[b]) for b in range(Bn)]
+        rows = np.zeros((Bn, n, Hq + 2 * H, D), np.float32)
+        for b in range(Bn):
+            rows[b, :take[b]] = x[b, done[b]:done[b] + take[b]]
+        t = torch_src(rows, cfg)
+        for b in range(Bn):
+            t[b, take[b]:] = float("nan")  # rows past a sequence's count are not read
+        q, k, v = t[:, :, :Hq], t[:, :, Hq:Hq + H], t[:, :, Hq + H:]
+        if not fused:
+            q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        out = torch.full((Bn, n, Hq, D), 3.5, dtype=t.dtype, device="cuda")
+        c.cache.append_rope(rope, q, k, v, torch.tensor(take, dtype=torch.int32, device="cuda"), q_out=out)
+        got = out.double().cpu().numpy()
+        for b in range(Bn):
+            assert np.all(got[b, take[b]:] == 3.5)
+            pos = np.arange(done[b], done[b] + take[b])
+            for h in range(Hq):
+                want = O.rope_rows(rows[b, :take[b], h], pos, table, rot, halves, cfg.src_dtype)
+                assert np.array_equal(got[b, :take[b], h], want), (b, h, step)
+            done[b] += take[b]
+    torch.cuda.synchronize()
+    assert int(c.cache.status.item()) == 0
+    c.K = [[(x[b, :lens[b], Hq + h].astype(np.float64) if cfg.rope_pre else
+             O.rope_rows(x[b, :lens[b], Hq + h], np.arange(lens[b]), table, rot, halves, cfg.src_dtype))
+            for h in range(H)] for b in range(Bn)]
+    c.V = [[x[b, :lens[b], Hq + H + h].astype(np.float64) for h in range(H)] for b in range(Bn)]
+    c.states = [[O.quantize_stream(cfg, c.K[b][h], c.V[b][h], c.k_scale[h], c.v_scale[h]) for h in range(H)]
+                for b in range(Bn)]
+    return c
+
+
+ROT = {  # name: (config, rot, halves, chunk sizes)
+    "one_by_one": (cfg_of(4, 2, 128, E4, E4, 32, 32, 16), 128, True, [1]),
+    "steps_and_prompts": (cfg_of(8, 2, 128, I8, I8, 64, 64, 64), 128, False, [3, 50, 1, 200]),
+    "prompt": (cfg_of(8, 2, 128, E4, E4, 64, 128, 64), 64, True, [400]),
+    "small_steps_d64": (cfg_of(6, 3, 64, E5, E5, 16, 32, 16), 16, True, [7, 16, 17]),
+    "d256": (cfg_of(4, 2, 256, I8, E4, 32, 64, 64), 256, False, [5, 90]),
+    "one_head": (cfg_of(3, 1, 128, E4, E4, 64, 64, 256), 96, False, [2, 70]),
+    "many_heads": (cfg_of(24, 12, 64, E4, E4, 64, 64, 64), 64, True, [1, 66]),
+    "f32": (cfg_of(4, 2, 128, E4, E4, 32, 64, 32, src=O.F32), 128, True, [4, 40, 1]),
+    "meta16": (cfg_of(4, 2, 128, I8, I8, 32, 64, 32, meta_dtype=O.F16), 32, False, [1, 33]),
+    "group_512": (cfg_of(4, 2, 128, I8, I8, 512, 512, 64), 128, True, [300]),
+    "other_kivi2": (OTHER["kivi2"][0], 128, True, [1, 100, 30]),
+    "other_fp8_static": (OTHER["fp8_static"][0], 64, False, [1, 70]),
+    "other_r512": (OTHER["int4_channel_r512"][0], 64, True, [600]),
+    "other_token_d256": (OTHER["int8_token_d256"][0], 256, True, [9, 40]),
+    "rope_pre": (OTHER["rope_pre_i8i4"][0], 128, False, [1, 90]),
+    "block_rope_pre": (OTHER["block_rope_pre"][0], 128, False, [1, 90]),
+}
+
+
+@pytest.mark.parametrize("fused", [True, False])
+@pytest.mark.parametrize("name", sorted(ROT))
+def test_rope_append_bit_exact(name, fused):
+    cfg, rot, halves, chunks = ROT[name]
+    big = cfg.residual >= 512
+    lens = [600, 520] if big else ([70, 33, 1] if name == "one_by_one" else [200, 131, 64, 1])
+    c = rotated_case(cfg, lens, rot, halves, chunks, seed=len(name), fused=fused)
+    c.check_pages()
+    c.check_lengths_and_window()
+    c.check_dequantize()
+
+
+def test_rotation_in_place_and_without_queries():
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(8, 2, 128, E4, E4, 64, 64, 64)
+    table, tt = rope_setup(256, 128)
+    rope = K.make_rope(tt, 128, K.KVQ_ROPE_HALVES)
+    for n in (3, 40):
+        a, b = (Case(cfg, [0, 0], seed=1, extra_pages=3).cache for _ in range(2))
+        g = torch.Generator(device="cuda").manual_seed(n)
+        q = torch.randn(2, n, 8, 128, generator=g, device="cuda").bfloat16()
+        k, v = (torch.randn(2, n, 2, 128, generator=g, device="cuda").bfloat16() for _ in range(2))
+        want = a.append_rope(rope, q, k, v)
+        mine = q.clone()
+        assert b.append_rope(rope, mine, k, v, q_out=mine) is mine
+        assert torch.equal(mine, want)
+        assert b.append_rope(rope, None, k, v) is None
+        a.append_rope(rope, None, k, v)
+        assert torch.equal(a.pages, b.pages) and torch.equal(a.k_win, b.k_win) and a.seq_lens.tolist() == [2 * n] * 2
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("axis", ["block", "other"])
+def test_rope_append_that_does_not_fit(n, axis):
+    """A sequence that would pass its pages, or the table, is left as it was and reported."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(4, 2, 128, E4, E4, 32, 32, 16) if axis == "block" else O.Config(
+        4, 2, 128, O.QSpec(I8, S, O.PER_CHANNEL, 32), O.QSpec(I8, S, O.PER_TOKEN, 0), 32, 32, 0, 1e4, O.BF16)
+    for positions, full in ((512, 1), (90, 0)):
+        c = Case(cfg, [10, 60], seed=2, extra_pages=0)   # 64 tokens fit
+        if full == 0:
+            c = Case(cfg, [10, 60], seed=2, extra_pages=10)
+        start = [10, 64 - n + 1] if full else [10, 90 - n + 1]
+        c.cache.seq_lens.copy_(torch.tensor(start, dtype=torch.int32))
+        _, tt = rope_setup(positions, 128)
+        rope = K.make_rope(tt, 128)
+        pages, win = c.cache.pages.clone(), c.cache.k_win.clone()
+        q = torch.randn(2, n, 4, 128, device="cuda").bfloat16()
+        k, v = (torch.randn(2, n, 2, 128, device="cuda").bfloat16() for _ in range(2))
+        out = torch.full_like(q, 2.0)
+        c.cache.append_rope(rope, q, k, v, q_out=out)
+        assert int(c.cache.status.item()) == K.KVQ_DEV_OVERFLOW
+        assert c.cache.seq_lens.tolist() == [10 + n, start[1]]
+        assert torch.equal(c.cache.k_win[1], win[1]) and bool((out[1] == 2.0).all())
+        own = c.cache.page_view()[c.block_table[1]]
+        assert torch.equal(own, pages.view_as(c.cache.page_view())[c.block_table[1]])
+
+
+# ------------------------------------------------------------------------ used together
+
+def test_prompt_drafts_and_steps_together():
+    """A prompt in two chunks, drafted tokens, a rejected draft (the lengths set back), single steps:
+    each append followed by its attention, against the oracle."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(8, 2, 128, E4, E4, 32, 64, 32)
+    Bn, H, Hq, D = 2, 2, 8, 128
+    table, tt = rope_setup(512, D)
+    rope = K.make_rope(tt, D, K.KVQ_ROPE_HALVES)
+    cache = Case(cfg, [0] * Bn, seed=1, extra_pages=12).cache
+    g = np.random.default_rng(8)
+    Ks, Vs = [np.zeros((0, H, D))] * Bn, [np.zeros((0, H, D))] * Bn
+    for n, keep in ((100, 100), (37, 37), (5, 3), (1, 1), (5, 5), (1, 1), (50, 50), (1, 1)):
+        x = O.bf16(g.standard_normal((Bn, n, Hq + 2 * H, D))).astype(np.float32)
+        t = torch_src(x, cfg)
+        q = cache.append_rope(rope, t[:, :, :Hq], t[:, :, Hq:Hq + H], t[:, :, Hq + H:])
+        out = cache.query_attention(q).double().cpu().numpy()
+        T0 = Ks[0].shape[0]
+        pos = np.arange(T0, T0 + n)
+        rot = lambda y: O.rope_rows(y, pos, table, D, True, O.BF16)
+        for b in range(Bn):
+            Ks[b] = np.concatenate([Ks[b], np.stack([rot(x[b, :, Hq + h]) for h in range(H)], 1)])
+            Vs[b] = np.concatenate([Vs[b], x[b, :, Hq + H:].astype(np.float64)])
+            for h in range(H):
+                st = O.quantize_stream(cfg, Ks[b][:, h], Vs[b][:, h])
+                Kd, Vd = O.dequantize_stream(cfg, st)
+                qq = np.stack([rot(x[b, :, r]) for r in range(4 * h, 4 * h + 4)], 1)
+                ref, size = O.query_attention(qq, Kd, Vd, True)
+                err = np.abs(out[b, :, 4 * h:4 * h + 4] - ref)
+                assert np.all(err <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * size), (n, b, h)
+        if keep < n:  # no window filled since, so its rows are all still there
+            assert T0 // 64 == (T0 + n) // 64
+            cache.seq_lens.sub_(n - keep)
+            Ks, Vs = [y[:T0 + keep] for y in Ks], [y[:T0 + keep] for y in Vs]
+    assert int(cache.status.item()) == 0
+
+
+def test_cross_attention_of_two_batches_over_shared_pages():
+    """Two decoder batches over one encoder cache, whose block table names the same pages twice."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg, _ = CASES["d64"]
+    c = Case(cfg, [192, 128], seed=4)   # whole windows: everything is in the pages
+    twice = K.PagedKVCache.over(c.c_cfg, c.cache.pages, c.cache.block_table.repeat(2, 1), c.cache.seq_lens.repeat(2),
+                                c.cache.k_win.repeat(2, 1, 1, 1), c.cache.v_win.repeat(2, 1, 1, 1))
+    q = torch.randn(4, 21, 16, 64, device="cuda").bfloat16()
+    both = twice.query_attention(q, causal=False)
+    assert torch.equal(both[:2], c.cache.query_attention(q[:2].contiguous(), causal=False))
+    assert torch.equal(both[2:], c.cache.query_attention(q[2:].contiguous(), causal=False))
+
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_graph_replays_step_by_step(n):
+    """Append and attention captured once and replayed advance the cache as eager calls do, bit for bit."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(8, 2, 128, E4, E4, 32, 32, 32)
+    _, tt = rope_setup(512, 128)
+    rope = K.make_rope(tt, 128)
+    eager, graph, warm = (Case(cfg, [30, 7], seed=6, extra_pages=8).cache for _ in range(3))
+    x = torch.randn(2, n, 12, 128, device="cuda").bfloat16()
+    qo, out = torch.empty(2, n, 8, 128, device="cuda").bfloat16(), torch.empty(2, n, 8, 128, device="cuda").bfloat16()
+
+    def step(cache, qo, out):
+        cache.append_rope(rope, x[:, :, :8], x[:, :, 8:10], x[:, :, 10:], q_out=qo)
+        cache.query_attention(qo, out=out)
+    step(warm, qo.clone(), out.clone())
+    graph.query_attention(qo.zero_(), out=out)  # its workspace, before the capture
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        step(graph, qo, out)
+    for i in range(4):
+        x.copy_(torch.randn(2, n, 12, 128, device="cuda"))
+        gr.replay()
+        qe, oe = torch.empty_like(qo), torch.empty_like(out)
+        step(eager, qe, oe)
+        assert torch.equal(qe, qo) and torch.equal(oe, out), i
+        assert torch.equal(eager.pages, graph.pages) and torch.equal(eager.seq_lens, graph.seq_lens)
+    assert int(graph.status.item()) == 0
+
+
+def test_bad_counts_and_pages():
+    """Counts outside [0, n] and block-table entries outside the pool are reported, never followed."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(8, 2, 128, E4, E4, 64, 64, 64)
+    for n in (2, 40):
+        c = Case(cfg, [300, 300, 300], seed=9)
+        q = torch.randn(3, n, 8, 128, device="cuda").bfloat16()
+        want = c.cache.query_attention(q)
+        out = torch.full_like(q, 5.0)
+        c.cache.query_attention(q, n_q_per_seq=torch.tensor([n, -1, n + 1], dtype=torch.int32, device="cuda"), out=out)
+        assert int(c.cache.status.item()) == K.KVQ_DEV_BAD_LENGTH
+        assert torch.equal(out[0], want[0]) and bool((out[1:] == 5.0).all())
+        c.cache.status.zero_()
+        c.cache.block_table[1, 1] = 1 << 20
+        c.cache.block_table[2, 2] = -5
+        got = c.cache.query_attention(q)
+        assert int(c.cache.status.item()) == K.KVQ_DEV_BAD_PAGE
+        assert torch.equal(got[0], want[0]) and bool(torch.isfinite(got).all())
+
+
+def test_binding_refusals():
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(8, 2, 128, E4, E4, 64, 64, 64)
+    c = Case(cfg, [10, 20], seed=1).cache
+    q = torch.zeros(2, 3, 8, 128, device="cuda").bfloat16()
+    kv = torch.zeros(2, 3, 2, 128, device="cuda").bfloat16()
+    rope = K.make_rope(rope_setup(256, 128)[1], 128)
+    bad = [lambda: c.query_attention(q.float()), lambda: c.query_attention(q[:1]), lambda: c.query_attention(q[:, :, :4]),
+           lambda: c.query_attention(q.transpose(0, 1).contiguous().transpose(0, 1)), lambda: c.query_attention(q.cpu()),
+           lambda: c.query_attention(q, out=q.float()),
+           lambda: c.query_attention(q, n_q_per_seq=torch.zeros(2, dtype=torch.int64, device="cuda")),
+           lambda: c.append_rope(rope, q, kv[:, :2], kv), lambda: c.append_rope(rope, q.float(), kv, kv),
+           lambda: c.append_rope(rope, q, kv.transpose(0, 1).contiguous().transpose(0, 1), kv),
+           lambda: c.append_rope(rope, q, kv, kv, q_out=q.float()),
+           lambda: c.append_rope(rope, q, kv, kv, torch.zeros(3, dtype=torch.int32, device="cuda")),
+           lambda: K.make_rope(torch.zeros(8, 64, device="cuda"), 128),
+           lambda: K.PagedKVCache.over(c.cfg, c.pages[:-1], c.block_table, c.seq_lens, c.k_win, c.v_win),
+           lambda: K.PagedKVCache.over(c.cfg, c.pages, c.block_table, c.seq_lens, None, c.v_win),
+           lambda: K.PagedKVCache.over(c.cfg, c.pages, c.block_table.long(), c.seq_lens, c.k_win, c.v_win)]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            print("not refused:", i)
+    assert c.seq_lens.tolist() == [10, 20]
