@@ -10,6 +10,7 @@
 
 #include "kvq_dequant.cuh"
 #include "kvq_query.cuh"
+#include "kvq_tmap.h"
 
 namespace kvq {
 namespace {
@@ -154,9 +155,25 @@ kvq_status launch_query_plain(const KvqView& v, const QueryArgs& a, cudaStream_t
 
 }  // namespace
 
-size_t query_workspace_bytes(const KvqView& v, int batch, int n_q) { return 256; }
+// The tensor-core kernels take bf16 sources over PER_BLOCK caches of one format whose keys are stored
+// rotated (or need no rotation).  A batch beyond 4096 sequences exceeds their plan's shared memory.
+bool query_tc_shape(const KvqView& v) {
+  return v.kaxis == KVQ_PER_BLOCK && v.kfmt == v.vfmt && v.src_bf16 && !v.rope_pre && v.batch <= 4096;
+}
+
+bool query_tc_eligible(const KvqView& v) {
+  return query_tc_shape(v) && (long long)v.n_pages * v.page_bytes / 128 < (1LL << 31) && tensor_map_encoder() != nullptr;
+}
+
+size_t query_workspace_bytes(const KvqView& v, int batch, int n_q) {
+  KvqView b = v;
+  b.batch = batch;
+  if (!query_tc_shape(b)) return 256;
+  return query_few_workspace_bytes(v, batch);
+}
 
 kvq_status launch_query(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st) {
+  if (query_tc_eligible(v) && (long long)a.n_q * v.n_rep <= kFewRows) return launch_query_few(v, a, ws, st);
   return launch_query_plain(v, a, st);
 }
 

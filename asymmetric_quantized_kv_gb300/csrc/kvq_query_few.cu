@@ -1,0 +1,711 @@
+// Attention of at most 8 rows (query token x query head) per kv-head over a PER_BLOCK
+// cache: decode steps and short drafts, bf16 sources, head_dim 64, 128 or 256.
+//
+// Mathematics, for a 16-token tile (it lies in one block of the cache, so one key scale ks
+// and one value scale vs = 2^e f, f in [1, 2)): with code matrices C_k, C_v,
+//   x = (q . C_k) (ks scale log2 e),   p = 2^(x + e - M),
+//   l += p 2^-e,   o += (p f) C_v,   out = o / l,
+// M a running maximum of x + e.  The value scale's exponent rides in the softmax's, so
+// the products that enter the tensor cores stay near 1 whatever the scales are; M is
+// raised only when a tile exceeds it by 2^8 (p f then stays below 2^9, inside f16).
+// The operands are exact: every code is an f16 number, and a bf16 query row is one after
+// scaling by a power of two (elements more than 2^-32 below the row's largest drop bits).
+// p f is rounded to f16 once (bf16 output: 2^-11 against the output's own 2^-8), or split
+// in two f16 terms for fp32 output.
+//
+// What bounds it: reading the codes.  A warp owns a unit (sequence, chunk, kv-head) and
+// streams 16-token tiles of keys and values through its own 3-stage ring, filled by 2-D
+// TMA copies of the pool seen as rows of 128 bytes with the 128-byte swizzle, so warps
+// never wait for one another.  Keys are the M operand of m16n8k16 (16 tokens x 8 rows),
+// values, transposed on the way from shared memory, that of the second product (16
+// channels x 8 rows); p crosses from one layout to the other with movmatrix.  The window's
+// tokens (bf16) take the same path from registers, scaled by a power of two per tile.
+// Units are sized so that they fill the warps of the GPU a whole number of times (up to
+// 4); a second kernel merges a (sequence, kv-head)'s chunks.
+#include <math.h>
+
+#include "kvq_ptx.cuh"
+#include "kvq_query.cuh"
+#include "kvq_tmap.h"
+
+namespace kvq {
+namespace {
+
+using namespace ptx;
+
+constexpr int kTile = 16;
+constexpr int kFWarps = 4;
+constexpr int kFThreads = kFWarps * 32;
+constexpr int kFStages = 3;
+constexpr int kRounds = 4;          // units per warp at most
+constexpr int kMaxUnits = 8192;     // units beyond one per (sequence, kv-head)
+constexpr int kUnitTokens = 512;    // a warp takes several units only if they are this long
+constexpr int kMinUnit = 64;        // tokens of the smallest chunk
+constexpr float kLazy = 8.f;
+constexpr float kMinit = -1e30f;
+constexpr int kMinExp = -100;       // smallest value-scale exponent that rides in the softmax
+
+constexpr int fmt_index(int fmt) { return fmt == KVQ_INT8 ? 0 : fmt == KVQ_FP8_E4M3 ? 1 : 2; }
+constexpr int kI8 = 0, kE4 = 1, kE5 = 2;
+
+// The four 8-bit codes of a word as two f16x2 (bytes 0, 1 and 2, 3); exact.
+template <int F>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (F == kI8) {
+    const uint32_t x = w ^ 0x80808080u;  // code + 128, into the mantissa of 1024
+    lo = hsub2(prmt(x, 0x64646464u, 0x4140u), 0x64806480u);
+    hi = hsub2(prmt(x, 0x64646464u, 0x4342u), 0x64806480u);
+  } else if constexpr (F == kE4) {
+    lo = e4m3x2_to_f16x2(lo16(w));
+    hi = e4m3x2_to_f16x2(hi16(w));
+  } else {  // E5M2 is the upper byte of an f16
+    lo = prmt(w, 0u, 0x1404u);
+    hi = prmt(w, 0u, 0x3424u);
+  }
+}
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// 2^e for e in [-126, 127].
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+// Exponent of |x| (x finite, not 0; subnormals count as 2^-126).
+__device__ __forceinline__ int exponent_of(float x) { return max(1, (__float_as_int(x) >> 23) & 255) - 127; }
+
+// A bf16 pair times a power of two, as f16x2.
+__device__ __forceinline__ uint32_t bf16x2_scaled(uint32_t u, float s) {
+  return pack_f16x2(__uint_as_float(u << 16) * s, __uint_as_float(u & 0xffff0000u) * s);
+}
+__device__ __forceinline__ uint32_t bf16x2_absmax(uint32_t m, uint32_t u) {  // of magnitudes, as bits
+  const uint32_t a = u & 0x7fff7fffu;
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;\n" : "=r"(r) : "r"(m), "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+// Factor 2^-k that brings values of largest magnitude `top` (bf16 bits) into [2^8, 2^9), and 2^k.
+__device__ __forceinline__ void norm_factors(uint32_t top, float& down, float& up) {
+  int k = exponent_of(__uint_as_float(top << 16)) - 8;
+  k = top == 0 ? 0 : max(-126, min(k, 119));
+  down = pow2i(-k);
+  up = pow2i(k);
+}
+
+// ---- plan: per sequence ceil(T / C) chunks (over pages and window alike) for each kv-head;
+// unit = pref[b] + kvh * chunks + chunk.  Workspace: int C, int units, pref[B + 1], u64 counter,
+// then a record (M, l, 2 pad, o[D]) per (unit, row).
+__host__ __device__ inline size_t few_counter_offset(int B) { return ((size_t)(B + 3) * 4 + 7) & ~(size_t)7; }
+__host__ __device__ inline size_t few_header_bytes(int B) { return (few_counter_offset(B) + 8 + 255) / 256 * 256; }
+
+// Whole CTA.  workers: warps of the grid.
+__device__ inline void few_plan(const KvqView& v, int workers, int* pref, int* s_C, int* s_units) {
+  __shared__ unsigned long long s_sum;
+  __shared__ int s_part[kFThreads];
+  const int B = v.batch, nt = kFThreads;
+  const int seg = (B + nt - 1) / nt, b0 = min(B, (int)threadIdx.x * seg), b1 = min(B, b0 + seg);
+  auto total = [&](unsigned long long mine) {
+    if (threadIdx.x == 0) s_sum = 0ull;
+    __syncthreads();
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if ((threadIdx.x & 31) == 0) atomicAdd(&s_sum, mine);
+    __syncthreads();
+    const unsigned long long s = s_sum;
+    __syncthreads();
+    return s;
+  };
+  unsigned long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += (unsigned long long)seq_tokens(v, b);
+  const unsigned long long work = total(mine) * v.Hkv;
+  const unsigned long long each = work / workers;
+  const int rounds = (int)min(max(each / kUnitTokens, 1ull), (unsigned long long)min(kRounds, max(1, kMaxUnits / workers)));
+  const unsigned long long most = min((unsigned long long)rounds * workers, (unsigned long long)kMaxUnits);
+  unsigned long long C = (work + most - 1) / most;
+  C = max((unsigned long long)kMinUnit, (C + kTile - 1) / kTile * kTile);
+  // the cut ends of the sequences may push the units past a whole number of rounds: longer chunks
+  for (int k = 0; k < 6; ++k) {
+    unsigned long long units = 0;
+    for (int b = b0; b < b1; ++b) units += ((unsigned long long)seq_tokens(v, b) + C - 1) / C;
+    if (total(units) * v.Hkv <= most) break;
+    C = (C + C / 16 + kTile - 1) / kTile * kTile;
+  }
+  for (;;) {  // never more units than the workspace holds
+    unsigned long long units = 0;
+    for (int b = b0; b < b1; ++b) units += ((unsigned long long)seq_tokens(v, b) + C - 1) / C;
+    if (total(units) <= (unsigned long long)kMaxUnits / v.Hkv + B) break;  // true once C covers every sequence
+    C *= 2;
+  }
+  int local = 0;
+  for (int b = b0; b < b1; ++b) local += (int)((seq_tokens(v, b) + (long long)C - 1) / (long long)C) * v.Hkv;
+  s_part[threadIdx.x] = local;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int per = nt / 32, i0 = threadIdx.x * per;
+    int s = 0;
+    for (int i = i0; i < i0 + per; ++i) s += s_part[i];
+    int incl = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if ((int)threadIdx.x >= o) incl += y;
+    }
+    int run = incl - s;
+    for (int i = i0; i < i0 + per; ++i) {
+      const int x = s_part[i];
+      s_part[i] = run;
+      run += x;
+    }
+    if (threadIdx.x == 31) {
+      *s_units = incl;
+      *s_C = (int)min(C, (unsigned long long)(1 << 30));
+    }
+  }
+  __syncthreads();
+  int run = s_part[threadIdx.x];
+  for (int b = b0; b < b1; ++b) {
+    pref[b] = run;
+    run += (int)((seq_tokens(v, b) + (long long)C - 1) / (long long)C) * v.Hkv;
+  }
+  if (threadIdx.x == 0) pref[B] = *s_units;
+  __syncthreads();
+}
+
+template <int D>
+struct __align__(1024) FewSmem {
+  uint8_t kv[kFWarps][kFStages][2][kTile * D];
+  uint64_t bar[kFWarps][kFStages];
+  int valid[kFWarps][kFStages];
+};
+
+// Byte o of a 1024-byte aligned tile under the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swz(uint32_t o) { return o ^ (((o >> 7) & 7u) << 4); }
+
+template <int F, int D, bool kF32>
+__global__ void __launch_bounds__(kFThreads)
+    query_few_kernel(KvqView v, QueryArgs a, float* ws, int dynamic, const __grid_constant__ CUtensorMap tmap) {
+  constexpr int NS = D / 16;      // steps of the first product, and channel tiles of the second
+  constexpr int LC = D / 4;       // channels a lane holds of a key row
+  constexpr int GC = D / 8;       // channels a lane holds of a value row
+  constexpr int KB = kTile * D;   // bytes of a tile
+  extern __shared__ unsigned char dyn_raw[];
+  unsigned char* dyn = dyn_raw + ((1024 - (smem_u32(dyn_raw) & 1023)) & 1023);
+  FewSmem<D>& sm = *reinterpret_cast<FewSmem<D>*>(dyn);
+  int* pref = reinterpret_cast<int*>(dyn + sizeof(FewSmem<D>));
+  __shared__ int s_C, s_units;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int workers = gridDim.x * kFWarps;
+  few_plan(v, workers, pref, &s_C, &s_units);
+  if (blockIdx.x == 0) {
+    int* hd = reinterpret_cast<int*>(ws);
+    if (threadIdx.x == 0) {
+      hd[0] = s_C;
+      hd[1] = s_units;
+    }
+    for (int b = threadIdx.x; b <= v.batch; b += kFThreads) hd[2 + b] = pref[b];
+  }
+  grid_dep_launch();
+  if (lane == 0) {
+    for (int s = 0; s < kFStages; ++s) mbar_init(&sm.bar[warp][s], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  const int C = s_C, n_units = s_units, rows_max = a.n_q * v.n_rep;
+  unsigned long long* counter =
+      reinterpret_cast<unsigned long long*>(reinterpret_cast<char*>(ws) + few_counter_offset(v.batch));
+  float* part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + few_header_bytes(v.batch));
+  int lstage = 0, cstage = 0;
+  uint32_t cphase = 0, n_loaded = 0, n_consumed = 0;
+  bool stalled = false;
+
+  int unit = blockIdx.x * kFWarps + warp;
+  while (unit < n_units) {
+    unsigned long long nxt = 0;
+    if (dynamic && lane == 0) nxt = atomicAdd(counter, 1ull);
+    int lo = 0, hi = v.batch - 1;  // largest b with pref[b] <= unit (sequences without units share a value)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pref[mid] <= unit) lo = mid; else hi = mid - 1;
+    }
+    const int b = lo, nc = (pref[b + 1] - pref[b]) / v.Hkv;
+    const int h = (unit - pref[b]) / nc, chunk = (unit - pref[b]) % nc;
+    const int T = seq_tokens(v, b), nq = n_quantized(T, v.R), n = query_count(v, a, b), rows = n * v.n_rep;
+    const int t0 = chunk * C, t1 = min(T, t0 + C);
+    const int tq = min(t1, nq);                                // tiles before tq come from the pages
+    const int qtiles = tq > t0 ? (tq - t0) / kTile : 0;        // nq and t0 are multiples of 16
+    const int tiles = (t1 - t0 + kTile - 1) / kTile;
+    const int32_t* bt = v.block_table + (long long)b * v.max_pages;
+    const long long head_off = (long long)h * v.head_bytes;
+
+    // ---- the ring: lane 0 walks page and slot; the next page's id is read a tile ahead
+    int pg = t0 / v.P, slot = t0 % v.P, pid = 0, pid_next = 0;
+    auto issue = [&]() {
+      const int stage = lstage;
+      if (++lstage == kFStages) lstage = 0;
+      ++n_loaded;
+      uint64_t* bar = &sm.bar[warp][stage];
+      const bool ok = pid >= 0 && pid < v.n_pages;
+      sm.valid[warp][stage] = ok;
+      if (!ok) {
+        atomicOr(v.status, KVQ_DEV_BAD_PAGE);
+        mbar_arrive(bar);
+      } else {
+        const long long byte0 = (long long)pid * v.page_bytes + head_off + (long long)slot * D;
+        const int yk = (int)(byte0 >> 7), yv = yk + (v.off_vc >> 7);
+        mbar_arrive_expect_tx(bar, 2 * KB);
+        const uint64_t pol = l2_evict_first();
+        tma_load_2d_hint(sm.kv[warp][stage][0], &tmap, 0, yk, bar, pol);
+        tma_load_2d_hint(sm.kv[warp][stage][1], &tmap, 0, yv, bar, pol);
+      }
+      slot += kTile;
+      if (slot >= v.P) {
+        slot = 0;
+        ++pg;
+        pid = pid_next;
+        pid_next = pg + 1 < v.max_pages ? bt[pg + 1] : -1;
+      }
+    };
+    if (lane == 0 && !stalled && qtiles > 0) {
+      pid = bt[pg];
+      pid_next = pg + 1 < v.max_pages ? bt[pg + 1] : -1;
+      fence_proxy_async();
+      for (int i = 0; i < min(kFStages, qtiles); ++i) issue();
+    }
+    // ---- block scales: lane j holds those of block blk0 + j of the unit
+    float ks_l = 0.f, vs_l = 0.f;
+    bool sok_l = true;
+    const int blk_first = t0 / v.kgroup;
+    int blk0 = blk_first;
+    auto load_scales = [&]() {
+      const int blk = blk0 + lane, g0 = blk * v.kgroup;
+      ks_l = vs_l = 0.f;
+      sok_l = true;
+      if (g0 < tq) {
+        const int p = bt[g0 / v.P];
+        sok_l = p >= 0 && p < v.n_pages;
+        if (sok_l) {
+          const uint8_t* hb = v.pages + (long long)p * v.page_bytes + head_off;
+          const int s = (g0 % v.P) / v.kgroup;
+          ks_l = load_meta(hb + v.off_km, s, v.meta16);
+          vs_l = load_meta(hb + v.off_vm, s, v.meta16);
+        } else {
+          atomicOr(v.status, KVQ_DEV_BAD_PAGE);
+        }
+      }
+    };
+    if (qtiles > 0) load_scales();
+
+    // ---- queries: column g is row g; lane (g, t) holds its channels t LC .. t LC + LC - 1, brought into
+    // f16 by the row's power of two
+    uint32_t bq[NS][2];
+    float up = 1.f;
+    {
+      uint32_t u[LC / 2];
+#pragma unroll
+      for (int i = 0; i < LC / 2; ++i) u[i] = 0u;
+      if (g < rows) {
+        const long long qi = (((long long)b * a.n_q + g / v.n_rep) * v.Hq + h * v.n_rep + g % v.n_rep) * D + t * LC;
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + qi);
+#pragma unroll
+        for (int i = 0; i < LC / 8; ++i) {
+          const uint4 x = p[i];
+          u[4 * i] = x.x; u[4 * i + 1] = x.y; u[4 * i + 2] = x.z; u[4 * i + 3] = x.w;
+        }
+      }
+      uint32_t m2 = 0u;
+#pragma unroll
+      for (int i = 0; i < LC / 2; ++i) m2 = bf16x2_absmax(m2, u[i]);
+      uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      float down;
+      norm_factors(top, down, up);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        bq[s][0] = bf16x2_scaled(u[2 * s], down);
+        bq[s][1] = bf16x2_scaled(u[2 * s + 1], down);
+      }
+    }
+    // this lane's logits are those of rows 2t, 2t + 1: their factor and the tokens they see
+    const float fct[2] = {__shfl_sync(0xffffffffu, up, 8 * t) * a.scale * 1.4426950408889634f,
+                          __shfl_sync(0xffffffffu, up, 8 * t + 4) * a.scale * 1.4426950408889634f};
+    int end[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) end[e] = 2 * t + e < rows ? query_end(a, T, n, (2 * t + e) / v.n_rep) : 0;
+
+    float O[NS][4];
+#pragma unroll
+    for (int m = 0; m < NS; ++m) O[m][0] = O[m][1] = O[m][2] = O[m][3] = 0.f;
+    float m_run[2] = {kMinit, kMinit}, l_run[2] = {0.f, 0.f};
+
+    // logits of the tile at token tok (acc: token g / g + 8 x row 2t / 2t + 1) -> B operand of the second
+    // product; kf, vf: scale of the keys, and of the values as 2^e f
+    auto softmax = [&](const float (&acc)[4], int tok, float kf, int e, float f, uint32_t (&ph)[2], uint32_t (&pl)[2]) {
+      float x[2][2];  // [token g / g + 8][row]
+      const float fe = (float)e;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float c = kf * fct[r];
+        x[0][r] = tok + g < end[r] ? fmaf(acc[r], c, fe) : -INFINITY;
+        x[1][r] = tok + g + 8 < end[r] ? fmaf(acc[2 + r], c, fe) : -INFINITY;
+      }
+      const bool need = fmaxf(x[0][0], x[1][0]) > m_run[0] + kLazy || fmaxf(x[0][1], x[1][1]) > m_run[1] + kLazy;
+      if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float mx = fmaxf(x[0][r], x[1][r]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float mn = fmaxf(m_run[r], mx), al = ex2(m_run[r] - mn);
+          m_run[r] = mn;
+          l_run[r] *= al;
+#pragma unroll
+          for (int m = 0; m < NS; ++m) {  // columns 2t, 2t + 1 of the outputs are the same rows
+            O[m][r] *= al;
+            O[m][2 + r] *= al;
+          }
+        }
+      }
+      const float ie = pow2i(-e);
+      float p[2][2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        p[0][r] = ex2(x[0][r] - m_run[r]);
+        p[1][r] = ex2(x[1][r] - m_run[r]);
+        l_run[r] = fmaf(p[0][r] + p[1][r], ie, l_run[r]);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if constexpr (kF32) {
+          uint32_t hi2, lo2;
+          split_hi_lo(p[k][0] * f, p[k][1] * f, hi2, lo2);
+          ph[k] = movmatrix(hi2);
+          pl[k] = movmatrix(lo2);
+        } else {
+          ph[k] = movmatrix(pack_f16x2(p[k][0] * f, p[k][1] * f));
+        }
+      }
+    };
+
+    for (int i = 0; i < qtiles; ++i) {
+      const int tok = t0 + i * kTile, stage = cstage;
+      bool valid = false;
+      if (!stalled) {
+        if (!mbar_wait_bounded(&sm.bar[warp][stage], cphase, kWaitPolls)) {
+          atomicOr(v.status, KVQ_DEV_TIMEOUT);
+          stalled = true;
+        } else {
+          valid = sm.valid[warp][stage] != 0;
+        }
+      }
+      if (++cstage == kFStages) {
+        cstage = 0;
+        cphase ^= 1u;
+      }
+      ++n_consumed;
+      const int blk = tok / v.kgroup;
+      if (blk - blk0 >= 32) {
+        blk0 = blk;
+        load_scales();
+      }
+      const float kf = __shfl_sync(0xffffffffu, ks_l, blk - blk0), vf = __shfl_sync(0xffffffffu, vs_l, blk - blk0);
+      valid = valid && __shfl_sync(0xffffffffu, (int)sok_l, blk - blk0);
+      if (__all_sync(0xffffffffu, valid)) {  // a tile without its page, or its scales, takes no weight
+        const uint8_t* kt = sm.kv[warp][stage][0];
+        const uint8_t* vt = sm.kv[warp][stage][1];
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < LC / 16; ++c) {
+          const uint4 k0 = *reinterpret_cast<const uint4*>(kt + swz(g * D + t * LC + 16 * c));
+          const uint4 k1 = *reinterpret_cast<const uint4*>(kt + swz((g + 8) * D + t * LC + 16 * c));
+          const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t a0, a1, a2, a3;
+            codes_to_f16<F>(w0[j], a0, a2);
+            codes_to_f16<F>(w1[j], a1, a3);
+            mma_16816(acc, a0, a1, a2, a3, bq[4 * c + j][0], bq[4 * c + j][1]);
+          }
+        }
+        const int e = vf == 0.f ? 0 : min(126, max(kMinExp, exponent_of(vf)));
+        const float f = vf * pow2i(-e);  // in [1, 2), or less below 2^kMinExp
+        uint32_t ph[2], pl[2] = {0u, 0u};
+        softmax(acc, tok, kf, e, f, ph, pl);
+        // ---- second product: rows g / g + 8 of channel tile m = channels g GC + 2m / + 1,
+        //      k-slots = tokens 2t, 2t + 1, 2t + 8, 2t + 9
+        constexpr int W = GC / 4;  // words of a value row a lane holds
+        uint32_t wv[4][W];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = 2 * t + (j & 1) + 8 * (j >> 1);
+          if constexpr (W == 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(vt + swz(r * D + g * GC));
+            wv[j][0] = x.x;
+            wv[j][1] = x.y;
+          } else {
+#pragma unroll
+            for (int c = 0; c < W / 4; ++c) {
+              const uint4 x = *reinterpret_cast<const uint4*>(vt + swz(r * D + g * GC + 16 * c));
+              wv[j][4 * c] = x.x; wv[j][4 * c + 1] = x.y; wv[j][4 * c + 2] = x.z; wv[j][4 * c + 3] = x.w;
+            }
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < NS; ++m) {
+          // bytes 2 (m % 2), 2 (m % 2) + 1 of word m / 2 of two tokens: (even channel: both, odd channel: both)
+          const uint32_t sel = (m & 1) ? 0x7362u : 0x5140u;
+          uint32_t a0, a1, a2, a3;
+          codes_to_f16<F>(prmt(wv[0][m >> 1], wv[1][m >> 1], sel), a0, a1);
+          codes_to_f16<F>(prmt(wv[2][m >> 1], wv[3][m >> 1], sel), a2, a3);
+          mma_16816(O[m], a0, a1, a2, a3, ph[0], ph[1]);
+          if constexpr (kF32) mma_16816(O[m], a0, a1, a2, a3, pl[0], pl[1]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0 && i + kFStages < qtiles && !stalled) {
+        fence_proxy_async();
+        issue();
+      }
+    }
+
+    // ---- the window's tokens: bf16 rows, a power of two per tile in place of the scales
+    for (int i = qtiles; i < tiles; ++i) {
+      const int tok = t0 + i * kTile;
+      const uint16_t* kw = static_cast<const uint16_t*>(v.k_win) + (((long long)b * v.R + (tok - nq)) * v.Hkv + h) * D;
+      const uint16_t* vw = static_cast<const uint16_t*>(v.v_win) + (((long long)b * v.R + (tok - nq)) * v.Hkv + h) * D;
+      const long long pitch = (long long)v.Hkv * D;
+      const uint4 z4 = make_uint4(0u, 0u, 0u, 0u);
+      float acc[4] = {0.f, 0.f, 0.f, 0.f}, down, kf, f;
+      {
+        uint32_t x0[LC / 2], x1[LC / 2], m2 = 0u;
+#pragma unroll
+        for (int c = 0; c < LC / 8; ++c) {
+          const uint4 y0 = tok + g < t1 ? *reinterpret_cast<const uint4*>(kw + g * pitch + t * LC + 8 * c) : z4;
+          const uint4 y1 = tok + g + 8 < t1 ? *reinterpret_cast<const uint4*>(kw + (g + 8) * pitch + t * LC + 8 * c) : z4;
+          x0[4 * c] = y0.x; x0[4 * c + 1] = y0.y; x0[4 * c + 2] = y0.z; x0[4 * c + 3] = y0.w;
+          x1[4 * c] = y1.x; x1[4 * c + 1] = y1.y; x1[4 * c + 2] = y1.z; x1[4 * c + 3] = y1.w;
+        }
+#pragma unroll
+        for (int c = 0; c < LC / 2; ++c) m2 = bf16x2_absmax(bf16x2_absmax(m2, x0[c]), x1[c]);
+        norm_factors(warp_max(max(m2 & 0xffffu, m2 >> 16)), down, kf);
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+          mma_16816(acc, bf16x2_scaled(x0[2 * s], down), bf16x2_scaled(x1[2 * s], down), bf16x2_scaled(x0[2 * s + 1], down),
+                    bf16x2_scaled(x1[2 * s + 1], down), bq[s][0], bq[s][1]);
+      }
+      constexpr int W = GC / 2;  // bf16 pairs of a value row a lane holds
+      uint32_t wv[4][W], m2 = 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 2 * t + (j & 1) + 8 * (j >> 1);
+#pragma unroll
+        for (int c = 0; c < W / 4; ++c) {
+          const uint4 x = tok + r < t1 ? *reinterpret_cast<const uint4*>(vw + r * pitch + g * GC + 8 * c) : z4;
+          wv[j][4 * c] = x.x; wv[j][4 * c + 1] = x.y; wv[j][4 * c + 2] = x.z; wv[j][4 * c + 3] = x.w;
+        }
+#pragma unroll
+        for (int c = 0; c < W; ++c) m2 = bf16x2_absmax(m2, wv[j][c]);
+      }
+      norm_factors(warp_max(max(m2 & 0xffffu, m2 >> 16)), down, f);
+      const int e = max(kMinExp, exponent_of(f));
+      f *= pow2i(-e);
+      uint32_t ph[2], pl[2] = {0u, 0u};
+      softmax(acc, tok, kf, e, f, ph, pl);
+#pragma unroll
+      for (int m = 0; m < NS; ++m) {  // channels g GC + 2m, + 1 are pair m of each row
+        const uint32_t y0 = bf16x2_scaled(wv[0][m], down), y1 = bf16x2_scaled(wv[1][m], down);
+        const uint32_t y2 = bf16x2_scaled(wv[2][m], down), y3 = bf16x2_scaled(wv[3][m], down);
+        const uint32_t a0 = prmt(y0, y1, 0x5410u), a1 = prmt(y0, y1, 0x7632u);
+        const uint32_t a2 = prmt(y2, y3, 0x5410u), a3 = prmt(y2, y3, 0x7632u);
+        mma_16816(O[m], a0, a1, a2, a3, ph[0], ph[1]);
+        if constexpr (kF32) mma_16816(O[m], a0, a1, a2, a3, pl[0], pl[1]);
+      }
+    }
+
+    // ---- the unit's records
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], o);
+      if (2 * t + r < rows) {
+        float* rec = part + ((long long)unit * rows_max + 2 * t + r) * (D + 4);
+        if (g == 0) {
+          rec[0] = m_run[r];
+          rec[1] = l_run[r];
+        }
+#pragma unroll
+        for (int m = 0; m < NS; ++m)
+          *reinterpret_cast<float2*>(rec + 4 + g * GC + 2 * m) = make_float2(O[m][r], O[m][2 + r]);
+      }
+    }
+    unit = dynamic ? workers + (int)__shfl_sync(0xffffffffu, (unsigned)nxt, 0) : unit + workers;
+  }
+  if (lane == 0) {  // copies issued and not consumed (a stalled ring): wait for them, bounded, before leaving
+    while (n_consumed < n_loaded) {
+      mbar_wait_bounded(&sm.bar[warp][cstage], cphase, kWaitPolls);
+      if (++cstage == kFStages) {
+        cstage = 0;
+        cphase ^= 1u;
+      }
+      ++n_consumed;
+    }
+  }
+}
+
+// One CTA of 4 warps per (sequence, query, head): the warps take every fourth record of the row's
+// chunks, lanes over channel pairs or quads, and merge through shared memory.
+constexpr int kMWarps = 4;
+template <int D, bool kF32>
+__global__ void __launch_bounds__(kMWarps * 32) few_merge_kernel(KvqView v, QueryArgs a, const float* ws) {
+  constexpr int PER = D / 32;  // channels per lane: 2, 4 or 8
+  __shared__ float o_s[kMWarps][D];
+  __shared__ float m_s[kMWarps], l_s[kMWarps];
+  const int hq = blockIdx.x % v.Hq, x = blockIdx.x / v.Hq, i = x % a.n_q, b = x / a.n_q;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dep_wait();
+  if (i >= query_count(v, a, b)) return;
+  const int* pref = reinterpret_cast<const int*>(ws) + 2;
+  const int nc = (pref[b + 1] - pref[b]) / v.Hkv, h = hq / v.n_rep, row = i * v.n_rep + hq % v.n_rep;
+  const long long rows_max = (long long)a.n_q * v.n_rep, stride = rows_max * (D + 4);
+  const float* rec = reinterpret_cast<const float*>(reinterpret_cast<const char*>(ws) + few_header_bytes(v.batch)) +
+                     ((long long)(pref[b] + h * nc) * rows_max + row) * (D + 4);
+  float m = kMinit, l = 0.f, o[PER];
+#pragma unroll
+  for (int c = 0; c < PER; ++c) o[c] = 0.f;
+  constexpr int kBatch = 4;
+  for (int k0 = warp; k0 < nc; k0 += kMWarps * kBatch) {
+    float rm[kBatch], rl[kBatch], y[kBatch][PER];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int k = k0 + j * kMWarps;
+      rm[j] = kMinit;
+      rl[j] = 0.f;
+#pragma unroll
+      for (int c = 0; c < PER; ++c) y[j][c] = 0.f;
+      if (k < nc) {
+        const float* r = rec + (long long)k * stride;
+        const float2 ml = *reinterpret_cast<const float2*>(r);
+        rm[j] = ml.x;
+        rl[j] = ml.y;
+#pragma unroll
+        for (int c = 0; c < PER; c += 2) {
+          const float2 z = *reinterpret_cast<const float2*>(r + 4 + lane * PER + c);
+          y[j][c] = z.x;
+          y[j][c + 1] = z.y;
+        }
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, rm[j]);
+    const float al = exp2f(m - mn);
+    l *= al;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) o[c] *= al;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const float w = exp2f(rm[j] - mn);
+      l = fmaf(rl[j], w, l);
+#pragma unroll
+      for (int c = 0; c < PER; ++c) o[c] = fmaf(y[j][c], w, o[c]);
+    }
+    m = mn;
+  }
+  if (lane == 0) {
+    m_s[warp] = m;
+    l_s[warp] = l;
+  }
+#pragma unroll
+  for (int c = 0; c < PER; ++c) o_s[warp][lane * PER + c] = o[c];
+  __syncthreads();
+  float M = kMinit, L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMWarps; ++w) M = fmaxf(M, m_s[w]);
+#pragma unroll
+  for (int w = 0; w < kMWarps; ++w) L = fmaf(l_s[w], exp2f(m_s[w] - M), L);
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const long long out0 = (((long long)b * a.n_q + i) * v.Hq + hq) * D;
+  for (int c = threadIdx.x; c < D; c += kMWarps * 32) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMWarps; ++w) s = fmaf(o_s[w][c], exp2f(m_s[w] - M), s);
+    s *= inv;
+    if (kF32) {
+      static_cast<float*>(a.out)[out0 + c] = s;
+    } else {
+      static_cast<__nv_bfloat16*>(a.out)[out0 + c] = __float2bfloat16_rn(s);
+    }
+  }
+}
+
+template <int F, int D, bool kF32>
+kvq_status launch_few_t(const KvqView& v, const QueryArgs& a, float* ws, const CUtensorMap& tmap, cudaStream_t st) {
+  constexpr int kMaxBatch = 4096;  // the plan's prefix in shared memory (query_tc_shape)
+  const auto kern = query_few_kernel<F, D, kF32>;
+  const size_t smem = sizeof(FewSmem<D>) + 1024 + sizeof(int) * (v.batch + 1);
+  int occ = 0;
+  const int slot = kSlotQueryFew + (F * 3 + (D == 64 ? 0 : D == 128 ? 1 : 2)) * 2 + (kF32 ? 1 : 0);
+  const kvq_status so = occupancy_once(slot, kern, kFThreads, sizeof(FewSmem<D>) + 1024 + sizeof(int) * 65,
+                                       sizeof(FewSmem<D>) + 1024 + sizeof(int) * (kMaxBatch + 1), &occ);
+  if (so != KVQ_OK) return so;
+  int grid = num_sms() * occ;
+  if (grid > kMaxUnits / kFWarps) grid = kMaxUnits / kFWarps;
+  // warps take their next unit from a counter where one may come (workers run at unequal speed);
+  // a call too small for that saves the counter's clearing
+  const long long most = (long long)v.batch * v.max_pages * v.P * v.Hkv;
+  const int dynamic = most > (long long)grid * kFWarps * kUnitTokens;
+  if (dynamic && cudaMemsetAsync(reinterpret_cast<char*>(ws) + few_counter_offset(v.batch), 0, 8, st) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  kern<<<grid, kFThreads, smem, st>>>(v, a, ws, dynamic, tmap);
+  if (cudaGetLastError() != cudaSuccess) return KVQ_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)v.batch * a.n_q * v.Hq));
+  cfg.blockDim = dim3(kMWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few_merge_kernel<D, kF32>, v, a, (const float*)ws) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+template <int F, bool kF32>
+kvq_status launch_few_d(const KvqView& v, const QueryArgs& a, float* ws, const CUtensorMap& tmap, cudaStream_t st) {
+  if (v.D == 64) return launch_few_t<F, 64, kF32>(v, a, ws, tmap, st);
+  if (v.D == 128) return launch_few_t<F, 128, kF32>(v, a, ws, tmap, st);
+  return launch_few_t<F, 256, kF32>(v, a, ws, tmap, st);
+}
+
+}  // namespace
+
+size_t query_few_workspace_bytes(const KvqView& v, int batch) {
+  const size_t units = (size_t)kMaxUnits + (size_t)batch * v.Hkv;
+  return few_header_bytes(batch) + units * kFewRows * (v.D + 4) * sizeof(float);
+}
+
+kvq_status launch_query_few(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st) {
+  CUtensorMap tmap;  // the pool as rows of 128 bytes, read in tiles of 16 tokens
+  const cuuint64_t dims[2] = {128, (cuuint64_t)((long long)v.n_pages * v.page_bytes / 128)};
+  const cuuint64_t strides[1] = {128};
+  const cuuint32_t box[2] = {128, (cuuint32_t)(kTile * v.D / 128)};
+  const cuuint32_t estr[2] = {1, 1};
+  if (tensor_map_encoder()(&tmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, v.pages, dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return KVQ_ERR_CUDA;
+  float* w = static_cast<float*>(ws);
+  switch (fmt_index(v.kfmt) * 2 + a.out_f32) {
+    case 0: return launch_few_d<kI8, false>(v, a, w, tmap, st);
+    case 1: return launch_few_d<kI8, true>(v, a, w, tmap, st);
+    case 2: return launch_few_d<kE4, false>(v, a, w, tmap, st);
+    case 3: return launch_few_d<kE4, true>(v, a, w, tmap, st);
+    case 4: return launch_few_d<kE5, false>(v, a, w, tmap, st);
+    default: return launch_few_d<kE5, true>(v, a, w, tmap, st);
+  }
+}
+
+}  // namespace kvq
