@@ -169,11 +169,15 @@ size_t query_workspace_bytes(const KvqView& v, int batch, int n_q) {
   KvqView b = v;
   b.batch = batch;
   if (!query_tc_shape(b)) return 256;
-  return query_few_workspace_bytes(v, batch);
+  if ((long long)n_q * v.n_rep <= kFewRows) return query_few_workspace_bytes(v, batch);
+  return v.D <= 128 ? query_many_workspace_bytes(v, batch, n_q) : 256;
 }
 
 kvq_status launch_query(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st) {
-  if (query_tc_eligible(v) && (long long)a.n_q * v.n_rep <= kFewRows) return launch_query_few(v, a, ws, st);
+  if (query_tc_eligible(v)) {
+    if ((long long)a.n_q * v.n_rep <= kFewRows) return launch_query_few(v, a, ws, st);
+    if (v.D <= 128 && !a.out_f32 && (long long)a.n_q * v.n_rep < (1LL << 30)) return launch_query_many(v, a, ws, st);
+  }
   return launch_query_plain(v, a, st);
 }
 

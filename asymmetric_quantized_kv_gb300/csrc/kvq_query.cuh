@@ -28,9 +28,8 @@ __device__ __forceinline__ int query_end(const QueryArgs& a, int T, int n, int i
   return a.causal ? max(0, T - n + i + 1) : T;
 }
 
-// Kernels of kvq_query_attention.
-enum QueryKernel { kQueryPlain, kQueryFew, kQueryMany };
-constexpr int kFewRows = 8;  // rows of the few-row kernel: one column block of its products
+constexpr int kFewRows = 8;     // rows of the few-row kernel: one column block of its products
+constexpr int kManyGrid = 160;  // CTAs of the many-row kernel at most (one per SM)
 
 bool query_tc_shape(const KvqView& v);      // config only: the tensor-core kernels take it
 bool query_tc_eligible(const KvqView& v);   // and the cache's pool

@@ -24,6 +24,7 @@
 // 4); a second kernel merges a (sequence, kv-head)'s chunks.
 #include <math.h>
 
+#include "kvq_code.cuh"
 #include "kvq_ptx.cuh"
 #include "kvq_query.cuh"
 #include "kvq_tmap.h"
@@ -43,55 +44,11 @@ constexpr int kUnitTokens = 512;    // a warp takes several units only if they a
 constexpr int kMinUnit = 64;        // tokens of the smallest chunk
 constexpr float kLazy = 8.f;
 constexpr float kMinit = -1e30f;
-constexpr int kMinExp = -100;       // smallest value-scale exponent that rides in the softmax
-
-constexpr int fmt_index(int fmt) { return fmt == KVQ_INT8 ? 0 : fmt == KVQ_FP8_E4M3 ? 1 : 2; }
-constexpr int kI8 = 0, kE4 = 1, kE5 = 2;
-
-// The four 8-bit codes of a word as two f16x2 (bytes 0, 1 and 2, 3); exact.
-template <int F>
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (F == kI8) {
-    const uint32_t x = w ^ 0x80808080u;  // code + 128, into the mantissa of 1024
-    lo = hsub2(prmt(x, 0x64646464u, 0x4140u), 0x64806480u);
-    hi = hsub2(prmt(x, 0x64646464u, 0x4342u), 0x64806480u);
-  } else if constexpr (F == kE4) {
-    lo = e4m3x2_to_f16x2(lo16(w));
-    hi = e4m3x2_to_f16x2(hi16(w));
-  } else {  // E5M2 is the upper byte of an f16
-    lo = prmt(w, 0u, 0x1404u);
-    hi = prmt(w, 0u, 0x3424u);
-  }
-}
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
   return r;
-}
-
-// 2^e for e in [-126, 127].
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
-// Exponent of |x| (x finite, not 0; subnormals count as 2^-126).
-__device__ __forceinline__ int exponent_of(float x) { return max(1, (__float_as_int(x) >> 23) & 255) - 127; }
-
-// A bf16 pair times a power of two, as f16x2.
-__device__ __forceinline__ uint32_t bf16x2_scaled(uint32_t u, float s) {
-  return pack_f16x2(__uint_as_float(u << 16) * s, __uint_as_float(u & 0xffff0000u) * s);
-}
-__device__ __forceinline__ uint32_t bf16x2_absmax(uint32_t m, uint32_t u) {  // of magnitudes, as bits
-  const uint32_t a = u & 0x7fff7fffu;
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;\n" : "=r"(r) : "r"(m), "r"(a));
-  return r;
-}
-__device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
-// Factor 2^-k that brings values of largest magnitude `top` (bf16 bits) into [2^8, 2^9), and 2^k.
-__device__ __forceinline__ void norm_factors(uint32_t top, float& down, float& up) {
-  int k = exponent_of(__uint_as_float(top << 16)) - 8;
-  k = top == 0 ? 0 : max(-126, min(k, 119));
-  down = pow2i(-k);
-  up = pow2i(k);
 }
 
 // ---- plan: per sequence ceil(T / C) chunks (over pages and window alike) for each kv-head;

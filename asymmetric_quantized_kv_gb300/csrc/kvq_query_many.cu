@@ -1,0 +1,903 @@
+// Attention of more than 8 rows (query token x query head) per kv-head over a PER_BLOCK
+// cache: prompts and their chunks, longer drafts, cross attention; bf16 sources, head_dim
+// 64 or 128.
+//
+// Mathematics, for a tile of 128 tokens whose 16-token pieces carry a key scale ks and a
+// value scale vs: with code matrices C_k, C_v,
+//   x = (q . C_k) (ks scale log2 e) + log2 vs,   p = 2^(x - M),
+//   l += p / vs,   o += p C_v,   out = o / l,
+// M a running maximum of x, raised when a tile exceeds it by 2^8.  The scales cost the
+// softmax nothing (one multiply-add per element, as without them) and p stays an f16 number
+// whatever they are.  Codes are exact in f16, and a bf16 query row is after scaling by a
+// power of two; p is rounded to f16 once (2^-11 against the output's own 2^-8).
+//
+// What bounds it: the tensor cores and the softmax's exponentials for many rows, the codes'
+// traffic for few.  One persistent CTA per SM of 14 warps, each with one task:
+//   12     copies the tiles' codes into shared memory (bulk copies, a page each) and reads
+//          the scales;
+//   8-11   turn codes (and the window's bf16 rows) into f16 tiles with the 128-byte swizzle;
+//   13     issues the products: S = Q K^T from shared memory, O += P V with P in tensor
+//          memory;
+//   0-3, 4-7  two streams of 128 rows: a thread owns a row, reads its S from tensor memory,
+//          writes P over it and rescales O.
+// The two streams' products alternate, so that one runs while the other's softmax does.
+// With more than 128 rows a unit is 256 rows, one half a stream, over the same tiles;
+// with fewer the streams take every other tile of one half and are joined at the end.
+//
+// Work split: units (sequence, kv-head, 256 or 128 rows) laid end to end as tiles; every CTA
+// takes an equal run of them, whatever the lengths are, so that all SMs finish together.
+// A unit cut by such a boundary leaves fp32 partial records, which a second kernel merges.
+#include <math.h>
+
+#include "kvq_code.cuh"
+#include "kvq_query.cuh"
+#include "kvq_tcgen05.cuh"
+
+namespace kvq {
+namespace {
+
+using namespace ptx;
+
+constexpr int kRows = 128;    // rows of a stream
+constexpr int kTok = 128;     // tokens of a tile
+constexpr int kPieces = kTok / 16;
+constexpr int kMThreads = 14 * 32;
+constexpr int kConvWarps = 4, kConv0 = 8, kLoadWarp = 12, kMmaWarp = 13;
+constexpr int kSlots = 8;     // tiles whose scales are kept
+constexpr float kLazyM = 8.f;
+constexpr float kMinitM = -1e30f;
+
+// A CTA's partial records: that of its first unit and that of its last, where they are cut.
+struct RecHeader {
+  int used;            // the record holds a cut unit's partial
+  int b, h, qt;        // the unit
+  int begins, ends;    // its first / last tile is in it
+  int pad[2];
+};
+
+// Shared memory (D the head_dim): f16 tiles of Q (one per stream), K and V (two stages each), then the raw
+// codes of one tile of keys and of values, then the small things.
+template <int D>
+struct Lay {
+  static constexpr int kTileB = 128 * D * 2;
+  static constexpr int kRawB = 128 * D;
+  // the second Q tile also carries the join of two streams: 32 channels and the statistics of 128 rows
+  static constexpr int kQ1B = kTileB > 17 * 1024 ? kTileB : 17 * 1024;
+  static constexpr int kQ = 0, kK = kTileB + kQ1B, kV = kK + 2 * kTileB, kRawK = kV + 2 * kTileB, kRawV = kRawK + kRawB;
+  static constexpr int kMisc = kRawV + kRawB;
+};
+
+struct Misc {
+  float sk[kSlots][kPieces];    // key scale of a piece
+  float lv[kSlots][kPieces];    // log2 of the value scale (-inf: the piece has no tokens to see)
+  float iv[kSlots][kPieces];    // 1 / value scale
+  uint32_t skip_k[kSlots];      // pieces to fill with zeros
+  uint32_t skip_v[kSlots];
+  uint64_t raw_k_full, raw_v_full, raw_k_empty, raw_v_empty;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2], o_full[2], q_full[2];
+  uint32_t tmem;
+  int abort;
+  int start_b, start_h, start_qt, start_tile;
+  unsigned long long total;
+};
+
+// ---- units
+
+struct Walk {  // one unit, and the CTA's place in it
+  int b, h, qt;
+  int T, nq, n, rows, nqt;  // of sequence b
+  int tiles;                // of the unit
+};
+
+__device__ __forceinline__ int unit_tiles(const KvqView& v, const QueryArgs& a, int T, int n, int rows, int qt, int RT) {
+  const int last = min(rows, (qt + 1) * RT) - 1;
+  return max(1, (query_end(a, T, n, last / v.n_rep) + kTok - 1) / kTok);
+}
+
+__device__ __forceinline__ void load_sequence(const KvqView& v, const QueryArgs& a, int RT, Walk& w) {
+  w.T = seq_tokens(v, w.b);
+  w.nq = n_quantized(w.T, v.R);
+  w.n = query_count(v, a, w.b);
+  w.rows = w.n * v.n_rep;
+  w.nqt = (w.rows + RT - 1) / RT;
+}
+
+__device__ __forceinline__ void next_unit(const KvqView& v, const QueryArgs& a, int RT, Walk& w) {
+  if (++w.qt == w.nqt) {
+    w.qt = 0;
+    if (++w.h == v.Hkv) {
+      w.h = 0;
+      do {
+        ++w.b;
+        load_sequence(v, a, RT, w);
+      } while (w.nqt == 0);  // units remain, so a sequence with rows follows
+    }
+  }
+  w.tiles = unit_tiles(v, a, w.T, w.n, w.rows, w.qt, RT);
+}
+
+// Bounded wait of a task; after a wait that gave up nothing more is waited for.
+struct Waiter {
+  Misc& m;
+  int32_t* status;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    for (uint32_t i = 0; i < kWaitPolls; ++i) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (*reinterpret_cast<volatile int*>(&m.abort)) return false;
+    }
+    *reinterpret_cast<volatile int*>(&m.abort) = 1;
+    atomicOr(status, KVQ_DEV_TIMEOUT);
+    return false;
+  }
+};
+
+// Byte offset of 16-byte chunk c (of 8 f16) of row r in a tile of 128-row panels of 64 channels.
+__device__ __forceinline__ uint32_t tile_chunk(int r, int c) {
+  return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// ---- converter: 16 tokens of a raw tile -> f16 (whole warp)
+template <int F, int D>
+__device__ __forceinline__ void convert_piece(const uint8_t* raw, uint8_t* dst, int piece, int lane) {
+  constexpr int CPR = D / 16;         // 16-code chunks per row
+  constexpr int RPI = 32 / CPR;       // rows per pass
+#pragma unroll
+  for (int i = 0; i < 16 / RPI; ++i) {
+    const int r = 16 * piece + i * RPI + lane / CPR, c = lane % CPR;
+    uint4 x = *reinterpret_cast<const uint4*>(raw + r * D + 16 * c);
+    // the upper panel's lanes write their second half first: a store's eight lanes then meet 8 chunks
+    const int sw = D == 128 ? c >> 2 : 0;
+    if (sw) x = make_uint4(x.z, x.w, x.x, x.y);
+    uint32_t f[8];
+    codes_to_f16<F>(x.x, f[0], f[1]);
+    codes_to_f16<F>(x.y, f[2], f[3]);
+    codes_to_f16<F>(x.z, f[4], f[5]);
+    codes_to_f16<F>(x.w, f[6], f[7]);
+    *reinterpret_cast<uint4*>(dst + tile_chunk(r, 2 * c + sw)) = make_uint4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<uint4*>(dst + tile_chunk(r, 2 * c + 1 - sw)) = make_uint4(f[4], f[5], f[6], f[7]);
+  }
+}
+template <int D>
+__device__ __forceinline__ void zero_piece(uint8_t* dst, int piece, int lane) {
+  for (int i = lane; i < 16 * (D / 8); i += 32)
+    *reinterpret_cast<uint4*>(dst + tile_chunk(16 * piece + i / (D / 8), i % (D / 8))) = make_uint4(0u, 0u, 0u, 0u);
+}
+// 16 window rows from token tok (those before T; zeros behind), scaled by 2^-k with k their common exponent.
+// write == false: only the exponent.
+template <int D>
+__device__ __forceinline__ int window_piece(const void* win, const KvqView& v, int b, int h, int tok, int T, int nq, uint8_t* dst,
+                                            int piece, int lane, bool write) {
+  constexpr int CPR = D / 8, RPI = 32 / CPR, N = 16 / RPI;
+  uint4 x[N];
+  uint32_t m2 = 0u;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int r = i * RPI + lane / CPR, c = lane % CPR;
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tok + r < T)
+      x[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(win) +
+                                             (((long long)b * v.R + (tok + r - nq)) * v.Hkv + h) * D + 8 * c);
+    m2 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(m2, x[i].x), x[i].y), x[i].z), x[i].w);
+  }
+  const int k = max(kMinExp, norm_exponent(warp_max(max(m2 & 0xffffu, m2 >> 16))));
+  if (write) {
+    const float down = pow2i(-k);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = i * RPI + lane / CPR, c = lane % CPR;
+      *reinterpret_cast<uint4*>(dst + tile_chunk(16 * piece + r, c)) =
+          make_uint4(bf16x2_scaled(x[i].x, down), bf16x2_scaled(x[i].y, down), bf16x2_scaled(x[i].z, down),
+                     bf16x2_scaled(x[i].w, down));
+    }
+  }
+  return k;
+}
+
+// Arrive once per warp on a barrier that hands shared memory written here to the tensor cores.
+__device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
+  fence_proxy_async();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+__host__ __device__ inline size_t many_rec_bytes(int D, int RT) { return (size_t)RT * (D + 4) * sizeof(float); }
+__host__ __device__ inline size_t many_header_bytes(int grid) { return ((size_t)grid * 2 * sizeof(RecHeader) + 255) / 256 * 256; }
+
+template <int F, int D>
+__global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, QueryArgs a, unsigned char* ws, int RT) {
+  using L = Lay<D>;
+  extern __shared__ unsigned char dyn_raw[];
+  unsigned char* sm = dyn_raw + ((1024 - (smem_u32(dyn_raw) & 1023)) & 1023);
+  Misc& mi = *reinterpret_cast<Misc*>(sm + L::kMisc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool two = RT == 2 * kRows;  // a stream per half of the unit; else both over one half
+  grid_dep_launch();
+
+  // ---- the CTA's run of tiles
+  unsigned long long* wb = reinterpret_cast<unsigned long long*>(sm);  // tiles of a kv-head of each sequence
+  if (threadIdx.x == 0) {
+    mi.total = 0ull;
+    mi.abort = 0;
+  }
+  __syncthreads();
+  {
+    // a thread a sequence, or, for few of them, a warp
+    const bool warps = v.batch < kMThreads / 32;
+    unsigned long long mine = 0;
+    for (int b = warps ? warp : threadIdx.x; b < v.batch; b += warps ? kMThreads / 32 : kMThreads) {
+      Walk w;
+      w.b = b;
+      load_sequence(v, a, RT, w);
+      unsigned long long s = 0;
+      for (int qt = warps ? lane : 0; qt < w.nqt; qt += warps ? 32 : 1) s += unit_tiles(v, a, w.T, w.n, w.rows, qt, RT);
+      if (warps) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      }
+      if (!warps || lane == 0) {
+        wb[b] = s;
+        mine += s;
+      }
+    }
+    if (mine) atomicAdd(&mi.total, mine);
+  }
+  __syncthreads();
+  const unsigned long long total = mi.total * v.Hkv;
+  // no CTA between two others is left without a tile: the merge walks from one to the next
+  const unsigned long long runs = min((unsigned long long)gridDim.x, total), me = blockIdx.x;
+  const unsigned long long w0 = me < runs ? total * me / runs : 0ull, w1 = me < runs ? total * (me + 1) / runs : 0ull;
+  RecHeader* hdr = reinterpret_cast<RecHeader*>(ws) + 2 * blockIdx.x;
+  if (threadIdx.x < 2) hdr[threadIdx.x].used = 0;
+  if (w0 == w1) return;
+  if (warp == 0) {
+    unsigned long long left = w0;
+    int b = 0;
+    for (int b0 = 0; b0 < v.batch; b0 += 32) {  // the sequence that holds tile w0
+      const unsigned long long x = b0 + lane < v.batch ? wb[b0 + lane] * v.Hkv : 0ull;
+      unsigned long long incl = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, incl > left);
+      if (hit) {
+        const int k = __ffs(hit) - 1;
+        b = b0 + k;
+        left -= __shfl_sync(0xffffffffu, incl - x, k);
+        break;
+      }
+      left -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    Walk w;
+    w.b = b;
+    load_sequence(v, a, RT, w);
+    const int h = (int)(left / wb[b]);
+    left -= (unsigned long long)h * wb[b];
+    int qt = 0;
+    for (int q0 = 0; q0 < w.nqt; q0 += 32) {
+      const unsigned x = q0 + lane < w.nqt ? unit_tiles(v, a, w.T, w.n, w.rows, q0 + lane, RT) : 0;
+      unsigned incl = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, incl > left);
+      if (hit) {
+        const int k = __ffs(hit) - 1;
+        qt = q0 + k;
+        left -= __shfl_sync(0xffffffffu, incl - x, k);
+        break;
+      }
+      left -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      mi.start_b = b;
+      mi.start_h = h;
+      mi.start_qt = qt;
+      mi.start_tile = (int)left;
+    }
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(&mi.tmem, 512);
+    if (lane == 0) {
+      mbar_init(&mi.raw_k_full, 1);
+      mbar_init(&mi.raw_v_full, 1);
+      mbar_init(&mi.raw_k_empty, kConvWarps);
+      mbar_init(&mi.raw_v_empty, kConvWarps);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&mi.k_full[i], kConvWarps);
+        mbar_init(&mi.k_empty[i], 1);
+        mbar_init(&mi.v_full[i], kConvWarps);
+        mbar_init(&mi.v_empty[i], 1);
+        mbar_init(&mi.s_full[i], 1);
+        mbar_init(&mi.p_full[i], kRows);
+        mbar_init(&mi.o_full[i], 1);
+        mbar_init(&mi.q_full[i], kRows / 32);
+      }
+      fence_mbar_init();
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = mi.tmem;
+  const Waiter wait{mi, v.status};
+
+  Walk w;
+  w.b = mi.start_b;
+  w.h = mi.start_h;
+  w.qt = mi.start_qt;
+  load_sequence(v, a, RT, w);
+  w.tiles = unit_tiles(v, a, w.T, w.n, w.rows, w.qt, RT);
+  int j0 = mi.start_tile;
+  unsigned long long left = w1 - w0;
+
+  // Every task walks the same segments: tiles [j0, j1) of unit w.
+  if (warp == kLoadWarp) {
+    uint32_t it = 0;  // tiles so far: phase of the single raw stage, slot of the scales
+    bool ok = true;
+    for (;;) {
+      const int j1 = (int)min((unsigned long long)w.tiles, j0 + left);
+      const int32_t* bt = v.block_table + (long long)w.b * v.max_pages;
+      const long long head_off = (long long)w.h * v.head_bytes;
+      for (int j = j0; j < j1 && ok; ++j, ++it) {
+        const int t0 = j * kTok, t1 = min(t0 + kTok, w.nq);  // tokens from pages
+        const int slot = it % kSlots;
+        // lane i: the tile's i-th page (at most 9)
+        const int pg = t0 / v.P + lane;
+        const int p0 = (int)max((long long)t0, min((long long)t1, (long long)pg * v.P));
+        const int p1 = (int)min((long long)t1, ((long long)pg + 1) * v.P);
+        int pid = -1;
+        const bool has = p0 < p1;
+        if (has) pid = bt[pg];
+        const bool good = has && pid >= 0 && pid < v.n_pages;
+        const uint8_t* src = v.pages + (long long)(good ? pid : 0) * v.page_bytes + head_off + (p0 - (long long)pg * v.P) * D;
+        const uint32_t bytes = good ? (uint32_t)(p1 - p0) * D : 0u;
+        const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
+        // pieces whose page is missing
+        uint32_t bad = has && !good ? ((1u << ((p1 - t0) / 16)) - 1u) & ~((1u << ((p0 - t0) / 16)) - 1u) : 0u;
+        bad = __reduce_or_sync(0xffffffffu, bad);
+        ok = wait(&mi.raw_k_empty, (it & 1) ^ 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0 && sum) asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(&mi.raw_k_full)), "r"(sum) : "memory");
+        __syncwarp();
+        if (bytes) bulk_g2s(sm + L::kRawK + (p0 - t0) * D, src, bytes, &mi.raw_k_full);
+        // scales, lane i for piece i
+        float ks = 0.f, lv = -INFINITY, iv = 0.f;
+        bool drop_v = false;
+        if (lane < kPieces) {
+          const int t = t0 + 16 * lane;
+          if (t < t1) {
+            const int g0 = t / v.kgroup * v.kgroup, gp = bt[g0 / v.P];
+            if (gp >= 0 && gp < v.n_pages && !((bad >> lane) & 1u)) {
+              const uint8_t* hb = v.pages + (long long)gp * v.page_bytes + head_off;
+              const int s = (g0 % v.P) / v.kgroup;
+              ks = load_meta(hb + v.off_km, s, v.meta16);
+              const float vs = load_meta(hb + v.off_vm, s, v.meta16);
+              drop_v = !(vs >= pow2i(kMinExp));  // values below 2^-91: read as 0, weight 1
+              lv = drop_v ? 0.f : __log2f(vs);
+              iv = drop_v ? 1.f : __frcp_rn(vs);
+            } else {
+              bad |= 1u << lane;
+            }
+          }
+          mi.sk[slot][lane] = ks;
+          mi.lv[slot][lane] = lv;
+          mi.iv[slot][lane] = iv;
+        }
+        bad = __reduce_or_sync(0xffffffffu, bad);
+        const uint32_t dv = __ballot_sync(0xffffffffu, drop_v);
+        if (lane == 0) {
+          mi.skip_k[slot] = bad;
+          mi.skip_v[slot] = bad | dv;
+          if (bad) atomicOr(v.status, KVQ_DEV_BAD_PAGE);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mi.raw_k_full);
+        ok = wait(&mi.raw_v_empty, (it & 1) ^ 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&mi.raw_v_full, sum);
+        __syncwarp();
+        if (bytes) bulk_g2s(sm + L::kRawV + (p0 - t0) * D, src + v.off_vc, bytes, &mi.raw_v_full);
+      }
+      left -= j1 - j0;
+      if (!ok || left == 0) break;
+      j0 = 0;
+      next_unit(v, a, RT, w);
+    }
+  } else if (warp >= kConv0 && warp < kConv0 + kConvWarps) {
+    uint32_t it = 0;
+    bool ok = true;
+    for (;;) {
+      const int j1 = (int)min((unsigned long long)w.tiles, j0 + left);
+      for (int j = j0; j < j1 && ok; ++j, ++it) {
+        const int t0 = j * kTok, slot = it % kSlots, st = it & 1;
+        const uint32_t ph = (it >> 1) & 1;
+        uint8_t* kd = sm + L::kK + st * L::kTileB;
+        uint8_t* vd = sm + L::kV + st * L::kTileB;
+        ok = wait(&mi.raw_k_full, it & 1) && wait(&mi.k_empty[st], ph ^ 1);
+        if (!ok) break;
+        const uint32_t skip_k = mi.skip_k[slot], skip_v = mi.skip_v[slot];
+#pragma unroll
+        for (int i = 0; i < kPieces / kConvWarps; ++i) {
+          const int piece = (warp - kConv0) + i * kConvWarps, tok = t0 + 16 * piece;
+          if (tok >= w.T || ((skip_k >> piece) & 1u)) {
+            zero_piece<D>(kd, piece, lane);
+          } else if (tok < w.nq) {
+            convert_piece<F, D>(sm + L::kRawK, kd, piece, lane);
+          } else {
+            const int kk = window_piece<D>(v.k_win, v, w.b, w.h, tok, w.T, w.nq, kd, piece, lane, true);
+            const int kv = window_piece<D>(v.v_win, v, w.b, w.h, tok, w.T, w.nq, vd, piece, lane, false);
+            if (lane == 0) {
+              mi.sk[slot][piece] = pow2i(kk);
+              mi.lv[slot][piece] = (float)kv;
+              mi.iv[slot][piece] = pow2i(-kv);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mi.raw_k_empty);
+        hand_over(&mi.k_full[st], lane);
+        ok = wait(&mi.raw_v_full, it & 1) && wait(&mi.v_empty[st], ph ^ 1);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < kPieces / kConvWarps; ++i) {
+          const int piece = (warp - kConv0) + i * kConvWarps, tok = t0 + 16 * piece;
+          if (tok >= w.T || (tok < w.nq && ((skip_v >> piece) & 1u))) {
+            zero_piece<D>(vd, piece, lane);
+          } else if (tok < w.nq) {
+            convert_piece<F, D>(sm + L::kRawV, vd, piece, lane);
+          } else {
+            window_piece<D>(v.v_win, v, w.b, w.h, tok, w.T, w.nq, vd, piece, lane, true);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mi.raw_v_empty);
+        hand_over(&mi.v_full[st], lane);
+      }
+      left -= j1 - j0;
+      if (!ok || left == 0) break;
+      j0 = 0;
+      next_unit(v, a, RT, w);
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      constexpr uint32_t id_s = tc::f16_idesc(128, 128, false), id_o = tc::f16_idesc(128, D, true);
+      constexpr uint32_t kPanel = 128 * 128;
+      uint32_t it0 = 0;                     // tiles before this segment
+      uint32_t np[2] = {0, 0}, nseg = 0;    // softmax hand-overs of each stream, segments
+      bool ok = true;
+      auto s_mma = [&](int s, uint32_t it) {  // S_s = Q K^T of the CTA's tile `it`
+        const uint32_t q = smem_u32(sm + L::kQ + (two ? s : 0) * L::kTileB), k = smem_u32(sm + L::kK + (it & 1) * L::kTileB);
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const uint32_t off = (x >> 2) * kPanel + (x & 3) * 32;
+          tc::mma_ss(tmem + 128 * s, tc::smem_desc(q + off, 16), tc::smem_desc(k + off, 16), id_s, x > 0);
+        }
+        tc::commit(&mi.s_full[s]);
+      };
+      auto o_mma = [&](int s, uint32_t it, bool first) {  // O_s (+)= P V
+        const uint32_t vt = smem_u32(sm + L::kV + (it & 1) * L::kTileB);
+#pragma unroll
+        for (int x = 0; x < kTok / 16; ++x)
+          tc::mma_ts(tmem + 256 + D * s, tmem + 128 * s + 8 * x, tc::smem_desc(vt + x * 2048, kPanel), id_o, !first || x > 0);
+      };
+      auto k_ready = [&](uint32_t it) { return wait(&mi.k_full[it & 1], (it >> 1) & 1); };
+      auto v_ready = [&](uint32_t it) { return wait(&mi.v_full[it & 1], (it >> 1) & 1); };
+      auto p_ready = [&](int s) {
+        const bool r = wait(&mi.p_full[s], np[s] & 1);
+        ++np[s];
+        tc::fence_after();
+        return r;
+      };
+      for (;;) {
+        const int j1 = (int)min((unsigned long long)w.tiles, j0 + left), nt = j1 - j0;
+        ok = wait(&mi.q_full[0], nseg & 1) && (!two || wait(&mi.q_full[1], nseg & 1));
+        ++nseg;
+        tc::fence_after();
+        if (two) {
+          if (ok && (ok = k_ready(it0))) {
+            tc::fence_after();
+            s_mma(0, it0);
+            s_mma(1, it0);
+            tc::commit(&mi.k_empty[it0 & 1]);
+          }
+          for (int i = 0; i < nt && ok; ++i) {
+            const uint32_t it = it0 + i;
+            const bool more = i + 1 < nt;
+            if (!(ok = p_ready(0) && v_ready(it))) break;
+            tc::fence_after();
+            o_mma(0, it, i == 0);
+            if (more) {
+              if (!(ok = k_ready(it + 1))) break;
+              tc::fence_after();
+              s_mma(0, it + 1);
+            } else {
+              tc::commit(&mi.o_full[0]);
+            }
+            if (!(ok = p_ready(1))) break;
+            o_mma(1, it, i == 0);
+            tc::commit(&mi.v_empty[it & 1]);
+            if (more) {
+              s_mma(1, it + 1);
+              tc::commit(&mi.k_empty[(it + 1) & 1]);
+            } else {
+              tc::commit(&mi.o_full[1]);
+            }
+          }
+        } else {  // tile i belongs to stream i & 1
+          for (int i = 0; i < min(2, nt) && ok; ++i) {
+            if (!(ok = k_ready(it0 + i))) break;
+            tc::fence_after();
+            s_mma(i, it0 + i);
+            tc::commit(&mi.k_empty[(it0 + i) & 1]);
+          }
+          for (int i = 0; i < nt && ok; ++i) {
+            const uint32_t it = it0 + i;
+            const int s = i & 1;
+            if (!(ok = p_ready(s) && v_ready(it))) break;
+            tc::fence_after();
+            o_mma(s, it, i < 2);
+            tc::commit(&mi.v_empty[it & 1]);
+            if (i + 2 < nt) {
+              if (!(ok = k_ready(it + 2))) break;
+              tc::fence_after();
+              s_mma(s, it + 2);
+              tc::commit(&mi.k_empty[it & 1]);
+            } else {
+              tc::commit(&mi.o_full[s]);
+            }
+          }
+        }
+        it0 += nt;
+        left -= nt;
+        if (!ok || left == 0) break;
+        j0 = 0;
+        next_unit(v, a, RT, w);
+      }
+    }
+    __syncwarp();
+  } else {  // ---- softmax streams
+    const int s = warp >> 2, row_l = threadIdx.x & (kRows - 1);
+    const uint32_t lane_off = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, in the address's upper half
+    const uint32_t tS = tmem + lane_off + 128 * s, tO = tmem + lane_off + 256 + D * s;
+    uint32_t ns = 0, nseg = 0, it0 = 0, no = 0;
+    bool ok = true;
+    for (;;) {
+      const int j1 = (int)min((unsigned long long)w.tiles, j0 + left), nt = j1 - j0;
+      const int row = w.qt * RT + (two ? s * kRows : 0) + row_l;  // of the sequence and kv-head
+      const bool live = row < w.rows;
+      const int qi = live ? row / v.n_rep : 0;
+      const long long q_elem = (((long long)w.b * a.n_q + qi) * v.Hq + w.h * v.n_rep + (live ? row % v.n_rep : 0)) * D;
+      // ---- this thread's query row into f16, K-major; rows past the last are zeros
+      float fct;
+      {
+        const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + q_elem);
+        uint32_t m2 = 0u;
+        if (live) {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 x = qp[c];
+            m2 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(m2, x.x), x.y), x.z), x.w);
+          }
+        }
+        float down, up;
+        norm_factors(max(m2 & 0xffffu, m2 >> 16), down, up);
+        fct = up * a.scale * 1.4426950408889634f;
+        if (two || s == 0) {
+          uint8_t* qd = sm + L::kQ + (two ? s : 0) * L::kTileB;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (live) x = qp[c];
+            *reinterpret_cast<uint4*>(qd + tile_chunk(row_l, c)) =
+                make_uint4(bf16x2_scaled(x.x, down), bf16x2_scaled(x.y, down), bf16x2_scaled(x.z, down), bf16x2_scaled(x.w, down));
+          }
+          hand_over(&mi.q_full[s], lane);
+        }
+      }
+      const int end = live ? query_end(a, w.T, w.n, qi) : 0x3FFFFFFF;  // rows past the last: never masked, never written
+      const int warp_end = __reduce_min_sync(0xffffffffu, end);
+      float M = kMinitM, l = 0.f;
+      bool any = false;  // this stream has had a tile of this segment
+      for (int i = two ? 0 : s; i < nt && ok; i += two ? 1 : 2) {
+        const int t0 = (j0 + i) * kTok, slot = (it0 + i) % kSlots;
+        ok = wait(&mi.s_full[s], ns & 1);
+        ++ns;
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after();
+        const bool masked = t0 + kTok > warp_end;
+        const int lim = end - t0;
+        // ---- maximum
+        float mx = -INFINITY;
+        {
+          uint32_t r[2][32];
+          tc::tmem_ld32(tS, r[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tc::wait_ld(r[c & 1]);
+            if (c < 3) tc::tmem_ld32(tS + 32 * (c + 1), r[(c + 1) & 1]);
+            if (masked) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (32 * c + e >= lim) r[c & 1][e] = 0xff800000u;  // -inf
+            }
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              float m4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) m4[e] = __uint_as_float(r[c & 1][16 * hf + e]);
+#pragma unroll
+              for (int e = 4; e < 16; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(r[c & 1][16 * hf + e]));
+              const float m16 = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+              // an all-masked piece times a zero scale is NaN, which fmaxf passes over
+              mx = fmaxf(mx, fmaf(m16, mi.sk[slot][2 * c + hf] * fct, mi.lv[slot][2 * c + hf]));
+            }
+          }
+        }
+        if (__any_sync(0xffffffffu, mx > M + kLazyM)) {
+          const float mn = fmaxf(M, mx), al = ex2(M - mn);
+          M = mn;
+          l *= al;
+          if (any) {
+            uint32_t r[32];
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              tc::tmem_ld32(tO + c, r);
+              tc::wait_ld(r);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * al);
+              tc::tmem_st32(tO + c, r);
+            }
+          }
+        }
+        any = true;
+        // ---- weights, over the logits' columns
+        {
+          uint32_t r[2][32];
+          tc::tmem_ld32(tS, r[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tc::wait_ld(r[c & 1]);
+            if (c < 3) tc::tmem_ld32(tS + 32 * (c + 1), r[(c + 1) & 1]);
+            uint32_t pk[16];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const float cc = mi.sk[slot][2 * c + hf] * fct, bb = mi.lv[slot][2 * c + hf] - M;
+              float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int k = 16 * hf + 2 * e;
+                float2 x = fma2(make_float2(__uint_as_float(r[c & 1][k]), __uint_as_float(r[c & 1][k + 1])),
+                                make_float2(cc, cc), make_float2(bb, bb));
+                if (masked) {
+                  if (32 * c + k >= lim) x.x = -INFINITY;
+                  if (32 * c + k + 1 >= lim) x.y = -INFINITY;
+                }
+                const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                sum = add2(sum, p);
+                pk[8 * hf + e] = pack_f16x2(p.x, p.y);
+              }
+              l = fmaf(sum.x + sum.y, mi.iv[slot][2 * c + hf], l);
+            }
+            tc::tmem_st16(tS + 16 * c, pk);
+          }
+        }
+        tc::wait_st();
+        tc::fence_before();
+        mbar_arrive(&mi.p_full[s]);
+      }
+      // ---- the segment's output
+      if (ok && any) {
+        ok = wait(&mi.o_full[s], no & 1);
+        ++no;
+        tc::fence_after();
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!two) {
+        // stream 1's (M, l, O) through the second half's place in shared memory, 32 channels at a time
+        float* ex = reinterpret_cast<float*>(sm + L::kQ + L::kTileB);
+        float* ml = ex + 32 * kRows;
+        float a1 = 0.f;
+        if (s == 1) {
+          ml[row_l] = any ? M : kMinitM;
+          ml[kRows + row_l] = any ? l : 0.f;
+        }
+        named_bar_sync(1, 2 * kRows);
+        float a0 = 1.f;
+        if (s == 0) {
+          const float M1 = ml[row_l], l1 = ml[kRows + row_l], mn = fmaxf(M, M1);
+          a0 = ex2(M - mn);
+          a1 = ex2(M1 - mn);
+          M = mn;
+          l = l * a0 + l1 * a1;
+        }
+        const bool have1 = nt > 1;
+        if (have1) {
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t r[32];
+            tc::tmem_ld32(tO + c, r);
+            tc::wait_ld(r);
+            if (s == 1) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ex[e * kRows + row_l] = __uint_as_float(r[e]);
+            }
+            named_bar_sync(1, 2 * kRows);
+            if (s == 0) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                r[e] = __float_as_uint(__uint_as_float(r[e]) * a0 + ex[e * kRows + row_l] * a1);
+              tc::tmem_st32(tO + c, r);
+              tc::wait_st();
+            }
+            named_bar_sync(1, 2 * kRows);
+          }
+        }
+      }
+      const bool begins = j0 == 0, ends = j1 == w.tiles;
+      if (ok && (two || s == 0)) {
+        const bool first = it0 == 0;
+        const bool whole = begins && ends;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int rs = (two ? s * kRows : 0) + row_l;
+        float* rec = reinterpret_cast<float*>(ws + many_header_bytes(gridDim.x) +
+                                              (2ull * blockIdx.x + (first ? 0 : 1)) * many_rec_bytes(D, RT)) +
+                     (long long)rs * (D + 4);
+        if (!whole) {
+          if (threadIdx.x == 0) hdr[first ? 0 : 1] = RecHeader{1, w.b, w.h, w.qt, begins, ends, {0, 0}};
+          if (live) *reinterpret_cast<float4*>(rec) = make_float4(M, l, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t r[32];
+          __syncwarp();
+          tc::tmem_ld32(tO + c, r);
+          tc::wait_ld(r);
+          if (!live) {
+          } else if (whole) {
+            uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + q_elem + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t y[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 z = __floats2bfloat162_rn(__uint_as_float(r[8 * e + 2 * k]) * inv,
+                                                               __uint_as_float(r[8 * e + 2 * k + 1]) * inv);
+                y[k] = *reinterpret_cast<const uint32_t*>(&z);
+              }
+              op[e] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          } else {
+            uint4* op = reinterpret_cast<uint4*>(rec + 4 + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) op[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+          }
+        }
+      }
+      tc::fence_before();
+      it0 += nt;
+      left -= nt;
+      ++nseg;
+      if (!ok || left == 0) break;
+      j0 = 0;
+      next_unit(v, a, RT, w);
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (mi.abort) {  // a wait gave up: copies and products in flight end (microseconds) before the memory is released
+    for (int i = 0; i < 4096; ++i) __nanosleep(250);
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+// Merge of the cut units: the blocks of CTA x take the unit whose first tile is in a record of x and whose
+// last is not, a warp a row; its records are x's and the first ones of the CTAs that follow.
+constexpr int kMergeRows = 16;
+template <int D>
+__global__ void __launch_bounds__(kMergeRows * 32) many_merge_kernel(KvqView v, QueryArgs a, const unsigned char* ws, int RT, int grid) {
+  constexpr int PER = D / 32;
+  const int per = RT / kMergeRows, x = blockIdx.x / per, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rs = blockIdx.x % per * kMergeRows + warp;
+  grid_dep_wait();
+  const RecHeader* hdr = reinterpret_cast<const RecHeader*>(ws);
+  int at = -1;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const RecHeader& r = hdr[2 * x + k];
+    if (r.used && r.begins && !r.ends) at = 2 * x + k;
+  }
+  if (at < 0) return;
+  const RecHeader u = hdr[at];
+  const int row = u.qt * RT + rs;
+  if (row >= query_count(v, a, u.b) * v.n_rep) return;
+  float m = kMinitM, l = 0.f, o[PER];
+#pragma unroll
+  for (int c = 0; c < PER; ++c) o[c] = 0.f;
+  for (int k = at;;) {
+    const float* rec =
+        reinterpret_cast<const float*>(ws + many_header_bytes(grid) + (unsigned long long)k * many_rec_bytes(D, RT)) + (long long)rs * (D + 4);
+    const float2 ml = *reinterpret_cast<const float2*>(rec);
+    float y[PER];
+#pragma unroll
+    for (int c = 0; c < PER; c += 2) {
+      const float2 z = *reinterpret_cast<const float2*>(rec + 4 + lane * PER + c);
+      y[c] = z.x;
+      y[c + 1] = z.y;
+    }
+    const float mn = fmaxf(m, ml.x), a0 = exp2f(m - mn), a1 = exp2f(ml.x - mn);
+    m = mn;
+    l = l * a0 + ml.y * a1;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) o[c] = o[c] * a0 + y[c] * a1;
+    if (hdr[k].ends) break;
+    k = (k / 2 + 1) * 2;  // the next CTA's first record
+    if (k >= 2 * grid || !hdr[k].used) break;  // a run that gave up
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const long long e = (((long long)u.b * a.n_q + row / v.n_rep) * v.Hq + u.h * v.n_rep + row % v.n_rep) * D + lane * PER;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + e);
+#pragma unroll
+  for (int c = 0; c < PER; c += 2) {
+    const __nv_bfloat162 z = __floats2bfloat162_rn(o[c] * inv, o[c + 1] * inv);
+    out[c / 2] = *reinterpret_cast<const uint32_t*>(&z);
+  }
+}
+
+template <int F, int D>
+kvq_status launch_many_t(const KvqView& v, const QueryArgs& a, unsigned char* ws, cudaStream_t st) {
+  const int RT = (long long)a.n_q * v.n_rep > kRows ? 2 * kRows : kRows;
+  const auto kern = query_many_kernel<F, D>;
+  // at least what keeps a second CTA off the SM: each takes all of its tensor memory
+  constexpr size_t need = Lay<D>::kMisc + sizeof(Misc) + 1024, smem = need > 120 * 1024 ? need : 120 * 1024;
+  static_assert(smem <= 232448, "shared memory of an SM");
+  const kvq_status ss = ensure_dynamic_smem(kSlotQueryTc + F * 2 + (D == 64 ? 0 : 1), kern, smem);
+  if (ss != KVQ_OK) return ss == KVQ_ERR_CAPACITY ? KVQ_ERR_CUDA : ss;
+  int grid = num_sms();
+  if (grid > kManyGrid) grid = kManyGrid;
+  kern<<<grid, kMThreads, smem, st>>>(v, a, ws, RT);
+  if (cudaGetLastError() != cudaSuccess) return KVQ_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid * (RT / kMergeRows));
+  cfg.blockDim = dim3(kMergeRows * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, many_merge_kernel<D>, v, a, (const unsigned char*)ws, RT, grid) == cudaSuccess ? KVQ_OK
+                                                                                                               : KVQ_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t query_many_workspace_bytes(const KvqView& v, int batch, int n_q) {
+  const int RT = (long long)n_q * v.n_rep > kRows ? 2 * kRows : kRows;
+  return many_header_bytes(kManyGrid) + 2ull * kManyGrid * many_rec_bytes(v.D, RT);
+}
+
+kvq_status launch_query_many(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st) {
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  switch (fmt_index(v.kfmt) * 2 + (v.D == 128)) {
+    case 0: return launch_many_t<kI8, 64>(v, a, w, st);
+    case 1: return launch_many_t<kI8, 128>(v, a, w, st);
+    case 2: return launch_many_t<kE4, 64>(v, a, w, st);
+    case 3: return launch_many_t<kE4, 128>(v, a, w, st);
+    case 4: return launch_many_t<kE5, 64>(v, a, w, st);
+    default: return launch_many_t<kE5, 128>(v, a, w, st);
+  }
+}
+
+}  // namespace kvq
