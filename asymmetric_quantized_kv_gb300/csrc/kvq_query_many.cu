@@ -68,9 +68,8 @@ struct Lay {
 };
 
 struct Misc {
-  float sk[kSlots][kPieces];    // key scale of a piece
-  float lv[kSlots][kPieces];    // log2 of the value scale (-inf: the piece has no tokens to see)
-  float iv[kSlots][kPieces];    // 1 / value scale
+  // of each piece: key scale, log2 of the value scale (-inf: it has no tokens to see), 1 / value scale
+  float4 scale[kSlots][kPieces];
   uint32_t skip_k[kSlots];      // pieces to fill with zeros
   uint32_t skip_v[kSlots];
   uint64_t raw_k_full, raw_v_full, raw_k_empty, raw_v_empty;
@@ -117,6 +116,58 @@ __device__ __forceinline__ void next_unit(const KvqView& v, const QueryArgs& a, 
   w.tiles = unit_tiles(v, a, w.T, w.n, w.rows, w.qt, RT);
 }
 
+// A tile on its way through the copying warp: this lane's share.
+struct Pending {
+  bool some;          // (whole warp) there is a tile
+  bool good, scaled;  // this lane's page of codes is there; its piece's scales were read
+  int t0, t1;         // the tile's tokens that come from pages
+  int p0, p1;         // tokens of this lane's page in it
+  int row0;           // the page's slot of token p0
+  int gp, gslot;      // page of this lane's piece's scales, and their slot
+  uint32_t missing;   // pieces whose page is missing
+  long long page;     // byte of the page's head block
+  long long head_off;
+  float ks, vs;
+
+  __device__ __forceinline__ void look_up(const KvqView& v, const Walk& w, int j, int lane) {
+    const int32_t* bt = v.block_table + (long long)w.b * v.max_pages;
+    t0 = j * kTok;
+    t1 = min(t0 + kTok, w.nq);
+    const int pg = t0 / v.P + lane;
+    p0 = (int)max((long long)t0, min((long long)t1, (long long)pg * v.P));
+    p1 = (int)min((long long)t1, ((long long)pg + 1) * v.P);
+    row0 = (int)(p0 - (long long)pg * v.P);
+    head_off = (long long)w.h * v.head_bytes;
+    page = p0 < p1 ? bt[pg] : -1;  // the id, until read_scales
+    gp = -1;
+    gslot = 0;
+    const int t = t0 + 16 * lane;
+    if (lane < kPieces && t < t1) {
+      const int g0 = t / v.kgroup * v.kgroup, q = g0 / v.P;
+      gp = bt[q];
+      gslot = (g0 - q * v.P) / v.kgroup;
+    }
+  }
+  __device__ __forceinline__ void read_scales(const KvqView& v, int D, int lane) {
+    const bool has = p0 < p1;
+    good = has && page >= 0 && page < v.n_pages;
+    missing = has && !good ? ((1u << ((p1 - t0) / 16)) - 1u) & ~((1u << ((p0 - t0) / 16)) - 1u) : 0u;
+    missing = __reduce_or_sync(0xffffffffu, missing);
+    page = (good ? page : 0) * v.page_bytes + head_off;
+    scaled = gp >= 0 && gp < v.n_pages;
+    ks = vs = 0.f;
+    if (scaled) {
+      const uint8_t* hb = v.pages + gp * v.page_bytes + head_off;
+      ks = load_meta(hb + v.off_km, gslot, v.meta16);
+      vs = load_meta(hb + v.off_vm, gslot, v.meta16);
+    }
+  }
+};
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {  // without an arrival
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 // Bounded wait of a task; after a wait that gave up nothing more is waited for.
 struct Waiter {
   Misc& m;
@@ -142,20 +193,23 @@ template <int F, int D>
 __device__ __forceinline__ void convert_piece(const uint8_t* raw, uint8_t* dst, int piece, int lane) {
   constexpr int CPR = D / 16;         // 16-code chunks per row
   constexpr int RPI = 32 / CPR;       // rows per pass
+  constexpr int N = 16 / RPI;
+  const int r0 = 16 * piece + lane / CPR, c = lane % CPR;
+  // the upper panel's lanes write their second half first: a store's eight lanes then meet 8 chunks
+  const int sw = D == 128 ? c >> 2 : 0;
+  uint4 x[N];
 #pragma unroll
-  for (int i = 0; i < 16 / RPI; ++i) {
-    const int r = 16 * piece + i * RPI + lane / CPR, c = lane % CPR;
-    uint4 x = *reinterpret_cast<const uint4*>(raw + r * D + 16 * c);
-    // the upper panel's lanes write their second half first: a store's eight lanes then meet 8 chunks
-    const int sw = D == 128 ? c >> 2 : 0;
-    if (sw) x = make_uint4(x.z, x.w, x.x, x.y);
+  for (int i = 0; i < N; ++i) x[i] = *reinterpret_cast<const uint4*>(raw + (r0 + i * RPI) * D + 16 * c);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint4 y = sw ? make_uint4(x[i].z, x[i].w, x[i].x, x[i].y) : x[i];
     uint32_t f[8];
-    codes_to_f16<F>(x.x, f[0], f[1]);
-    codes_to_f16<F>(x.y, f[2], f[3]);
-    codes_to_f16<F>(x.z, f[4], f[5]);
-    codes_to_f16<F>(x.w, f[6], f[7]);
-    *reinterpret_cast<uint4*>(dst + tile_chunk(r, 2 * c + sw)) = make_uint4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<uint4*>(dst + tile_chunk(r, 2 * c + 1 - sw)) = make_uint4(f[4], f[5], f[6], f[7]);
+    codes_to_f16<F>(y.x, f[0], f[1]);
+    codes_to_f16<F>(y.y, f[2], f[3]);
+    codes_to_f16<F>(y.z, f[4], f[5]);
+    codes_to_f16<F>(y.w, f[6], f[7]);
+    *reinterpret_cast<uint4*>(dst + tile_chunk(r0 + i * RPI, 2 * c + sw)) = make_uint4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<uint4*>(dst + tile_chunk(r0 + i * RPI, 2 * c + 1 - sw)) = make_uint4(f[4], f[5], f[6], f[7]);
   }
 }
 template <int D>
@@ -199,6 +253,95 @@ __device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
   fence_proxy_async();
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// ---- softmax of one row over a tile's 128 logits at tS; columns from lim on are masked
+
+// The row's largest x.  Loops are kept short: the tasks' code together has to stay in the instruction
+// caches, and its misses were 40% of the stalls of the fully unrolled form.
+template <bool kMasked>
+__device__ __forceinline__ float tile_max(uint32_t tS, const float4* sc, float fct, int lim) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t r[2][32];
+    tc::tmem_ld32(tS + 64 * c, r[0]);
+    tc::tmem_ld32(tS + 64 * c + 32, r[1]);
+    tc::wait_ld(r[0]);
+    tc::wait_ld(r[1]);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      float x[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[e] = __uint_as_float(r[h >> 1][16 * (h & 1) + e]);
+        if (kMasked && 64 * c + 16 * h + e >= lim) x[e] = -INFINITY;
+      }
+      float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]);
+      m0 = max3(m0, x[6], x[7]);
+      m1 = max3(m1, x[8], x[9]);
+      m0 = max3(m0, x[10], x[11]);
+      m1 = max3(m1, x[12], x[13]);
+      m0 = max3(m0, x[14], x[15]);
+      // an all-masked piece times a zero scale is NaN, which fmaxf passes over
+      const float4 k = sc[4 * c + h];
+      mx = fmaxf(mx, fmaf(fmaxf(m0, m1), k.x * fct, k.y));
+    }
+  }
+  return mx;
+}
+
+// 32 columns: weights into pk as f16 pairs; returns their sum over the value scales.
+template <bool kMasked>
+__device__ __forceinline__ float weights32(const uint32_t (&r)[32], uint32_t (&pk)[16], const float4* sc, float fct, float M,
+                                           int lim) {
+  float l = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float4 k = sc[h];
+    const float cc = k.x * fct, bb = k.y - M;
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = 16 * h + 2 * e;
+      float2 x = fma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(cc, cc), make_float2(bb, bb));
+      if (kMasked) {
+        if (i >= lim) x.x = -INFINITY;
+        if (i + 1 >= lim) x.y = -INFINITY;
+      }
+      const float2 p = make_float2(ex2(x.x), ex2(x.y));
+      sum = add2(sum, p);
+      pk[8 * h + e] = pack_f16x2(p.x, p.y);
+    }
+    l = fmaf(sum.x + sum.y, k.z, l);
+  }
+  return l;
+}
+
+// The row's weights 2^(x - M), written over its logits as f16; returns sum of weight / value scale.
+template <bool kMasked>
+__device__ __forceinline__ float tile_weights(uint32_t tS, const float4* sc, float fct, float M, int lim) {
+  float l = 0.f;
+  uint32_t r0[32], r1[32], pk[16];
+  tc::tmem_ld32(tS, r0);
+#pragma unroll 1
+  for (int c = 0; c < 4; c += 2) {  // columns 32 c ..: P's 16 lie over logits that have been read
+    tc::wait_ld(r0);
+    tc::tmem_ld32(tS + 32 * c + 32, r1);
+    l += weights32<kMasked>(r0, pk, sc + 2 * c, fct, M, lim - 32 * c);
+    tc::tmem_st16(tS + 16 * c, pk);
+    tc::wait_ld(r1);
+    if (c == 0) tc::tmem_ld32(tS + 64, r0);
+    l += weights32<kMasked>(r1, pk, sc + 2 * c + 2, fct, M, lim - 32 * c - 32);
+    tc::tmem_st16(tS + 16 * c + 16, pk);
+  }
+  return l;
 }
 
 __host__ __device__ inline size_t many_rec_bytes(int D, int RT) { return (size_t)RT * (D + 4) * sizeof(float); }
@@ -337,60 +480,49 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
 
   // Every task walks the same segments: tiles [j0, j1) of unit w.
   if (warp == kLoadWarp) {
-    uint32_t it = 0;  // tiles so far: phase of the single raw stage, slot of the scales
+    // Tiles pass through three steps, one tile apart, so that no load's latency is waited for: page ids
+    // (lane i: the tile's i-th page, and the page of piece i's scales), then scales, then the copies.
+    Pending p2, p1, p0;
+    p1.some = p0.some = false;
+    unsigned long long todo = left;  // tiles not yet looked up
+    int j = j0;
     bool ok = true;
+    uint32_t it = 0;  // tiles copied: phase of the single raw stage, slot of the scales
     for (;;) {
-      const int j1 = (int)min((unsigned long long)w.tiles, j0 + left);
-      const int32_t* bt = v.block_table + (long long)w.b * v.max_pages;
-      const long long head_off = (long long)w.h * v.head_bytes;
-      for (int j = j0; j < j1 && ok; ++j, ++it) {
-        const int t0 = j * kTok, t1 = min(t0 + kTok, w.nq);  // tokens from pages
+      p2.some = todo > 0;
+      if (p2.some) {
+        p2.look_up(v, w, j, lane);
+        --todo;
+        if (++j == w.tiles && todo > 0) {
+          j = 0;
+          next_unit(v, a, RT, w);
+        }
+      }
+      if (p1.some) p1.read_scales(v, D, lane);
+      if (p0.some) {
         const int slot = it % kSlots;
-        // lane i: the tile's i-th page (at most 9)
-        const int pg = t0 / v.P + lane;
-        const int p0 = (int)max((long long)t0, min((long long)t1, (long long)pg * v.P));
-        const int p1 = (int)min((long long)t1, ((long long)pg + 1) * v.P);
-        int pid = -1;
-        const bool has = p0 < p1;
-        if (has) pid = bt[pg];
-        const bool good = has && pid >= 0 && pid < v.n_pages;
-        const uint8_t* src = v.pages + (long long)(good ? pid : 0) * v.page_bytes + head_off + (p0 - (long long)pg * v.P) * D;
-        const uint32_t bytes = good ? (uint32_t)(p1 - p0) * D : 0u;
+        const uint32_t bytes = p0.good ? (uint32_t)(p0.p1 - p0.p0) * D : 0u;
         const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
-        // pieces whose page is missing
-        uint32_t bad = has && !good ? ((1u << ((p1 - t0) / 16)) - 1u) & ~((1u << ((p0 - t0) / 16)) - 1u) : 0u;
-        bad = __reduce_or_sync(0xffffffffu, bad);
-        ok = wait(&mi.raw_k_empty, (it & 1) ^ 1);
-        ok = __all_sync(0xffffffffu, ok);
+        const uint8_t* src = v.pages + p0.page + (long long)p0.row0 * D;
+        ok = __all_sync(0xffffffffu, wait(&mi.raw_k_empty, (it & 1) ^ 1));
         if (!ok) break;
-        if (lane == 0 && sum) asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(&mi.raw_k_full)), "r"(sum) : "memory");
+        if (lane == 0 && sum) mbar_expect_tx(&mi.raw_k_full, sum);
         __syncwarp();
-        if (bytes) bulk_g2s(sm + L::kRawK + (p0 - t0) * D, src, bytes, &mi.raw_k_full);
-        // scales, lane i for piece i
-        float ks = 0.f, lv = -INFINITY, iv = 0.f;
+        if (bytes) bulk_g2s(sm + L::kRawK + (p0.p0 - p0.t0) * D, src, bytes, &mi.raw_k_full);
+        float4 sc = make_float4(0.f, -INFINITY, 0.f, 0.f);
         bool drop_v = false;
-        if (lane < kPieces) {
-          const int t = t0 + 16 * lane;
-          if (t < t1) {
-            const int g0 = t / v.kgroup * v.kgroup, gp = bt[g0 / v.P];
-            if (gp >= 0 && gp < v.n_pages && !((bad >> lane) & 1u)) {
-              const uint8_t* hb = v.pages + (long long)gp * v.page_bytes + head_off;
-              const int s = (g0 % v.P) / v.kgroup;
-              ks = load_meta(hb + v.off_km, s, v.meta16);
-              const float vs = load_meta(hb + v.off_vm, s, v.meta16);
-              drop_v = !(vs >= pow2i(kMinExp));  // values below 2^-91: read as 0, weight 1
-              lv = drop_v ? 0.f : __log2f(vs);
-              iv = drop_v ? 1.f : __frcp_rn(vs);
-            } else {
-              bad |= 1u << lane;
-            }
+        uint32_t bad = p0.missing;
+        if (lane < kPieces && p0.t0 + 16 * lane < p0.t1) {
+          if (p0.scaled && !((bad >> lane) & 1u)) {
+            drop_v = !(p0.vs >= pow2i(kMinExp));  // values below 2^-91: read as 0, weight 1
+            sc = make_float4(p0.ks, drop_v ? 0.f : __log2f(p0.vs), drop_v ? 1.f : __frcp_rn(p0.vs), 0.f);
+          } else {
+            bad |= 1u << lane;
           }
-          mi.sk[slot][lane] = ks;
-          mi.lv[slot][lane] = lv;
-          mi.iv[slot][lane] = iv;
         }
         bad = __reduce_or_sync(0xffffffffu, bad);
         const uint32_t dv = __ballot_sync(0xffffffffu, drop_v);
+        if (lane < kPieces) mi.scale[slot][lane] = sc;
         if (lane == 0) {
           mi.skip_k[slot] = bad;
           mi.skip_v[slot] = bad | dv;
@@ -398,17 +530,17 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&mi.raw_k_full);
-        ok = wait(&mi.raw_v_empty, (it & 1) ^ 1);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, wait(&mi.raw_v_empty, (it & 1) ^ 1));
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&mi.raw_v_full, sum);
         __syncwarp();
-        if (bytes) bulk_g2s(sm + L::kRawV + (p0 - t0) * D, src + v.off_vc, bytes, &mi.raw_v_full);
+        if (bytes) bulk_g2s(sm + L::kRawV + (p0.p0 - p0.t0) * D, src + v.off_vc, bytes, &mi.raw_v_full);
+        ++it;
+      } else if (!p1.some && !p2.some) {
+        break;
       }
-      left -= j1 - j0;
-      if (!ok || left == 0) break;
-      j0 = 0;
-      next_unit(v, a, RT, w);
+      p0 = p1;
+      p1 = p2;
     }
   } else if (warp >= kConv0 && warp < kConv0 + kConvWarps) {
     uint32_t it = 0;
@@ -423,7 +555,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         ok = wait(&mi.raw_k_full, it & 1) && wait(&mi.k_empty[st], ph ^ 1);
         if (!ok) break;
         const uint32_t skip_k = mi.skip_k[slot], skip_v = mi.skip_v[slot];
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kPieces / kConvWarps; ++i) {
           const int piece = (warp - kConv0) + i * kConvWarps, tok = t0 + 16 * piece;
           if (tok >= w.T || ((skip_k >> piece) & 1u)) {
@@ -433,11 +565,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           } else {
             const int kk = window_piece<D>(v.k_win, v, w.b, w.h, tok, w.T, w.nq, kd, piece, lane, true);
             const int kv = window_piece<D>(v.v_win, v, w.b, w.h, tok, w.T, w.nq, vd, piece, lane, false);
-            if (lane == 0) {
-              mi.sk[slot][piece] = pow2i(kk);
-              mi.lv[slot][piece] = (float)kv;
-              mi.iv[slot][piece] = pow2i(-kv);
-            }
+            if (lane == 0) mi.scale[slot][piece] = make_float4(pow2i(kk), (float)kv, pow2i(-kv), 0.f);
           }
         }
         __syncwarp();
@@ -445,7 +573,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         hand_over(&mi.k_full[st], lane);
         ok = wait(&mi.raw_v_full, it & 1) && wait(&mi.v_empty[st], ph ^ 1);
         if (!ok) break;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kPieces / kConvWarps; ++i) {
           const int piece = (warp - kConv0) + i * kConvWarps, tok = t0 + 16 * piece;
           if (tok >= w.T || (tok < w.nq && ((skip_v >> piece) & 1u))) {
@@ -469,89 +597,46 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
     if (lane == 0) {
       constexpr uint32_t id_s = tc::f16_idesc(128, 128, false), id_o = tc::f16_idesc(128, D, true);
       constexpr uint32_t kPanel = 128 * 128;
-      uint32_t it0 = 0;                     // tiles before this segment
-      uint32_t np[2] = {0, 0}, nseg = 0;    // softmax hand-overs of each stream, segments
+      const uint64_t dq = tc::smem_desc(smem_u32(sm + L::kQ), 16), dk = tc::smem_desc(smem_u32(sm + L::kK), 16);
+      const uint64_t dv = tc::smem_desc(smem_u32(sm + L::kV), kPanel);
+      uint32_t it0 = 0;                // tiles before this segment
+      uint32_t np = 0, nseg = 0;       // phase bits of the streams' hand-overs; segments
       bool ok = true;
-      auto s_mma = [&](int s, uint32_t it) {  // S_s = Q K^T of the CTA's tile `it`
-        const uint32_t q = smem_u32(sm + L::kQ + (two ? s : 0) * L::kTileB), k = smem_u32(sm + L::kK + (it & 1) * L::kTileB);
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          const uint32_t off = (x >> 2) * kPanel + (x & 3) * 32;
-          tc::mma_ss(tmem + 128 * s, tc::smem_desc(q + off, 16), tc::smem_desc(k + off, 16), id_s, x > 0);
-        }
-        tc::commit(&mi.s_full[s]);
-      };
-      auto o_mma = [&](int s, uint32_t it, bool first) {  // O_s (+)= P V
-        const uint32_t vt = smem_u32(sm + L::kV + (it & 1) * L::kTileB);
-#pragma unroll
-        for (int x = 0; x < kTok / 16; ++x)
-          tc::mma_ts(tmem + 256 + D * s, tmem + 128 * s + 8 * x, tc::smem_desc(vt + x * 2048, kPanel), id_o, !first || x > 0);
-      };
-      auto k_ready = [&](uint32_t it) { return wait(&mi.k_full[it & 1], (it >> 1) & 1); };
-      auto v_ready = [&](uint32_t it) { return wait(&mi.v_full[it & 1], (it >> 1) & 1); };
-      auto p_ready = [&](int s) {
-        const bool r = wait(&mi.p_full[s], np[s] & 1);
-        ++np[s];
-        tc::fence_after();
-        return r;
-      };
+      // Step u of a segment is stream u & 1's: P V of its tile, then S of step u + 2, which takes P's place.
       for (;;) {
         const int j1 = (int)min((unsigned long long)w.tiles, j0 + left), nt = j1 - j0;
+        const int steps = two ? 2 * nt : nt;
         ok = wait(&mi.q_full[0], nseg & 1) && (!two || wait(&mi.q_full[1], nseg & 1));
         ++nseg;
-        tc::fence_after();
-        if (two) {
-          if (ok && (ok = k_ready(it0))) {
+#pragma unroll 1
+        for (int u = -2; u < steps && ok; ++u) {
+          const int s = u & 1;
+          const bool last_use = !two || s == 1;  // of the step's tile
+          if (u >= 0) {
+            const uint32_t it = it0 + (two ? u >> 1 : u);
+            if (!(ok = wait(&mi.p_full[s], (np >> s) & 1) && wait(&mi.v_full[it & 1], (it >> 1) & 1))) break;
+            np ^= 1u << s;
             tc::fence_after();
-            s_mma(0, it0);
-            s_mma(1, it0);
-            tc::commit(&mi.k_empty[it0 & 1]);
+            const uint64_t b = dv + (it & 1) * (L::kTileB >> 4);
+#pragma unroll
+            for (int x = 0; x < kTok / 16; ++x)
+              tc::mma_ts(tmem + 256 + D * s, tmem + 128 * s + 8 * x, b + x * (2048 >> 4), id_o, u > 1 || x > 0);
+            if (last_use) tc::commit(&mi.v_empty[it & 1]);
           }
-          for (int i = 0; i < nt && ok; ++i) {
-            const uint32_t it = it0 + i;
-            const bool more = i + 1 < nt;
-            if (!(ok = p_ready(0) && v_ready(it))) break;
+          if (u + 2 < steps) {
+            const uint32_t it = it0 + (two ? (u + 2) >> 1 : u + 2);
+            if (!(ok = wait(&mi.k_full[it & 1], (it >> 1) & 1))) break;
             tc::fence_after();
-            o_mma(0, it, i == 0);
-            if (more) {
-              if (!(ok = k_ready(it + 1))) break;
-              tc::fence_after();
-              s_mma(0, it + 1);
-            } else {
-              tc::commit(&mi.o_full[0]);
+            const uint64_t q = dq + (two ? s : 0) * (L::kTileB >> 4), k = dk + (it & 1) * (L::kTileB >> 4);
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+              const uint32_t off = ((x >> 2) * kPanel + (x & 3) * 32) >> 4;
+              tc::mma_ss(tmem + 128 * s, q + off, k + off, id_s, x > 0);
             }
-            if (!(ok = p_ready(1))) break;
-            o_mma(1, it, i == 0);
-            tc::commit(&mi.v_empty[it & 1]);
-            if (more) {
-              s_mma(1, it + 1);
-              tc::commit(&mi.k_empty[(it + 1) & 1]);
-            } else {
-              tc::commit(&mi.o_full[1]);
-            }
-          }
-        } else {  // tile i belongs to stream i & 1
-          for (int i = 0; i < min(2, nt) && ok; ++i) {
-            if (!(ok = k_ready(it0 + i))) break;
-            tc::fence_after();
-            s_mma(i, it0 + i);
-            tc::commit(&mi.k_empty[(it0 + i) & 1]);
-          }
-          for (int i = 0; i < nt && ok; ++i) {
-            const uint32_t it = it0 + i;
-            const int s = i & 1;
-            if (!(ok = p_ready(s) && v_ready(it))) break;
-            tc::fence_after();
-            o_mma(s, it, i < 2);
-            tc::commit(&mi.v_empty[it & 1]);
-            if (i + 2 < nt) {
-              if (!(ok = k_ready(it + 2))) break;
-              tc::fence_after();
-              s_mma(s, it + 2);
-              tc::commit(&mi.k_empty[it & 1]);
-            } else {
-              tc::commit(&mi.o_full[s]);
-            }
+            tc::commit(&mi.s_full[s]);
+            if (last_use) tc::commit(&mi.k_empty[it & 1]);
+          } else if (u >= 0) {
+            tc::commit(&mi.o_full[s]);
           }
         }
         it0 += nt;
@@ -614,43 +699,18 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           break;
         }
         tc::fence_after();
-        const bool masked = t0 + kTok > warp_end;
+        const float4* sc = mi.scale[slot];
         const int lim = end - t0;
-        // ---- maximum
-        float mx = -INFINITY;
-        {
-          uint32_t r[2][32];
-          tc::tmem_ld32(tS, r[0]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tc::wait_ld(r[c & 1]);
-            if (c < 3) tc::tmem_ld32(tS + 32 * (c + 1), r[(c + 1) & 1]);
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (32 * c + e >= lim) r[c & 1][e] = 0xff800000u;  // -inf
-            }
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              float m4[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) m4[e] = __uint_as_float(r[c & 1][16 * hf + e]);
-#pragma unroll
-              for (int e = 4; e < 16; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(r[c & 1][16 * hf + e]));
-              const float m16 = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-              // an all-masked piece times a zero scale is NaN, which fmaxf passes over
-              mx = fmaxf(mx, fmaf(m16, mi.sk[slot][2 * c + hf] * fct, mi.lv[slot][2 * c + hf]));
-            }
-          }
-        }
+        const bool masked = t0 + kTok > warp_end;
+        const float mx = masked ? tile_max<true>(tS, sc, fct, lim) : tile_max<false>(tS, sc, fct, lim);
         if (__any_sync(0xffffffffu, mx > M + kLazyM)) {
           const float mn = fmaxf(M, mx), al = ex2(M - mn);
           M = mn;
           l *= al;
           if (any) {
-            uint32_t r[32];
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
+              uint32_t r[32];
               tc::tmem_ld32(tO + c, r);
               tc::wait_ld(r);
 #pragma unroll
@@ -660,37 +720,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           }
         }
         any = true;
-        // ---- weights, over the logits' columns
-        {
-          uint32_t r[2][32];
-          tc::tmem_ld32(tS, r[0]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tc::wait_ld(r[c & 1]);
-            if (c < 3) tc::tmem_ld32(tS + 32 * (c + 1), r[(c + 1) & 1]);
-            uint32_t pk[16];
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const float cc = mi.sk[slot][2 * c + hf] * fct, bb = mi.lv[slot][2 * c + hf] - M;
-              float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int k = 16 * hf + 2 * e;
-                float2 x = fma2(make_float2(__uint_as_float(r[c & 1][k]), __uint_as_float(r[c & 1][k + 1])),
-                                make_float2(cc, cc), make_float2(bb, bb));
-                if (masked) {
-                  if (32 * c + k >= lim) x.x = -INFINITY;
-                  if (32 * c + k + 1 >= lim) x.y = -INFINITY;
-                }
-                const float2 p = make_float2(ex2(x.x), ex2(x.y));
-                sum = add2(sum, p);
-                pk[8 * hf + e] = pack_f16x2(p.x, p.y);
-              }
-              l = fmaf(sum.x + sum.y, mi.iv[slot][2 * c + hf], l);
-            }
-            tc::tmem_st16(tS + 16 * c, pk);
-          }
-        }
+        l += masked ? tile_weights<true>(tS, sc, fct, M, lim) : tile_weights<false>(tS, sc, fct, M, lim);
         tc::wait_st();
         tc::fence_before();
         mbar_arrive(&mi.p_full[s]);
