@@ -168,13 +168,27 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) { 
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
+// Polls of a wait, each of which may sleep for the hint (20 us): idle warps then leave the issue slots to
+// the others, and a wait that nothing ends gives up after about a second.
+constexpr uint32_t kManyPolls = 1u << 16, kManyHint = 20000;
+
+__device__ __forceinline__ bool mbar_try_wait_hint(uint64_t* bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+
 // Bounded wait of a task; after a wait that gave up nothing more is waited for.
 struct Waiter {
   Misc& m;
   int32_t* status;
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    for (uint32_t i = 0; i < kWaitPolls; ++i) {
-      if (mbar_try_wait(bar, parity)) return true;
+    for (uint32_t i = 0; i < kManyPolls; ++i) {
+      if (mbar_try_wait_hint(bar, parity, kManyHint)) return true;
       if (*reinterpret_cast<volatile int*>(&m.abort)) return false;
     }
     *reinterpret_cast<volatile int*>(&m.abort) = 1;
@@ -594,59 +608,71 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
       next_unit(v, a, RT, w);
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      constexpr uint32_t id_s = tc::f16_idesc(128, 128, false), id_o = tc::f16_idesc(128, D, true);
-      constexpr uint32_t kPanel = 128 * 128;
-      const uint64_t dq = tc::smem_desc(smem_u32(sm + L::kQ), 16), dk = tc::smem_desc(smem_u32(sm + L::kK), 16);
-      const uint64_t dv = tc::smem_desc(smem_u32(sm + L::kV), kPanel);
-      uint32_t it0 = 0;                // tiles before this segment
-      uint32_t np = 0, nseg = 0;       // phase bits of the streams' hand-overs; segments
-      bool ok = true;
-      // Step u of a segment is stream u & 1's: P V of its tile, then S of step u + 2, which takes P's place.
-      for (;;) {
-        const int j1 = (int)min((unsigned long long)w.tiles, j0 + left), nt = j1 - j0;
-        const int steps = two ? 2 * nt : nt;
-        ok = wait(&mi.q_full[0], nseg & 1) && (!two || wait(&mi.q_full[1], nseg & 1));
-        ++nseg;
+    // The whole warp walks the steps with values it knows to be uniform, and one elected lane issues: the
+    // descriptors then stay in uniform registers (issued from a divergent lane, a product cost 160 cycles).
+    constexpr uint32_t id_s = tc::f16_idesc(128, 128, false), id_o = tc::f16_idesc(128, D, true);
+    constexpr uint32_t kPanel = 128 * 128;
+    const uint64_t dq = tc::smem_desc(smem_u32(sm + L::kQ), 16), dk = tc::smem_desc(smem_u32(sm + L::kK), 16);
+    const uint64_t dv = tc::smem_desc(smem_u32(sm + L::kV), kPanel);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const bool elected = tc::elect_one();
+    uint32_t it0 = 0;                // tiles before this segment
+    uint32_t np = 0, nseg = 0;       // phase bits of the streams' hand-overs; segments
+    bool ok = true;
+    // Step u of a segment is stream u & 1's: P V of its tile, then S of step u + 2, which takes P's place.
+    for (;;) {
+      const int j1 = (int)min((unsigned long long)w.tiles, j0 + left);
+      const int nt = __shfl_sync(0xffffffffu, j1 - j0, 0);
+      const int steps = two ? 2 * nt : nt;
+      ok = wait(&mi.q_full[0], nseg & 1) && (!two || wait(&mi.q_full[1], nseg & 1));
+      ok = __all_sync(0xffffffffu, ok);
+      ++nseg;
 #pragma unroll 1
-        for (int u = -2; u < steps && ok; ++u) {
-          const int s = u & 1;
-          const bool last_use = !two || s == 1;  // of the step's tile
-          if (u >= 0) {
-            const uint32_t it = it0 + (two ? u >> 1 : u);
-            if (!(ok = wait(&mi.p_full[s], (np >> s) & 1) && wait(&mi.v_full[it & 1], (it >> 1) & 1))) break;
-            np ^= 1u << s;
-            tc::fence_after();
-            const uint64_t b = dv + (it & 1) * (L::kTileB >> 4);
+      for (int u = -2; u < steps && ok; ++u) {
+        const int s = u & 1;
+        const bool last_use = !two || s == 1;  // of the step's tile
+        if (u >= 0) {
+          const uint32_t it = it0 + (two ? u >> 1 : u);
+          ok = wait(&mi.p_full[s], (np >> s) & 1) && wait(&mi.v_full[it & 1], (it >> 1) & 1);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          np ^= 1u << s;
+          tc::fence_after();
+          const uint64_t b = dv + (it & 1) * (L::kTileB >> 4);
+          if (elected) {
 #pragma unroll
             for (int x = 0; x < kTok / 16; ++x)
-              tc::mma_ts(tmem + 256 + D * s, tmem + 128 * s + 8 * x, b + x * (2048 >> 4), id_o, u > 1 || x > 0);
+              tc::mma_ts(tm + 256 + D * s, tm + 128 * s + 8 * x, b + x * (2048 >> 4), id_o, u > 1 || x > 0);
             if (last_use) tc::commit(&mi.v_empty[it & 1]);
           }
-          if (u + 2 < steps) {
-            const uint32_t it = it0 + (two ? (u + 2) >> 1 : u + 2);
-            if (!(ok = wait(&mi.k_full[it & 1], (it >> 1) & 1))) break;
-            tc::fence_after();
-            const uint64_t q = dq + (two ? s : 0) * (L::kTileB >> 4), k = dk + (it & 1) * (L::kTileB >> 4);
+          __syncwarp();
+        }
+        if (u + 2 < steps) {
+          const uint32_t it = it0 + (two ? (u + 2) >> 1 : u + 2);
+          ok = wait(&mi.k_full[it & 1], (it >> 1) & 1);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          tc::fence_after();
+          const uint64_t q = dq + (two ? s : 0) * (L::kTileB >> 4), k = dk + (it & 1) * (L::kTileB >> 4);
+          if (elected) {
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
               const uint32_t off = ((x >> 2) * kPanel + (x & 3) * 32) >> 4;
-              tc::mma_ss(tmem + 128 * s, q + off, k + off, id_s, x > 0);
+              tc::mma_ss(tm + 128 * s, q + off, k + off, id_s, x > 0);
             }
             tc::commit(&mi.s_full[s]);
             if (last_use) tc::commit(&mi.k_empty[it & 1]);
-          } else if (u >= 0) {
-            tc::commit(&mi.o_full[s]);
           }
+          __syncwarp();
+        } else if (u >= 0) {
+          if (elected) tc::commit(&mi.o_full[s]);
+          __syncwarp();
         }
-        it0 += nt;
-        left -= nt;
-        if (!ok || left == 0) break;
-        j0 = 0;
-        next_unit(v, a, RT, w);
       }
+      it0 += nt;
+      left -= nt;
+      if (!ok || left == 0) break;
+      j0 = 0;
+      next_unit(v, a, RT, w);
     }
-    __syncwarp();
   } else {  // ---- softmax streams
     const int s = warp >> 2, row_l = threadIdx.x & (kRows - 1);
     const uint32_t lane_off = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, in the address's upper half

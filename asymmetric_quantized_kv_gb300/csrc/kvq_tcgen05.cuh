@@ -61,6 +61,13 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 
 // ---- products (one thread)
 
+// True in one lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
 // Shared-memory operand of 16-bit elements in 128-byte rows with the 128-byte swizzle (atoms of 8 rows,
 // 1024-byte aligned), atoms 1024 bytes apart.  Rows along K contiguous (K-major: a row is 64 elements of K)
 // or along M/N (MN-major: a row is 64 elements of M/N, further ones lead_bytes on).
