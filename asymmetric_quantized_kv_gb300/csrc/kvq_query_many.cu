@@ -12,14 +12,14 @@
 // power of two; p is rounded to f16 once (2^-11 against the output's own 2^-8).
 //
 // What bounds it: the tensor cores and the softmax's exponentials for many rows, the codes'
-// traffic for few.  One persistent CTA per SM of 14 warps, each with one task:
-//   12     copies the tiles' codes into shared memory (bulk copies, a page each) and reads
-//          the scales;
-//   8-11   turn codes (and the window's bf16 rows) into f16 tiles with the 128-byte swizzle;
-//   13     issues the products: S = Q K^T from shared memory, O += P V with P in tensor
+// traffic for few.  One persistent CTA per SM of 22 warps, each with one task:
+//   20     copies the tiles' codes into shared memory (bulk copies, a page each) and reads
+//          the scales, two tiles ahead;
+//   16-19  turn codes (and the window's bf16 rows) into f16 tiles with the 128-byte swizzle;
+//   21     issues the products: S = Q K^T from shared memory, O += P V with P in tensor
 //          memory;
-//   0-3, 4-7  two streams of 128 rows: a thread owns a row, reads its S from tensor memory,
-//          writes P over it and rescales O.
+//   0-7, 8-15  two streams of 128 rows: two threads own a row, half of its columns each,
+//          read S from tensor memory, write P over it and rescale O.
 // The two streams' products alternate, so that one runs while the other's softmax does.
 // With more than 128 rows a unit is 256 rows, one half a stream, over the same tiles;
 // with fewer the streams take every other tile of one half and are joined at the end.
@@ -41,8 +41,10 @@ using namespace ptx;
 constexpr int kRows = 128;    // rows of a stream
 constexpr int kTok = 128;     // tokens of a tile
 constexpr int kPieces = kTok / 16;
-constexpr int kMThreads = 14 * 32;
-constexpr int kConvWarps = 4, kConv0 = 8, kLoadWarp = 12, kMmaWarp = 13;
+constexpr int kSoftWarps = 16;           // 8 a stream: 4 warps reach the 128 rows, twice, for half the columns each
+constexpr int kConv0 = kSoftWarps, kConvWarps = 4, kLoadWarp = kConv0 + kConvWarps, kMmaWarp = kLoadWarp + 1;
+constexpr int kMThreads = (kMmaWarp + 1) * 32;
+constexpr int kBarStream = 1, kBarJoin = 3;  // named barriers: of the streams (and the next), of both
 constexpr int kSlots = 8;     // tiles whose scales are kept
 constexpr float kLazyM = 8.f;
 constexpr float kMinitM = -1e30f;
@@ -75,6 +77,7 @@ struct Misc {
   uint64_t raw_k_full, raw_v_full, raw_k_empty, raw_v_empty;
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2], q_full[2];
+  float row_x[2][kRows];        // exchange between the two threads of a row
   uint32_t tmem;
   int abort;
   int start_b, start_h, start_qt, start_tile;
@@ -89,12 +92,15 @@ struct Walk {  // one unit, and the CTA's place in it
   int tiles;                // of the unit
 };
 
-__device__ __forceinline__ int unit_tiles(const KvqView& v, const QueryArgs& a, int T, int n, int rows, int qt, int RT) {
+// Out of line, like everything that a tile's loop does not run: the tasks' loops share the SM's instruction
+// caches, and the kernel's inlined form (250 KB) missed them all the time.
+static __device__ __noinline__ int unit_tiles(int causal, int n_rep, int T, int n, int rows, int qt, int RT) {
   const int last = min(rows, (qt + 1) * RT) - 1;
-  return max(1, (query_end(a, T, n, last / v.n_rep) + kTok - 1) / kTok);
+  const int end = causal ? max(0, T - n + last / n_rep + 1) : T;
+  return max(1, (end + kTok - 1) / kTok);
 }
 
-__device__ __forceinline__ void load_sequence(const KvqView& v, const QueryArgs& a, int RT, Walk& w) {
+static __device__ __noinline__ void load_sequence(const KvqView& v, const QueryArgs& a, int RT, Walk& w) {
   w.T = seq_tokens(v, w.b);
   w.nq = n_quantized(w.T, v.R);
   w.n = query_count(v, a, w.b);
@@ -102,7 +108,7 @@ __device__ __forceinline__ void load_sequence(const KvqView& v, const QueryArgs&
   w.nqt = (w.rows + RT - 1) / RT;
 }
 
-__device__ __forceinline__ void next_unit(const KvqView& v, const QueryArgs& a, int RT, Walk& w) {
+static __device__ __noinline__ void next_unit(const KvqView& v, const QueryArgs& a, int RT, Walk& w) {
   if (++w.qt == w.nqt) {
     w.qt = 0;
     if (++w.h == v.Hkv) {
@@ -113,7 +119,7 @@ __device__ __forceinline__ void next_unit(const KvqView& v, const QueryArgs& a, 
       } while (w.nqt == 0);  // units remain, so a sequence with rows follows
     }
   }
-  w.tiles = unit_tiles(v, a, w.T, w.n, w.rows, w.qt, RT);
+  w.tiles = unit_tiles(a.causal, v.n_rep, w.T, w.n, w.rows, w.qt, RT);
 }
 
 // A tile on its way through the copying warp: this lane's share.
@@ -187,6 +193,7 @@ struct Waiter {
   Misc& m;
   int32_t* status;
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+#pragma unroll 1
     for (uint32_t i = 0; i < kManyPolls; ++i) {
       if (mbar_try_wait_hint(bar, parity, kManyHint)) return true;
       if (*reinterpret_cast<volatile int*>(&m.abort)) return false;
@@ -202,39 +209,55 @@ __device__ __forceinline__ uint32_t tile_chunk(int r, int c) {
   return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// ---- converter: 16 tokens of a raw tile -> f16 (whole warp)
-template <int F, int D>
-__device__ __forceinline__ void convert_piece(const uint8_t* raw, uint8_t* dst, int piece, int lane) {
+// ---- converter: K pieces of 16 tokens of a raw tile, 4 pieces apart, -> f16 (whole warp)
+template <int F, int D, int K>
+__device__ __forceinline__ void convert_n(const uint8_t* raw, uint8_t* dst, int piece, int lane) {
   constexpr int CPR = D / 16;         // 16-code chunks per row
   constexpr int RPI = 32 / CPR;       // rows per pass
   constexpr int N = 16 / RPI;
   const int r0 = 16 * piece + lane / CPR, c = lane % CPR;
   // the upper panel's lanes write their second half first: a store's eight lanes then meet 8 chunks
   const int sw = D == 128 ? c >> 2 : 0;
-  uint4 x[N];
+  uint4 x[K][N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = *reinterpret_cast<const uint4*>(raw + (r0 + i * RPI) * D + 16 * c);
+  for (int k = 0; k < K; ++k)
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const uint4 y = sw ? make_uint4(x[i].z, x[i].w, x[i].x, x[i].y) : x[i];
-    uint32_t f[8];
-    codes_to_f16<F>(y.x, f[0], f[1]);
-    codes_to_f16<F>(y.y, f[2], f[3]);
-    codes_to_f16<F>(y.z, f[4], f[5]);
-    codes_to_f16<F>(y.w, f[6], f[7]);
-    *reinterpret_cast<uint4*>(dst + tile_chunk(r0 + i * RPI, 2 * c + sw)) = make_uint4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<uint4*>(dst + tile_chunk(r0 + i * RPI, 2 * c + 1 - sw)) = make_uint4(f[4], f[5], f[6], f[7]);
-  }
+    for (int i = 0; i < N; ++i)
+      x[k][i] = *reinterpret_cast<const uint4*>(raw + (r0 + 64 * k + i * RPI) * D + 16 * c);
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint4 z = x[k][i], y = sw ? make_uint4(z.z, z.w, z.x, z.y) : z;
+      uint32_t f[8];
+      codes_to_f16<F>(y.x, f[0], f[1]);
+      codes_to_f16<F>(y.y, f[2], f[3]);
+      codes_to_f16<F>(y.z, f[4], f[5]);
+      codes_to_f16<F>(y.w, f[6], f[7]);
+      *reinterpret_cast<uint4*>(dst + tile_chunk(r0 + 64 * k + i * RPI, 2 * c + sw)) = make_uint4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<uint4*>(dst + tile_chunk(r0 + 64 * k + i * RPI, 2 * c + 1 - sw)) = make_uint4(f[4], f[5], f[6], f[7]);
+    }
+}
+template <int F, int D>
+__device__ __noinline__ void convert_piece(const uint8_t* raw, uint8_t* dst, int piece, int lane) {
+  convert_n<F, D, 1>(raw, dst, piece, lane);
+}
+// Both pieces of a warp, their loads in flight together.
+template <int F, int D>
+__device__ __forceinline__ void convert_pieces(const uint8_t* raw, uint8_t* dst, int piece, int lane) {
+  static_assert(kPieces == 2 * kConvWarps && kConvWarps == 4, "two pieces a warp, 64 rows apart");
+  convert_n<F, D, 2>(raw, dst, piece, lane);
 }
 template <int D>
-__device__ __forceinline__ void zero_piece(uint8_t* dst, int piece, int lane) {
+__device__ __noinline__ void zero_piece(uint8_t* dst, int piece, int lane) {
+#pragma unroll 1
   for (int i = lane; i < 16 * (D / 8); i += 32)
     *reinterpret_cast<uint4*>(dst + tile_chunk(16 * piece + i / (D / 8), i % (D / 8))) = make_uint4(0u, 0u, 0u, 0u);
 }
 // 16 window rows from token tok (those before T; zeros behind), scaled by 2^-k with k their common exponent.
 // write == false: only the exponent.
 template <int D>
-__device__ __forceinline__ int window_piece(const void* win, const KvqView& v, int b, int h, int tok, int T, int nq, uint8_t* dst,
+__device__ __noinline__ int window_piece(const void* win, const KvqView& v, int b, int h, int tok, int T, int nq, uint8_t* dst,
                                             int piece, int lane, bool write) {
   constexpr int CPR = D / 8, RPI = 32 / CPR, N = 16 / RPI;
   uint4 x[N];
@@ -275,27 +298,25 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// ---- softmax of one row over a tile's 128 logits at tS; columns from lim on are masked
+// ---- softmax of half a row: 64 of a tile's logits, from column tS; columns from lim on are masked.
+// Loops are short: the tasks' code together has to stay in the instruction caches.
 
-// The row's largest x.  Loops are kept short: the tasks' code together has to stay in the instruction
-// caches, and its misses were 40% of the stalls of the fully unrolled form.
+// Largest x.
 template <bool kMasked>
-__device__ __forceinline__ float tile_max(uint32_t tS, const float4* sc, float fct, int lim) {
+__device__ __forceinline__ float half_max(uint32_t tS, const float4* sc, float fct, int lim) {
   float mx = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
-    uint32_t r[2][32];
-    tc::tmem_ld32(tS + 64 * c, r[0]);
-    tc::tmem_ld32(tS + 64 * c + 32, r[1]);
-    tc::wait_ld(r[0]);
-    tc::wait_ld(r[1]);
+    uint32_t r[32];
+    tc::tmem_ld32(tS + 32 * c, r);
+    tc::wait_ld(r);
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
+    for (int h = 0; h < 2; ++h) {
       float x[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        x[e] = __uint_as_float(r[h >> 1][16 * (h & 1) + e]);
-        if (kMasked && 64 * c + 16 * h + e >= lim) x[e] = -INFINITY;
+        x[e] = __uint_as_float(r[16 * h + e]);
+        if (kMasked && 32 * c + 16 * h + e >= lim) x[e] = -INFINITY;
       }
       float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]);
       m0 = max3(m0, x[6], x[7]);
@@ -304,58 +325,56 @@ __device__ __forceinline__ float tile_max(uint32_t tS, const float4* sc, float f
       m1 = max3(m1, x[12], x[13]);
       m0 = max3(m0, x[14], x[15]);
       // an all-masked piece times a zero scale is NaN, which fmaxf passes over
-      const float4 k = sc[4 * c + h];
+      const float4 k = sc[2 * c + h];
       mx = fmaxf(mx, fmaf(fmaxf(m0, m1), k.x * fct, k.y));
     }
   }
   return mx;
 }
 
-// 32 columns: weights into pk as f16 pairs; returns their sum over the value scales.
+// Weights 2^(x - M) as f16, over the first 32 of the columns they come from (a piece's lie over logits
+// that have been read); returns the sum of weight / value scale.
 template <bool kMasked>
-__device__ __forceinline__ float weights32(const uint32_t (&r)[32], uint32_t (&pk)[16], const float4* sc, float fct, float M,
-                                           int lim) {
+__device__ __forceinline__ float half_weights(uint32_t tS, const float4* sc, float fct, float M, int lim) {
   float l = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t r[32], pk[16];
+    tc::tmem_ld32(tS + 32 * c, r);
+    tc::wait_ld(r);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float4 k = sc[h];
-    const float cc = k.x * fct, bb = k.y - M;
-    float2 sum = make_float2(0.f, 0.f);
+    for (int h = 0; h < 2; ++h) {
+      const float4 k = sc[2 * c + h];
+      const float cc = k.x * fct, bb = k.y - M;
+      float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int i = 16 * h + 2 * e;
-      float2 x = fma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(cc, cc), make_float2(bb, bb));
-      if (kMasked) {
-        if (i >= lim) x.x = -INFINITY;
-        if (i + 1 >= lim) x.y = -INFINITY;
+      for (int e = 0; e < 8; ++e) {
+        const int i = 16 * h + 2 * e;
+        float2 x = fma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(cc, cc), make_float2(bb, bb));
+        if (kMasked) {
+          if (32 * c + i >= lim) x.x = -INFINITY;
+          if (32 * c + i + 1 >= lim) x.y = -INFINITY;
+        }
+        const float2 p = make_float2(ex2(x.x), ex2(x.y));
+        sum = add2(sum, p);
+        pk[8 * h + e] = pack_f16x2(p.x, p.y);
       }
-      const float2 p = make_float2(ex2(x.x), ex2(x.y));
-      sum = add2(sum, p);
-      pk[8 * h + e] = pack_f16x2(p.x, p.y);
+      l = fmaf(sum.x + sum.y, k.z, l);
     }
-    l = fmaf(sum.x + sum.y, k.z, l);
+    tc::tmem_st16(tS + 16 * c, pk);
   }
   return l;
 }
 
-// The row's weights 2^(x - M), written over its logits as f16; returns sum of weight / value scale.
-template <bool kMasked>
-__device__ __forceinline__ float tile_weights(uint32_t tS, const float4* sc, float fct, float M, int lim) {
-  float l = 0.f;
-  uint32_t r0[32], r1[32], pk[16];
-  tc::tmem_ld32(tS, r0);
-#pragma unroll 1
-  for (int c = 0; c < 4; c += 2) {  // columns 32 c ..: P's 16 lie over logits that have been read
-    tc::wait_ld(r0);
-    tc::tmem_ld32(tS + 32 * c + 32, r1);
-    l += weights32<kMasked>(r0, pk, sc + 2 * c, fct, M, lim - 32 * c);
-    tc::tmem_st16(tS + 16 * c, pk);
-    tc::wait_ld(r1);
-    if (c == 0) tc::tmem_ld32(tS + 64, r0);
-    l += weights32<kMasked>(r1, pk, sc + 2 * c + 2, fct, M, lim - 32 * c - 32);
-    tc::tmem_st16(tS + 16 * c + 16, pk);
-  }
-  return l;
+// Barrier of a stream's 256 threads that also says whether any of them asks.
+__device__ __forceinline__ bool stream_any(int bar, bool ask) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(bar), "r"((uint32_t)ask)
+      : "memory");
+  return r != 0;
 }
 
 __host__ __device__ inline size_t many_rec_bytes(int D, int RT) { return (size_t)RT * (D + 4) * sizeof(float); }
@@ -364,8 +383,7 @@ __host__ __device__ inline size_t many_header_bytes(int grid) { return ((size_t)
 template <int F, int D>
 __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, QueryArgs a, unsigned char* ws, int RT) {
   using L = Lay<D>;
-  extern __shared__ unsigned char dyn_raw[];
-  unsigned char* sm = dyn_raw + ((1024 - (smem_u32(dyn_raw) & 1023)) & 1023);
+  extern __shared__ __align__(1024) unsigned char sm[];  // the swizzle's atoms
   Misc& mi = *reinterpret_cast<Misc*>(sm + L::kMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool two = RT == 2 * kRows;  // a stream per half of the unit; else both over one half
@@ -382,12 +400,14 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
     // a thread a sequence, or, for few of them, a warp
     const bool warps = v.batch < kMThreads / 32;
     unsigned long long mine = 0;
+#pragma unroll 1
     for (int b = warps ? warp : threadIdx.x; b < v.batch; b += warps ? kMThreads / 32 : kMThreads) {
       Walk w;
       w.b = b;
       load_sequence(v, a, RT, w);
       unsigned long long s = 0;
-      for (int qt = warps ? lane : 0; qt < w.nqt; qt += warps ? 32 : 1) s += unit_tiles(v, a, w.T, w.n, w.rows, qt, RT);
+#pragma unroll 1
+      for (int qt = warps ? lane : 0; qt < w.nqt; qt += warps ? 32 : 1) s += unit_tiles(a.causal, v.n_rep, w.T, w.n, w.rows, qt, RT);
       if (warps) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -410,6 +430,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
   if (warp == 0) {
     unsigned long long left = w0;
     int b = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < v.batch; b0 += 32) {  // the sequence that holds tile w0
       const unsigned long long x = b0 + lane < v.batch ? wb[b0 + lane] * v.Hkv : 0ull;
       unsigned long long incl = x;
@@ -433,8 +454,9 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
     const int h = (int)(left / wb[b]);
     left -= (unsigned long long)h * wb[b];
     int qt = 0;
+#pragma unroll 1
     for (int q0 = 0; q0 < w.nqt; q0 += 32) {
-      const unsigned x = q0 + lane < w.nqt ? unit_tiles(v, a, w.T, w.n, w.rows, q0 + lane, RT) : 0;
+      const unsigned x = q0 + lane < w.nqt ? unit_tiles(a.causal, v.n_rep, w.T, w.n, w.rows, q0 + lane, RT) : 0;
       unsigned incl = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -470,9 +492,9 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         mbar_init(&mi.v_full[i], kConvWarps);
         mbar_init(&mi.v_empty[i], 1);
         mbar_init(&mi.s_full[i], 1);
-        mbar_init(&mi.p_full[i], kRows);
+        mbar_init(&mi.p_full[i], 8);
         mbar_init(&mi.o_full[i], 1);
-        mbar_init(&mi.q_full[i], kRows / 32);
+        mbar_init(&mi.q_full[i], 8);
       }
       fence_mbar_init();
     }
@@ -488,7 +510,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
   w.h = mi.start_h;
   w.qt = mi.start_qt;
   load_sequence(v, a, RT, w);
-  w.tiles = unit_tiles(v, a, w.T, w.n, w.rows, w.qt, RT);
+  w.tiles = unit_tiles(a.causal, v.n_rep, w.T, w.n, w.rows, w.qt, RT);
   int j0 = mi.start_tile;
   unsigned long long left = w1 - w0;
 
@@ -569,6 +591,10 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         ok = wait(&mi.raw_k_full, it & 1) && wait(&mi.k_empty[st], ph ^ 1);
         if (!ok) break;
         const uint32_t skip_k = mi.skip_k[slot], skip_v = mi.skip_v[slot];
+        const bool plain = t0 + kTok <= w.nq;  // every piece is a page's
+        if (plain && skip_k == 0) {
+          convert_pieces<F, D>(sm + L::kRawK, kd, warp - kConv0, lane);
+        } else
 #pragma unroll 1
         for (int i = 0; i < kPieces / kConvWarps; ++i) {
           const int piece = (warp - kConv0) + i * kConvWarps, tok = t0 + 16 * piece;
@@ -587,6 +613,9 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         hand_over(&mi.k_full[st], lane);
         ok = wait(&mi.raw_v_full, it & 1) && wait(&mi.v_empty[st], ph ^ 1);
         if (!ok) break;
+        if (plain && skip_v == 0) {
+          convert_pieces<F, D>(sm + L::kRawV, vd, warp - kConv0, lane);
+        } else
 #pragma unroll 1
         for (int i = 0; i < kPieces / kConvWarps; ++i) {
           const int piece = (warp - kConv0) + i * kConvWarps, tok = t0 + 16 * piece;
@@ -641,7 +670,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           if (elected) {
 #pragma unroll
             for (int x = 0; x < kTok / 16; ++x)
-              tc::mma_ts(tm + 256 + D * s, tm + 128 * s + 8 * x, b + x * (2048 >> 4), id_o, u > 1 || x > 0);
+              tc::mma_ts(tm + 256 + D * s, tm + 128 * s + 8 * x + (x < 4 ? 0 : 32), b + x * (2048 >> 4), id_o, u > 1 || x > 0);
             if (last_use) tc::commit(&mi.v_empty[it & 1]);
           }
           __syncwarp();
@@ -673,11 +702,13 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
       j0 = 0;
       next_unit(v, a, RT, w);
     }
-  } else {  // ---- softmax streams
-    const int s = warp >> 2, row_l = threadIdx.x & (kRows - 1);
+  } else {  // ---- softmax streams: warp = 8 stream + 4 half + quarter of the rows
+    const int s = warp >> 3, hf = (warp >> 2) & 1, row_l = threadIdx.x & (kRows - 1);
     const uint32_t lane_off = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, in the address's upper half
-    const uint32_t tS = tmem + lane_off + 128 * s, tO = tmem + lane_off + 256 + D * s;
-    uint32_t ns = 0, nseg = 0, it0 = 0, no = 0;
+    constexpr int kOutC = D / 2;                           // channels of this thread's output
+    const uint32_t tS = tmem + lane_off + 128 * s + 64 * hf, tO = tmem + lane_off + 256 + D * s + kOutC * hf;
+    float* rx = &mi.row_x[s][row_l];
+    uint32_t ns = 0, it0 = 0, no = 0;
     bool ok = true;
     for (;;) {
       const int j1 = (int)min((unsigned long long)w.tiles, j0 + left), nt = j1 - j0;
@@ -685,7 +716,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
       const bool live = row < w.rows;
       const int qi = live ? row / v.n_rep : 0;
       const long long q_elem = (((long long)w.b * a.n_q + qi) * v.Hq + w.h * v.n_rep + (live ? row % v.n_rep : 0)) * D;
-      // ---- this thread's query row into f16, K-major; rows past the last are zeros
+      // ---- half of this thread's query row into f16, K-major; rows past the last are zeros
       float fct;
       {
         const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + q_elem);
@@ -702,8 +733,8 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         fct = up * a.scale * 1.4426950408889634f;
         if (two || s == 0) {
           uint8_t* qd = sm + L::kQ + (two ? s : 0) * L::kTileB;
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
+#pragma unroll 4
+          for (int c = hf * (D / 16); c < (hf + 1) * (D / 16); ++c) {
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
             if (live) x = qp[c];
             *reinterpret_cast<uint4*>(qd + tile_chunk(row_l, c)) =
@@ -716,26 +747,36 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
       const int warp_end = __reduce_min_sync(0xffffffffu, end);
       float M = kMinitM, l = 0.f;
       bool any = false;  // this stream has had a tile of this segment
-      for (int i = two ? 0 : s; i < nt && ok; i += two ? 1 : 2) {
-        const int t0 = (j0 + i) * kTok, slot = (it0 + i) % kSlots;
+      for (int i = two ? 0 : s; i < nt; i += two ? 1 : 2) {
+        const int t0 = (j0 + i) * kTok + 64 * hf, slot = (it0 + i) % kSlots;
         ok = wait(&mi.s_full[s], ns & 1);
         ++ns;
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
         tc::fence_after();
-        const float4* sc = mi.scale[slot];
+        const float4* sc = mi.scale[slot] + 4 * hf;
         const int lim = end - t0;
-        const bool masked = t0 + kTok > warp_end;
-        const float mx = masked ? tile_max<true>(tS, sc, fct, lim) : tile_max<false>(tS, sc, fct, lim);
-        if (__any_sync(0xffffffffu, mx > M + kLazyM)) {
-          const float mn = fmaxf(M, mx), al = ex2(M - mn);
+        const bool masked = t0 + 64 > warp_end;
+        const float mx = masked ? half_max<true>(tS, sc, fct, lim) : half_max<false>(tS, sc, fct, lim);
+        // (a stream whose wait gave up stops as one: the barrier carries that too)
+        if (stream_any(kBarStream + s, mx > M + kLazyM || !ok)) {
+          if (stream_any(kBarStream + s, !ok)) {
+            ok = false;
+            break;
+          }
+          if (hf) *rx = mx;
+          named_bar_sync(kBarStream + s, 2 * kRows);
+          float mn = M;
+          if (!hf) {
+            mn = fmaxf(M, fmaxf(mx, *rx));
+            *rx = mn;
+          }
+          named_bar_sync(kBarStream + s, 2 * kRows);
+          if (hf) mn = *rx;
+          const float al = ex2(M - mn);
           M = mn;
           l *= al;
           if (any) {
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
+            for (int c = 0; c < kOutC; c += 32) {
               uint32_t r[32];
               tc::tmem_ld32(tO + c, r);
               tc::wait_ld(r);
@@ -746,10 +787,11 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           }
         }
         any = true;
-        l += masked ? tile_weights<true>(tS, sc, fct, M, lim) : tile_weights<false>(tS, sc, fct, M, lim);
+        l += masked ? half_weights<true>(tS, sc, fct, M, lim) : half_weights<false>(tS, sc, fct, M, lim);
         tc::wait_st();
         tc::fence_before();
-        mbar_arrive(&mi.p_full[s]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mi.p_full[s]);
       }
       // ---- the segment's output
       if (ok && any) {
@@ -758,17 +800,25 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         tc::fence_after();
       }
       ok = __all_sync(0xffffffffu, ok);
+      named_bar_sync(kBarStream + s, 2 * kRows);
+      if (hf) *rx = l;
+      named_bar_sync(kBarStream + s, 2 * kRows);
+      if (!hf) {
+        l += *rx;
+        *rx = l;
+      }
+      named_bar_sync(kBarStream + s, 2 * kRows);
+      if (hf) l = *rx;
       if (!two) {
-        // stream 1's (M, l, O) through the second half's place in shared memory, 32 channels at a time
-        float* ex = reinterpret_cast<float*>(sm + L::kQ + L::kTileB);
-        float* ml = ex + 32 * kRows;
-        float a1 = 0.f;
-        if (s == 1) {
+        // stream 1's (M, l, O) through the second half's place in shared memory, 16 channels a thread at a time
+        float* ex = reinterpret_cast<float*>(sm + L::kQ + L::kTileB) + hf * (16 * kRows);
+        float* ml = reinterpret_cast<float*>(sm + L::kQ + L::kTileB) + 32 * kRows;
+        if (s == 1 && !hf) {
           ml[row_l] = any ? M : kMinitM;
           ml[kRows + row_l] = any ? l : 0.f;
         }
-        named_bar_sync(1, 2 * kRows);
-        float a0 = 1.f;
+        named_bar_sync(kBarJoin, 4 * kRows);
+        float a0 = 1.f, a1 = 0.f;
         if (s == 0) {
           const float M1 = ml[row_l], l1 = ml[kRows + row_l], mn = fmaxf(M, M1);
           a0 = ex2(M - mn);
@@ -776,26 +826,25 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           M = mn;
           l = l * a0 + l1 * a1;
         }
-        const bool have1 = nt > 1;
-        if (have1) {
-#pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t r[32];
-            tc::tmem_ld32(tO + c, r);
+        if (nt > 1) {
+#pragma unroll 1
+          for (int c = 0; c < kOutC; c += 16) {
+            uint32_t r[16];
+            tc::tmem_ld16(tO + c, r);
             tc::wait_ld(r);
             if (s == 1) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) ex[e * kRows + row_l] = __uint_as_float(r[e]);
+              for (int e = 0; e < 16; ++e) ex[e * kRows + row_l] = __uint_as_float(r[e]);
             }
-            named_bar_sync(1, 2 * kRows);
+            named_bar_sync(kBarJoin, 4 * kRows);
             if (s == 0) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
+              for (int e = 0; e < 16; ++e)
                 r[e] = __float_as_uint(__uint_as_float(r[e]) * a0 + ex[e * kRows + row_l] * a1);
-              tc::tmem_st32(tO + c, r);
+              tc::tmem_st16(tO + c, r);
               tc::wait_st();
             }
-            named_bar_sync(1, 2 * kRows);
+            named_bar_sync(kBarJoin, 4 * kRows);
           }
         }
       }
@@ -810,17 +859,17 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
                      (long long)rs * (D + 4);
         if (!whole) {
           if (threadIdx.x == 0) hdr[first ? 0 : 1] = RecHeader{1, w.b, w.h, w.qt, begins, ends, {0, 0}};
-          if (live) *reinterpret_cast<float4*>(rec) = make_float4(M, l, 0.f, 0.f);
+          if (live && !hf) *reinterpret_cast<float4*>(rec) = make_float4(M, l, 0.f, 0.f);
         }
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
+#pragma unroll 1
+        for (int c = 0; c < kOutC; c += 32) {
           uint32_t r[32];
           __syncwarp();
           tc::tmem_ld32(tO + c, r);
           tc::wait_ld(r);
           if (!live) {
           } else if (whole) {
-            uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + q_elem + c);
+            uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + q_elem + kOutC * hf + c);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint32_t y[4];
@@ -833,7 +882,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
               op[e] = make_uint4(y[0], y[1], y[2], y[3]);
             }
           } else {
-            uint4* op = reinterpret_cast<uint4*>(rec + 4 + c);
+            uint4* op = reinterpret_cast<uint4*>(rec + 4 + kOutC * hf + c);
 #pragma unroll
             for (int e = 0; e < 8; ++e) op[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
           }
@@ -842,7 +891,6 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
       tc::fence_before();
       it0 += nt;
       left -= nt;
-      ++nseg;
       if (!ok || left == 0) break;
       j0 = 0;
       next_unit(v, a, RT, w);
@@ -852,6 +900,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
   __syncthreads();
   tc::fence_after();
   if (mi.abort) {  // a wait gave up: copies and products in flight end (microseconds) before the memory is released
+#pragma unroll 1
     for (int i = 0; i < 4096; ++i) __nanosleep(250);
     __syncthreads();
   }
@@ -916,7 +965,7 @@ kvq_status launch_many_t(const KvqView& v, const QueryArgs& a, unsigned char* ws
   const int RT = (long long)a.n_q * v.n_rep > kRows ? 2 * kRows : kRows;
   const auto kern = query_many_kernel<F, D>;
   // at least what keeps a second CTA off the SM: each takes all of its tensor memory
-  constexpr size_t need = Lay<D>::kMisc + sizeof(Misc) + 1024, smem = need > 120 * 1024 ? need : 120 * 1024;
+  constexpr size_t need = Lay<D>::kMisc + sizeof(Misc), smem = need > 120 * 1024 ? need : 120 * 1024;
   static_assert(smem <= 232448, "shared memory of an SM");
   const kvq_status ss = ensure_dynamic_smem(kSlotQueryTc + F * 2 + (D == 64 ? 0 : 1), kern, smem);
   if (ss != KVQ_OK) return ss == KVQ_ERR_CAPACITY ? KVQ_ERR_CUDA : ss;
