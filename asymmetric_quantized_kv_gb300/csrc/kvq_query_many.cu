@@ -188,6 +188,33 @@ __device__ __forceinline__ bool mbar_try_wait_hint(uint64_t* bar, uint32_t parit
   return ok != 0;
 }
 
+// A CTA's run over the units.  A unit counts its tiles and kUnitCost more, for what its start and end cost
+// (queries in, outputs out, and products and softmax without each other); these stand before its tiles.
+constexpr int kUnitCost = 2;
+struct Run {
+  Walk w;
+  unsigned long long left;  // of the run, from place p of unit w on
+  int p;
+  int j0, j1;               // the unit's tiles in the run (may be none)
+  __device__ __forceinline__ void open() {
+    const int n = (int)min((unsigned long long)(w.tiles + kUnitCost - p), left);
+    j0 = max(0, p - kUnitCost);
+    j1 = max(0, p + n - kUnitCost);
+  }
+  // To the next unit with tiles; false at the run's end.
+  __device__ __forceinline__ bool next(const KvqView& v, const QueryArgs& a, int RT) {
+    do {
+      const unsigned long long n = min((unsigned long long)(w.tiles + kUnitCost - p), left);
+      left -= n;
+      if (left == 0) return false;
+      p = 0;
+      next_unit(v, a, RT, w);
+      open();
+    } while (j0 == j1);
+    return true;
+  }
+};
+
 // Bounded wait of a task; after a wait that gave up nothing more is waited for.
 struct Waiter {
   Misc& m;
@@ -302,67 +329,55 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // Loops are short: the tasks' code together has to stay in the instruction caches.
 
 // Largest x.
-template <bool kMasked>
-__device__ __forceinline__ float half_max(uint32_t tS, const float4* sc, float fct, int lim) {
+__device__ __noinline__ float half_max(uint32_t tS, const float4* sc, float fct, int lim) {
   float mx = -INFINITY;
 #pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
-    uint32_t r[32];
-    tc::tmem_ld32(tS + 32 * c, r);
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[16];
+    tc::tmem_ld16(tS + 16 * c, r);
     tc::wait_ld(r);
+    float m = -INFINITY;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float x[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[e] = __uint_as_float(r[16 * h + e]);
-        if (kMasked && 32 * c + 16 * h + e >= lim) x[e] = -INFINITY;
-      }
-      float m0 = max3(x[0], x[1], x[2]), m1 = max3(x[3], x[4], x[5]);
-      m0 = max3(m0, x[6], x[7]);
-      m1 = max3(m1, x[8], x[9]);
-      m0 = max3(m0, x[10], x[11]);
-      m1 = max3(m1, x[12], x[13]);
-      m0 = max3(m0, x[14], x[15]);
-      // an all-masked piece times a zero scale is NaN, which fmaxf passes over
-      const float4 k = sc[2 * c + h];
-      mx = fmaxf(mx, fmaf(fmaxf(m0, m1), k.x * fct, k.y));
-    }
+    for (int e = 0; e < 16; ++e) m = 16 * c + e < lim ? fmaxf(m, __uint_as_float(r[e])) : m;
+    // an all-masked piece times a zero scale is NaN, which fmaxf passes over
+    const float4 k = sc[c];
+    mx = fmaxf(mx, fmaf(m, k.x * fct, k.y));
   }
   return mx;
 }
 
-// Weights 2^(x - M) as f16, over the first 32 of the columns they come from (a piece's lie over logits
-// that have been read); returns the sum of weight / value scale.
+// Weights 2^(x - M) as f16 pairs in pk, to go over the first 32 of the columns they come from; returns the
+// sum of weight / value scale, and in top the largest x - M.
 template <bool kMasked>
-__device__ __forceinline__ float half_weights(uint32_t tS, const float4* sc, float fct, float M, int lim) {
-  float l = 0.f;
-#pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
-    uint32_t r[32], pk[16];
-    tc::tmem_ld32(tS + 32 * c, r);
-    tc::wait_ld(r);
+__device__ __forceinline__ float half_weights(uint32_t tS, const float4* sc, float fct, float M, int lim, uint32_t (&pk)[32],
+                                              float& top) {
+  float l = 0.f, t0 = -INFINITY, t1 = -INFINITY;
+  uint32_t r[2][16];
+  tc::tmem_ld16(tS, r[0]);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 k = sc[2 * c + h];
-      const float cc = k.x * fct, bb = k.y - M;
-      float2 sum = make_float2(0.f, 0.f);
+  for (int c = 0; c < 4; ++c) {
+    tc::wait_ld(r[c & 1]);
+    if (c < 3) tc::tmem_ld16(tS + 16 * c + 16, r[(c + 1) & 1]);
+    const float4 k = sc[c];
+    const float cc = k.x * fct, bb = k.y - M;
+    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int i = 16 * h + 2 * e;
-        float2 x = fma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(cc, cc), make_float2(bb, bb));
-        if (kMasked) {
-          if (32 * c + i >= lim) x.x = -INFINITY;
-          if (32 * c + i + 1 >= lim) x.y = -INFINITY;
-        }
-        const float2 p = make_float2(ex2(x.x), ex2(x.y));
-        sum = add2(sum, p);
-        pk[8 * h + e] = pack_f16x2(p.x, p.y);
+    for (int e = 0; e < 8; ++e) {
+      float2 x = fma2(make_float2(__uint_as_float(r[c & 1][2 * e]), __uint_as_float(r[c & 1][2 * e + 1])), make_float2(cc, cc),
+                      make_float2(bb, bb));
+      if (kMasked) {
+        if (16 * c + 2 * e >= lim) x.x = -INFINITY;
+        if (16 * c + 2 * e + 1 >= lim) x.y = -INFINITY;
       }
-      l = fmaf(sum.x + sum.y, k.z, l);
+      if (e & 1) t1 = max3(t1, x.x, x.y);
+      else t0 = max3(t0, x.x, x.y);
+      const float2 p = make_float2(ex2(x.x), ex2(x.y));
+      sum = add2(sum, p);
+      pk[8 * c + e] = pack_f16x2(p.x, p.y);
     }
-    tc::tmem_st16(tS + 16 * c, pk);
+    l = fmaf(sum.x + sum.y, k.z, l);
   }
+  top = fmaxf(t0, t1);
   return l;
 }
 
@@ -390,7 +405,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
   grid_dep_launch();
 
   // ---- the CTA's run of tiles
-  unsigned long long* wb = reinterpret_cast<unsigned long long*>(sm);  // tiles of a kv-head of each sequence
+  unsigned long long* wb = reinterpret_cast<unsigned long long*>(sm);  // places of a kv-head of each sequence
   if (threadIdx.x == 0) {
     mi.total = 0ull;
     mi.abort = 0;
@@ -407,7 +422,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
       load_sequence(v, a, RT, w);
       unsigned long long s = 0;
 #pragma unroll 1
-      for (int qt = warps ? lane : 0; qt < w.nqt; qt += warps ? 32 : 1) s += unit_tiles(a.causal, v.n_rep, w.T, w.n, w.rows, qt, RT);
+      for (int qt = warps ? lane : 0; qt < w.nqt; qt += warps ? 32 : 1) s += unit_tiles(a.causal, v.n_rep, w.T, w.n, w.rows, qt, RT) + kUnitCost;
       if (warps) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -456,7 +471,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
     int qt = 0;
 #pragma unroll 1
     for (int q0 = 0; q0 < w.nqt; q0 += 32) {
-      const unsigned x = q0 + lane < w.nqt ? unit_tiles(a.causal, v.n_rep, w.T, w.n, w.rows, q0 + lane, RT) : 0;
+      const unsigned x = q0 + lane < w.nqt ? unit_tiles(a.causal, v.n_rep, w.T, w.n, w.rows, q0 + lane, RT) + kUnitCost : 0;
       unsigned incl = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -505,33 +520,37 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
   const uint32_t tmem = mi.tmem;
   const Waiter wait{mi, v.status};
 
-  Walk w;
+  Run run;
+  Walk& w = run.w;
   w.b = mi.start_b;
   w.h = mi.start_h;
   w.qt = mi.start_qt;
   load_sequence(v, a, RT, w);
   w.tiles = unit_tiles(a.causal, v.n_rep, w.T, w.n, w.rows, w.qt, RT);
-  int j0 = mi.start_tile;
-  unsigned long long left = w1 - w0;
+  run.p = mi.start_tile;
+  run.left = w1 - w0;
+  run.open();
+  const bool some = run.j0 < run.j1 || run.next(v, a, RT);  // a run may lie in what stands before the tiles
 
   // Every task walks the same segments: tiles [j0, j1) of unit w.
+  if (!some) {
+  } else
   if (warp == kLoadWarp) {
     // Tiles pass through three steps, one tile apart, so that no load's latency is waited for: page ids
     // (lane i: the tile's i-th page, and the page of piece i's scales), then scales, then the copies.
     Pending p2, p1, p0;
     p1.some = p0.some = false;
-    unsigned long long todo = left;  // tiles not yet looked up
-    int j = j0;
+    bool todo = true;  // tiles not yet looked up: j of the run's unit
+    int j = run.j0;
     bool ok = true;
     uint32_t it = 0;  // tiles copied: phase of the single raw stage, slot of the scales
     for (;;) {
-      p2.some = todo > 0;
-      if (p2.some) {
+      p2.some = todo;
+      if (todo) {
         p2.look_up(v, w, j, lane);
-        --todo;
-        if (++j == w.tiles && todo > 0) {
-          j = 0;
-          next_unit(v, a, RT, w);
+        if (++j == run.j1) {
+          todo = run.next(v, a, RT);
+          j = run.j0;
         }
       }
       if (p1.some) p1.read_scales(v, D, lane);
@@ -581,9 +600,8 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
   } else if (warp >= kConv0 && warp < kConv0 + kConvWarps) {
     uint32_t it = 0;
     bool ok = true;
-    for (;;) {
-      const int j1 = (int)min((unsigned long long)w.tiles, j0 + left);
-      for (int j = j0; j < j1 && ok; ++j, ++it) {
+    do {
+      for (int j = run.j0; j < run.j1; ++j, ++it) {
         const int t0 = j * kTok, slot = it % kSlots, st = it & 1;
         const uint32_t ph = (it >> 1) & 1;
         uint8_t* kd = sm + L::kK + st * L::kTileB;
@@ -631,11 +649,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         if (lane == 0) mbar_arrive(&mi.raw_v_empty);
         hand_over(&mi.v_full[st], lane);
       }
-      left -= j1 - j0;
-      if (!ok || left == 0) break;
-      j0 = 0;
-      next_unit(v, a, RT, w);
-    }
+    } while (ok && run.next(v, a, RT));
   } else if (warp == kMmaWarp) {
     // The whole warp walks the steps with values it knows to be uniform, and one elected lane issues: the
     // descriptors then stay in uniform registers (issued from a divergent lane, a product cost 160 cycles).
@@ -649,9 +663,8 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
     uint32_t np = 0, nseg = 0;       // phase bits of the streams' hand-overs; segments
     bool ok = true;
     // Step u of a segment is stream u & 1's: P V of its tile, then S of step u + 2, which takes P's place.
-    for (;;) {
-      const int j1 = (int)min((unsigned long long)w.tiles, j0 + left);
-      const int nt = __shfl_sync(0xffffffffu, j1 - j0, 0);
+    do {
+      const int nt = __shfl_sync(0xffffffffu, run.j1 - run.j0, 0);
       const int steps = two ? 2 * nt : nt;
       ok = wait(&mi.q_full[0], nseg & 1) && (!two || wait(&mi.q_full[1], nseg & 1));
       ok = __all_sync(0xffffffffu, ok);
@@ -659,90 +672,90 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
 #pragma unroll 1
       for (int u = -2; u < steps && ok; ++u) {
         const int s = u & 1;
-        const bool last_use = !two || s == 1;  // of the step's tile
-        if (u >= 0) {
-          const uint32_t it = it0 + (two ? u >> 1 : u);
-          ok = wait(&mi.p_full[s], (np >> s) & 1) && wait(&mi.v_full[it & 1], (it >> 1) & 1);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const bool last_use = !two || s == 1;  // of the step's tiles
+        const uint32_t it = it0 + (two ? u >> 1 : u), nx = it + (two ? 1 : 2);
+        const bool now = u >= 0, more = u + 2 < steps;
+        const uint64_t b = dv + (it & 1) * (L::kTileB >> 4);
+        const uint64_t q = dq + (two ? s : 0) * (L::kTileB >> 4), k = dk + (nx & 1) * (L::kTileB >> 4);
+        // what is ready early is waited for first, the weights last
+        if (more) ok = wait(&mi.k_full[nx & 1], (nx >> 1) & 1);
+        if (now) {
+          ok = ok && wait(&mi.v_full[it & 1], (it >> 1) & 1) && wait(&mi.p_full[s], (np >> s) & 1);
           np ^= 1u << s;
-          tc::fence_after();
-          const uint64_t b = dv + (it & 1) * (L::kTileB >> 4);
-          if (elected) {
+        }
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc::fence_after();
+        if (elected) {
+          if (now) {
 #pragma unroll
             for (int x = 0; x < kTok / 16; ++x)
               tc::mma_ts(tm + 256 + D * s, tm + 128 * s + 8 * x + (x < 4 ? 0 : 32), b + x * (2048 >> 4), id_o, u > 1 || x > 0);
             if (last_use) tc::commit(&mi.v_empty[it & 1]);
           }
-          __syncwarp();
-        }
-        if (u + 2 < steps) {
-          const uint32_t it = it0 + (two ? (u + 2) >> 1 : u + 2);
-          ok = wait(&mi.k_full[it & 1], (it >> 1) & 1);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          tc::fence_after();
-          const uint64_t q = dq + (two ? s : 0) * (L::kTileB >> 4), k = dk + (it & 1) * (L::kTileB >> 4);
-          if (elected) {
+          if (more) {
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
               const uint32_t off = ((x >> 2) * kPanel + (x & 3) * 32) >> 4;
               tc::mma_ss(tm + 128 * s, q + off, k + off, id_s, x > 0);
             }
             tc::commit(&mi.s_full[s]);
-            if (last_use) tc::commit(&mi.k_empty[it & 1]);
+            if (last_use) tc::commit(&mi.k_empty[nx & 1]);
+          } else if (now) {
+            tc::commit(&mi.o_full[s]);
           }
-          __syncwarp();
-        } else if (u >= 0) {
-          if (elected) tc::commit(&mi.o_full[s]);
-          __syncwarp();
         }
+        __syncwarp();
       }
       it0 += nt;
-      left -= nt;
-      if (!ok || left == 0) break;
-      j0 = 0;
-      next_unit(v, a, RT, w);
-    }
+    } while (ok && run.next(v, a, RT));
   } else {  // ---- softmax streams: warp = 8 stream + 4 half + quarter of the rows
-    const int s = warp >> 3, hf = (warp >> 2) & 1, row_l = threadIdx.x & (kRows - 1);
+    const int s = __shfl_sync(0xffffffffu, warp >> 3, 0), hf = (warp >> 2) & 1, row_l = threadIdx.x & (kRows - 1);
     const uint32_t lane_off = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, in the address's upper half
     constexpr int kOutC = D / 2;                           // channels of this thread's output
     const uint32_t tS = tmem + lane_off + 128 * s + 64 * hf, tO = tmem + lane_off + 256 + D * s + kOutC * hf;
     float* rx = &mi.row_x[s][row_l];
     uint32_t ns = 0, it0 = 0, no = 0;
     bool ok = true;
-    for (;;) {
-      const int j1 = (int)min((unsigned long long)w.tiles, j0 + left), nt = j1 - j0;
+    do {
+      const int j0 = run.j0, j1 = run.j1, nt = j1 - j0;
       const int row = w.qt * RT + (two ? s * kRows : 0) + row_l;  // of the sequence and kv-head
       const bool live = row < w.rows;
       const int qi = live ? row / v.n_rep : 0;
-      const long long q_elem = (((long long)w.b * a.n_q + qi) * v.Hq + w.h * v.n_rep + (live ? row % v.n_rep : 0)) * D;
-      // ---- half of this thread's query row into f16, K-major; rows past the last are zeros
-      float fct;
+      // ---- the stream's query rows into f16, K-major, 16 rows a warp with the lanes along them; rows past the
+      // last are zeros.  Each row's power of two goes to its threads.
       {
-        const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + q_elem);
-        uint32_t m2 = 0u;
-        if (live) {
+        constexpr int CPR = D / 8, RPP = 32 / CPR, NP = 16 / RPP;  // chunks a row, rows a pass, passes
+        const int r0 = (warp & 7) * 16 + lane / CPR, c = lane % CPR;
+        uint8_t* qd = sm + L::kQ + (two ? s : 0) * L::kTileB;
+        uint4 x[NP];
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 x = qp[c];
-            m2 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(m2, x.x), x.y), x.z), x.w);
+        for (int i = 0; i < NP; ++i) {
+          const int rr = w.qt * RT + (two ? s * kRows : 0) + r0 + i * RPP;
+          x[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (rr < w.rows) {
+            const long long e = (((long long)w.b * a.n_q + rr / v.n_rep) * v.Hq + w.h * v.n_rep + rr % v.n_rep) * D + 8 * c;
+            x[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + e);
           }
         }
-        float down, up;
-        norm_factors(max(m2 & 0xffffu, m2 >> 16), down, up);
-        fct = up * a.scale * 1.4426950408889634f;
-        if (two || s == 0) {
-          uint8_t* qd = sm + L::kQ + (two ? s : 0) * L::kTileB;
-#pragma unroll 4
-          for (int c = hf * (D / 16); c < (hf + 1) * (D / 16); ++c) {
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (live) x = qp[c];
-            *reinterpret_cast<uint4*>(qd + tile_chunk(row_l, c)) =
-                make_uint4(bf16x2_scaled(x.x, down), bf16x2_scaled(x.y, down), bf16x2_scaled(x.z, down), bf16x2_scaled(x.w, down));
-          }
-          hand_over(&mi.q_full[s], lane);
+        if (it0 > 0) named_bar_sync(kBarStream + s, 2 * kRows);  // the last segment's rows have left the tile
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const uint32_t m2 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(0u, x[i].x), x[i].y), x[i].z), x[i].w);
+          uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+          for (int o = CPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          float down, up;
+          norm_factors(top, down, up);
+          if (c == 0) mi.row_x[s][r0 + i * RPP] = up;
+          if (two || s == 0)
+            *reinterpret_cast<uint4*>(qd + tile_chunk(r0 + i * RPP, c)) =
+                make_uint4(bf16x2_scaled(x[i].x, down), bf16x2_scaled(x[i].y, down), bf16x2_scaled(x[i].z, down),
+                           bf16x2_scaled(x[i].w, down));
         }
+        if (two || s == 0) hand_over(&mi.q_full[s], lane);
+        named_bar_sync(kBarStream + s, 2 * kRows);
       }
+      const float fct = *rx * a.scale * 1.4426950408889634f;
       const int end = live ? query_end(a, w.T, w.n, qi) : 0x3FFFFFFF;  // rows past the last: never masked, never written
       const int warp_end = __reduce_min_sync(0xffffffffu, end);
       float M = kMinitM, l = 0.f;
@@ -755,13 +768,18 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         const float4* sc = mi.scale[slot] + 4 * hf;
         const int lim = end - t0;
         const bool masked = t0 + 64 > warp_end;
-        const float mx = masked ? half_max<true>(tS, sc, fct, lim) : half_max<false>(tS, sc, fct, lim);
+        // With the standing maximum first: it holds for nearly every tile.  The weights stay in registers
+        // until both halves of every row have agreed to it.
+        uint32_t pk[32];
+        float top, sum;
+        sum = masked ? half_weights<true>(tS, sc, fct, M, lim, pk, top) : half_weights<false>(tS, sc, fct, M, lim, pk, top);
         // (a stream whose wait gave up stops as one: the barrier carries that too)
-        if (stream_any(kBarStream + s, mx > M + kLazyM || !ok)) {
+        if (stream_any(kBarStream + s, top > kLazyM || !ok)) {
           if (stream_any(kBarStream + s, !ok)) {
             ok = false;
             break;
           }
+          const float mx = half_max(tS, sc, fct, lim);
           if (hf) *rx = mx;
           named_bar_sync(kBarStream + s, 2 * kRows);
           float mn = M;
@@ -776,18 +794,20 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           l *= al;
           if (any) {
 #pragma unroll 1
-            for (int c = 0; c < kOutC; c += 32) {
-              uint32_t r[32];
-              tc::tmem_ld32(tO + c, r);
+            for (int c = 0; c < kOutC; c += 16) {
+              uint32_t r[16];
+              tc::tmem_ld16(tO + c, r);
               tc::wait_ld(r);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * al);
-              tc::tmem_st32(tO + c, r);
+              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * al);
+              tc::tmem_st16(tO + c, r);
             }
           }
+          sum = half_weights<true>(tS, sc, fct, M, lim, pk, top);
         }
         any = true;
-        l += masked ? half_weights<true>(tS, sc, fct, M, lim) : half_weights<false>(tS, sc, fct, M, lim);
+        l += sum;
+        tc::tmem_st32(tS, pk);
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
@@ -861,17 +881,17 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           if (threadIdx.x == 0) hdr[first ? 0 : 1] = RecHeader{1, w.b, w.h, w.qt, begins, ends, {0, 0}};
           if (live && !hf) *reinterpret_cast<float4*>(rec) = make_float4(M, l, 0.f, 0.f);
         }
+        // a whole unit's rows leave through the Q tile (its products are done), lanes along the rows
+        uint8_t* qd = sm + L::kQ + (two ? s : 0) * L::kTileB;
 #pragma unroll 1
-        for (int c = 0; c < kOutC; c += 32) {
-          uint32_t r[32];
+        for (int c = 0; c < kOutC; c += 16) {
+          uint32_t r[16];
           __syncwarp();
-          tc::tmem_ld32(tO + c, r);
+          tc::tmem_ld16(tO + c, r);
           tc::wait_ld(r);
-          if (!live) {
-          } else if (whole) {
-            uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + q_elem + kOutC * hf + c);
+          if (whole) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
               uint32_t y[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -879,22 +899,32 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
                                                                __uint_as_float(r[8 * e + 2 * k + 1]) * inv);
                 y[k] = *reinterpret_cast<const uint32_t*>(&z);
               }
-              op[e] = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(qd + tile_chunk(row_l, (kOutC * hf + c) / 8 + e)) = make_uint4(y[0], y[1], y[2], y[3]);
             }
-          } else {
+          } else if (live) {
             uint4* op = reinterpret_cast<uint4*>(rec + 4 + kOutC * hf + c);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) op[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) op[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+          }
+        }
+        if (whole) {
+          named_bar_sync(kBarStream + s, 2 * kRows);
+          constexpr int CPR = D / 8, RPP = 32 / CPR, NP = 16 / RPP;
+          const int r0 = (warp & 7) * 16 + lane / CPR, c = lane % CPR;
+#pragma unroll 4
+          for (int i = 0; i < NP; ++i) {
+            const int rr = w.qt * RT + (two ? s * kRows : 0) + r0 + i * RPP;
+            if (rr < w.rows) {
+              const long long e = (((long long)w.b * a.n_q + rr / v.n_rep) * v.Hq + w.h * v.n_rep + rr % v.n_rep) * D + 8 * c;
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + e) =
+                  *reinterpret_cast<const uint4*>(qd + tile_chunk(r0 + i * RPP, c));
+            }
           }
         }
       }
       tc::fence_before();
       it0 += nt;
-      left -= nt;
-      if (!ok || left == 0) break;
-      j0 = 0;
-      next_unit(v, a, RT, w);
-    }
+    } while (ok && run.next(v, a, RT));
   }
   tc::fence_before();
   __syncthreads();
