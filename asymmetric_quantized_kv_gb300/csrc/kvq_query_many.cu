@@ -46,7 +46,7 @@ constexpr int kConv0 = kSoftWarps, kConvWarps = 4, kLoadWarp = kConv0 + kConvWar
 constexpr int kMThreads = (kMmaWarp + 1) * 32;
 constexpr int kBarStream = 1, kBarJoin = 3;  // named barriers: of the streams (and the next), of both
 constexpr int kSlots = 8;     // tiles whose scales are kept
-constexpr float kLazyM = 8.f;
+constexpr float kLazyM = 256.f;  // a piece's weights may sum to this before the maximum is raised
 constexpr float kMinitM = -1e30f;
 
 // A CTA's partial records: that of its first unit and that of its last, where they are cut.
@@ -174,20 +174,6 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) { 
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
-// Polls of a wait, each of which may sleep for the hint (20 us): idle warps then leave the issue slots to
-// the others, and a wait that nothing ends gives up after about a second.
-constexpr uint32_t kManyPolls = 1u << 16, kManyHint = 20000;
-
-__device__ __forceinline__ bool mbar_try_wait_hint(uint64_t* bar, uint32_t parity, uint32_t ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
-      : "memory");
-  return ok != 0;
-}
-
 // A CTA's run over the units.  A unit counts its tiles and kUnitCost more, for what its start and end cost
 // (queries in, outputs out, and products and softmax without each other); these stand before its tiles.
 constexpr int kUnitCost = 2;
@@ -221,8 +207,8 @@ struct Waiter {
   int32_t* status;
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
 #pragma unroll 1
-    for (uint32_t i = 0; i < kManyPolls; ++i) {
-      if (mbar_try_wait_hint(bar, parity, kManyHint)) return true;
+    for (uint32_t i = 0; i < kWaitPolls; ++i) {
+      if (mbar_try_wait(bar, parity)) return true;
       if (*reinterpret_cast<volatile int*>(&m.abort)) return false;
     }
     *reinterpret_cast<volatile int*>(&m.abort) = 1;
@@ -236,33 +222,31 @@ __device__ __forceinline__ uint32_t tile_chunk(int r, int c) {
   return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// ---- converter: K pieces of 16 tokens of a raw tile, 4 pieces apart, -> f16 (whole warp)
+// ---- converter: K pieces of 16 tokens of a raw tile, 4 pieces apart, -> f16 (whole warp).  A lane takes 8 codes
+// of a row, one 16-byte chunk of the tile: eight lanes' loads and stores then meet no bank twice.
 template <int F, int D, int K>
 __device__ __forceinline__ void convert_n(const uint8_t* raw, uint8_t* dst, int piece, int lane) {
-  constexpr int CPR = D / 16;         // 16-code chunks per row
-  constexpr int RPI = 32 / CPR;       // rows per pass
+  constexpr int CPR = D / 8;          // chunks per row
+  constexpr int RPI = 32 / CPR;       // rows per pass: 2 or 4
   constexpr int N = 16 / RPI;
   const int r0 = 16 * piece + lane / CPR, c = lane % CPR;
-  // the upper panel's lanes write their second half first: a store's eight lanes then meet 8 chunks
-  const int sw = D == 128 ? c >> 2 : 0;
-  uint4 x[K][N];
+  const uint8_t* src = raw + r0 * D + 8 * c;
+  uint2 x[K][N];
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      x[k][i] = *reinterpret_cast<const uint4*>(raw + (r0 + 64 * k + i * RPI) * D + 16 * c);
+    for (int i = 0; i < N; ++i) x[k][i] = *reinterpret_cast<const uint2*>(src + (64 * k + i * RPI) * D);
+  uint8_t* at[8 / RPI];  // rows 8 apart share their swizzle
+#pragma unroll
+  for (int i = 0; i < 8 / RPI; ++i) at[i] = dst + tile_chunk(r0 + i * RPI, c);
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const uint4 z = x[k][i], y = sw ? make_uint4(z.z, z.w, z.x, z.y) : z;
-      uint32_t f[8];
-      codes_to_f16<F>(y.x, f[0], f[1]);
-      codes_to_f16<F>(y.y, f[2], f[3]);
-      codes_to_f16<F>(y.z, f[4], f[5]);
-      codes_to_f16<F>(y.w, f[6], f[7]);
-      *reinterpret_cast<uint4*>(dst + tile_chunk(r0 + 64 * k + i * RPI, 2 * c + sw)) = make_uint4(f[0], f[1], f[2], f[3]);
-      *reinterpret_cast<uint4*>(dst + tile_chunk(r0 + 64 * k + i * RPI, 2 * c + 1 - sw)) = make_uint4(f[4], f[5], f[6], f[7]);
+      uint32_t f[4];
+      codes_to_f16<F>(x[k][i].x, f[0], f[1]);
+      codes_to_f16<F>(x[k][i].y, f[2], f[3]);
+      *reinterpret_cast<uint4*>(at[i % (8 / RPI)] + 64 * k * 128 + i / (8 / RPI) * 1024) = make_uint4(f[0], f[1], f[2], f[3]);
     }
 }
 template <int F, int D>
@@ -319,12 +303,6 @@ __device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // ---- softmax of half a row: 64 of a tile's logits, from column tS; columns from lim on are masked.
 // Loops are short: the tasks' code together has to stay in the instruction caches.
 
@@ -347,11 +325,12 @@ __device__ __noinline__ float half_max(uint32_t tS, const float4* sc, float fct,
 }
 
 // Weights 2^(x - M) as f16 pairs in pk, to go over the first 32 of the columns they come from; returns the
-// sum of weight / value scale, and in top the largest x - M.
+// sum of weight / value scale, and in top the largest sum of a piece's weights (above 2^8 when M lags).
 template <bool kMasked>
 __device__ __forceinline__ float half_weights(uint32_t tS, const float4* sc, float fct, float M, int lim, uint32_t (&pk)[32],
                                               float& top) {
-  float l = 0.f, t0 = -INFINITY, t1 = -INFINITY;
+  float l = 0.f;
+  top = 0.f;
   uint32_t r[2][16];
   tc::tmem_ld16(tS, r[0]);
 #pragma unroll
@@ -369,15 +348,14 @@ __device__ __forceinline__ float half_weights(uint32_t tS, const float4* sc, flo
         if (16 * c + 2 * e >= lim) x.x = -INFINITY;
         if (16 * c + 2 * e + 1 >= lim) x.y = -INFINITY;
       }
-      if (e & 1) t1 = max3(t1, x.x, x.y);
-      else t0 = max3(t0, x.x, x.y);
       const float2 p = make_float2(ex2(x.x), ex2(x.y));
       sum = add2(sum, p);
       pk[8 * c + e] = pack_f16x2(p.x, p.y);
     }
-    l = fmaf(sum.x + sum.y, k.z, l);
+    const float piece = sum.x + sum.y;
+    top = fmaxf(top, piece);
+    l = fmaf(piece, k.z, l);
   }
-  top = fmaxf(t0, t1);
   return l;
 }
 
@@ -677,10 +655,11 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         const bool now = u >= 0, more = u + 2 < steps;
         const uint64_t b = dv + (it & 1) * (L::kTileB >> 4);
         const uint64_t q = dq + (two ? s : 0) * (L::kTileB >> 4), k = dk + (nx & 1) * (L::kTileB >> 4);
-        // what is ready early is waited for first, the weights last
-        if (more) ok = wait(&mi.k_full[nx & 1], (nx >> 1) & 1);
+        // what is ready early is waited for first (256 rows: once for both streams), the weights last
+        if (more && !(two && s)) ok = wait(&mi.k_full[nx & 1], (nx >> 1) & 1);
         if (now) {
-          ok = ok && wait(&mi.v_full[it & 1], (it >> 1) & 1) && wait(&mi.p_full[s], (np >> s) & 1);
+          if (!(two && s)) ok = ok && wait(&mi.v_full[it & 1], (it >> 1) & 1);
+          ok = ok && wait(&mi.p_full[s], (np >> s) & 1);
           np ^= 1u << s;
         }
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
