@@ -267,7 +267,9 @@ def _run_own(s):
     if c["op"] == "append":
         s["lens"].copy_(s["lens0"])  # the scheduler's lengths of this step's batch
         cache.append_rope(rope, s["q"], s["k"], s["v"], s["n"], q_out=s["q_out"])
-        return _append_outputs(s)
+        if "outputs" not in s:  # views of the buffers that the call writes: a program names them once
+            s["outputs"] = _append_outputs(s)
+        return s["outputs"]
     return cache.query_attention(s["q"], causal=c["op"] == "attend")
 
 
