@@ -106,14 +106,15 @@ def _check(fn, code):
 
 
 def _ptr(t):
-    return None if t is None else c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
+    """Address of a stream (a torch stream or an address), torch's current one by default."""
     if stream is None:
         import torch
-        stream = torch.cuda.current_stream()
-    return c_void_p(getattr(stream, "cuda_stream", stream))
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return getattr(stream, "cuda_stream", stream)
 
 
 def kvq_validate(cfg: kvq_config) -> int:

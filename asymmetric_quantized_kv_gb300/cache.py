@@ -94,7 +94,8 @@ class PagedKVCache:
         self.workspace = torch.empty(
             max(B.kvq_workspace_bytes(cfg, batch, max_pages_per_seq * cfg.page_size), 256),
             dtype=torch.uint8, device=dev)
-        self._outgrown = []
+        self._outgrown, self._query_bytes = [], {}
+        self._device, self._src = pages.device, src_torch_dtype(cfg)
         self.rope_table, self.rope_positions = None, 0
         if cfg.rope_pre and rope_table is not False:
             if rope_table is True:
@@ -122,64 +123,70 @@ class PagedKVCache:
 
     def _beside(self, name, t):
         """The library launches on the current device, over the cache's memory."""
-        if t.device != self.pages.device or (t.is_cuda and t.device.index != torch.cuda.current_device()):
-            raise ValueError(f"{name} must be on the cache's device ({self.pages.device}), which must be the current one")
+        if t.device != self._device or torch._C._cuda_getDevice() != self._device.index:
+            raise ValueError(f"{name} must be on the cache's device ({self._device}), which must be the current one")
 
     def _counts(self, name, t):
         self._beside(name, t)
         if tuple(t.shape) != (self.batch,) or t.dtype != torch.int32 or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous int32 of shape {(self.batch,)}")
 
+    def _rows(self, name, t, n, heads):
+        """Elements between consecutive tokens of t [batch, n, heads, D]: a token's row contiguous, tokens evenly spaced."""
+        D = self.cfg.head_dim
+        if t.shape != (self.batch, n, heads, D) or t.dtype != self._src:
+            raise ValueError(f"{name} must be {self._src} of shape {(self.batch, n, heads, D)}")
+        sb, sn, sh, sd = t.stride()
+        row = sn if n > 1 else sb if self.batch > 1 else heads * D
+        if sd != 1 or (heads > 1 and sh != D) or (self.batch > 1 and n > 1 and sb != n * row):
+            raise ValueError(f"{name}: a token's row must be contiguous and the tokens evenly spaced")
+        self._beside(name, t)
+        return row
+
     def append_rope(self, rope, q, k_new, v_new, n_new_per_seq=None, q_out=None, stream=None):
         """append() with the position rotation on the way: k_new, v_new [batch, n_new, Hkv, D] and q
         [batch, n_new, Hq, D] (or None) may be slices of one fused projection (rows of one token contiguous,
         tokens evenly spaced).  Returns the rotated queries."""
-        n = k_new.shape[1]
-        strides = []
-        for name, t, heads in (("q", q, self.cfg.num_q_heads), ("k_new", k_new, self.cfg.num_kv_heads),
-                               ("v_new", v_new, self.cfg.num_kv_heads)):
-            if t is None and name == "q":
-                strides.append(0)
-                continue
-            D = self.cfg.head_dim
-            if tuple(t.shape) != (self.batch, n, heads, D) or t.dtype != src_torch_dtype(self.cfg):
-                raise ValueError(f"{name} must be {src_torch_dtype(self.cfg)} of shape {(self.batch, n, heads, D)}")
-            self._beside(name, t)
-            row = t.stride(1) if n > 1 else t.stride(0) if self.batch > 1 else heads * D
-            if (D > 1 and t.stride(3) != 1) or (heads > 1 and t.stride(2) != D) or (
-                    self.batch > 1 and n > 1 and t.stride(0) != n * row):
-                raise ValueError(f"{name}: a token's row must be contiguous and the tokens evenly spaced")
-            strides.append(row)
+        n, cfg = k_new.shape[1], self.cfg
         if n_new_per_seq is not None:
             self._counts("n_new_per_seq", n_new_per_seq)
+        qs = 0
         if q is not None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-            if q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
+            qs = self._rows("q", q, n, cfg.num_q_heads)
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
                 raise ValueError("q_out must be contiguous, of q's shape and dtype")
-        B.kvq_rope_append(self.cfg, self.c, rope, q, k_new, v_new, n, n_new_per_seq, q_out, *strides, stream=stream)
+            else:
+                self._beside("q_out", q_out)
+        ks, vs = self._rows("k_new", k_new, n, cfg.num_kv_heads), self._rows("v_new", v_new, n, cfg.num_kv_heads)
+        B.kvq_rope_append(cfg, self.c, rope, q, k_new, v_new, n, n_new_per_seq, q_out, qs, ks, vs, stream)
         return q_out
 
     def query_attention(self, q, causal=True, n_q_per_seq=None, out=None, softmax_scale=0.0, stream=None):
         """Attention of n_q queries per sequence, q [batch, n_q, Hq, D]: the sequence's newest n_q tokens over its
         own cache (causal), or a decoder's tokens over an encoder's states (causal=False).  The workspace grows
         with n_q on first use and is kept; calls on several streams at once need a cache object each."""
-        n = q.shape[1]
-        shape = (self.batch, n, self.cfg.num_q_heads, self.cfg.head_dim)
-        if tuple(q.shape) != shape or q.dtype != src_torch_dtype(self.cfg) or not q.is_contiguous():
-            raise ValueError(f"q must be contiguous {src_torch_dtype(self.cfg)} of shape {shape}")
+        cfg, n = self.cfg, q.shape[1]
+        if q.shape != (self.batch, n, cfg.num_q_heads, cfg.head_dim) or q.dtype != self._src or not q.is_contiguous():
+            raise ValueError(f"q must be contiguous {self._src} of shape {(self.batch, n, cfg.num_q_heads, cfg.head_dim)}")
         self._beside("q", q)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = torch.empty_like(q)
         elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
             raise ValueError("out must be contiguous, of q's shape and dtype")
+        else:
+            self._beside("out", out)
         if n_q_per_seq is not None:
             self._counts("n_q_per_seq", n_q_per_seq)
-        need = B.kvq_query_workspace_bytes(self.cfg, self.batch, max(n, 1))
+        need = self._query_bytes.get(n)
+        if need is None:
+            need = self._query_bytes[n] = B.kvq_query_workspace_bytes(cfg, self.batch, max(n, 1))
         if self.workspace.numel() < need:
             self._outgrown.append(self.workspace)  # a captured graph may still use it
             self.workspace = torch.empty(need, dtype=torch.uint8, device=self.pages.device)
-        B.kvq_query_attention(self.cfg, self.c, q, n, n_q_per_seq, B.KVQ_MASK_CAUSAL if causal else B.KVQ_MASK_NONE,
-                              out, softmax_scale, self.workspace, stream)
+        B.kvq_query_attention(cfg, self.c, q, n, n_q_per_seq, B.KVQ_MASK_CAUSAL if causal else B.KVQ_MASK_NONE, out,
+                              softmax_scale, self.workspace, stream)
         return out
 
     def decode_kernel(self) -> int:

@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(128) combine_kernel(KvqView v, float* ws, floa
 }
 
 size_t attention_workspace_bytes(const KvqView& v, int batch) {
-  if (v.kaxis == KVQ_PER_BLOCK) return query_workspace_bytes(v, batch, 1);
+  if (v.kaxis == KVQ_PER_BLOCK) return decode_workspace_bytes(v, batch);
   const int HB = (v.n_rep + kHB - 1) / kHB;
   const long long items = kTargetItems + 2LL * batch * v.Hkv * HB;
   const size_t generic = plan_header_bytes(batch) + (size_t)items * kHB * generic_rec(v.D) * sizeof(float);

@@ -12,8 +12,8 @@
 // pairs (adjacent pieces for interleaved pairs, half the rotated width apart for
 // halves), so a rotation never leaves the thread and its cosines and sines are two
 // contiguous runs of 8.  A CTA keeps a whole block's keys and values in registers
-// between the maximum and the rounding, where they fit (kItems items a thread: 64
-// tokens of 256 channels, or 128 of 128); larger blocks are read twice, the second
+// between the maximum and the rounding, where they fit (64 bf16 tokens of 128 channels);
+// larger blocks are read twice, the second
 // time from L2.
 //
 // Decode steps take one launch: a cluster per sequence, its CTAs over the kv-heads, the
@@ -106,9 +106,10 @@ struct Item<false> {
   }
 };
 
-// Items a thread holds of each of keys and values: 64 packed registers in all.
+// Items a thread holds of each of keys and values: 32 packed registers in all, so that four CTAs share an SM
+// (a batch's decode step is then resident at once, and a prompt's loads cover the memory's latency).
 template <bool BF16>
-constexpr int items_held() { return BF16 ? 4 : 2; }
+constexpr int items_held() { return BF16 ? 2 : 1; }
 
 // Channels of item p of a row: its two pieces.
 __device__ __forceinline__ void item_channels(const RopeView& r, int p, int& cl, int& ch) {
@@ -217,40 +218,77 @@ __device__ __forceinline__ float item_absmax(const Item<BF16>& it) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// The codes of 8 channels.  INT8: rint(fl32(x * r)) with r = fl32(1 / s) equals rint(fl32(x / s))
-// unless a half-integer lies between them; products within 2^-20 |q| of one (over five times the
-// distance of the two quotients) and values that are not finite take the IEEE division.
-template <bool FP8>
-__device__ __forceinline__ uint2 codes8(const float* x, float s, float r, int fmt) {
+// Two FP8 bytes (a in the low one): nearest, ties to even, saturating.
+template <bool E5M2>
+__device__ __forceinline__ uint32_t fp8x2(float a, float b) {
+  uint16_t r;
+  if constexpr (E5M2) {
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(b), "f"(a));
+  } else {
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(b), "f"(a));
+  }
+  return r;
+}
+
+// The codes of 8 channels, from r = fl32(1 / s) instead of a division each.
+// INT8: rint(fl32(x * r)) equals rint(fl32(x / s)) unless a half-integer lies between them; products within
+// 2^-20 |q| of one (over five times the distance of the two quotients) and values that are not finite take the
+// IEEE division.  FP8: the quotient lies between q (1 - 2^-20) and q (1 + 2^-20), and rounding is monotone: where
+// both ends give the same byte it is the quotient's, elsewhere the division decides.  (r is exact enough only
+// while 1 / s is a normal number: smaller or larger scales divide.)
+template <int F>  // 0 INT8, 1 E4M3, 2 E5M2
+__device__ __forceinline__ uint2 codes8(const float* x, float s, float r) {
   uint32_t w[2] = {0u, 0u};
+  if constexpr (F == 0) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t u;
-    if (FP8) {
-      u = fp8_code(x[i], s, fmt);
-    } else {
+    for (int i = 0; i < 8; ++i) {
       const float q = __fmul_rn(x[i], r);
       float c = rintf(q);
       if (!(fabsf(__fsub_rn(fabsf(__fsub_rn(q, c)), 0.5f)) > __fmul_rn(9.5367431640625e-07f, fabsf(q))))
         c = rintf(__fdiv_rn(x[i], s));
-      u = s == 0.f ? 0u : static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(c, -127.f), 127.f))) & 0xFFu;
+      const uint32_t u = s == 0.f ? 0u : static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(c, -127.f), 127.f))) & 0xFFu;
+      w[i >> 2] |= u << (8 * (i & 3));
     }
-    w[i >> 2] |= u << (8 * (i & 3));
+  } else {
+    constexpr float kLo = 1.f - 9.5367431640625e-07f, kHi = 1.f + 9.5367431640625e-07f;
+    const bool near = s > 7.888609052210118e-31f && s < 1.2676506002282294e+30f;  // 2^-100 .. 2^100
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float a = __fmul_rn(x[i], r), b = __fmul_rn(x[i + 1], r);
+      uint32_t u = fp8x2<F == 2>(__fmul_rn(a, kLo), __fmul_rn(b, kLo));
+      if (!near || u != fp8x2<F == 2>(__fmul_rn(a, kHi), __fmul_rn(b, kHi)))
+        u = s == 0.f ? 0u : fp8x2<F == 2>(__fdiv_rn(x[i], s), __fdiv_rn(x[i + 1], s));
+      w[i >> 2] |= u << (8 * (i & 2));
+    }
   }
   return make_uint2(w[0], w[1]);
 }
 
+// The 16 codes of an item.  Out of line: a launch runs this code a few times from cold instruction caches, so
+// one copy for every item of keys and values costs less than the calls.
 template <bool BF16>
-__device__ __forceinline__ void store_codes(uint8_t* row, int cl, int ch, const Item<BF16>& it, float s, float r, int fmt) {
+__device__ __noinline__ uint4 item_codes(Item<BF16> it, float s, float r, int fmt) {
   float x[kCh];
   it.get(x);
-  if (is_fp8(fmt)) {
-    *reinterpret_cast<uint2*>(row + cl) = codes8<true>(x, s, r, fmt);
-    *reinterpret_cast<uint2*>(row + ch) = codes8<true>(x + 8, s, r, fmt);
+  uint2 a, b;
+  if (fmt == KVQ_FP8_E4M3) {
+    a = codes8<1>(x, s, r);
+    b = codes8<1>(x + 8, s, r);
+  } else if (fmt == KVQ_FP8_E5M2) {
+    a = codes8<2>(x, s, r);
+    b = codes8<2>(x + 8, s, r);
   } else {
-    *reinterpret_cast<uint2*>(row + cl) = codes8<false>(x, s, r, fmt);
-    *reinterpret_cast<uint2*>(row + ch) = codes8<false>(x + 8, s, r, fmt);
+    a = codes8<0>(x, s, r);
+    b = codes8<0>(x + 8, s, r);
   }
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_codes(uint8_t* row, int cl, int ch, const Item<BF16>& it, float s, float r, int fmt) {
+  const uint4 c = item_codes<BF16>(it, s, r, fmt);
+  *reinterpret_cast<uint2*>(row + cl) = make_uint2(c.x, c.y);
+  *reinterpret_cast<uint2*>(row + ch) = make_uint2(c.z, c.w);
 }
 
 __device__ __forceinline__ float block_qmax(int fmt) {
@@ -258,22 +296,22 @@ __device__ __forceinline__ float block_qmax(int fmt) {
 }
 
 struct FoldSmem {
-  float mk[kThreads / 32], mv[kThreads / 32];
+  float mk[kThreads / 32], mv[kThreads / 32];  // of either kernel's warps
 };
 
 // Quantize block [t0, t0 + G) of one head.  Whole CTA; ends with a barrier, so the window
 // rows it read may be overwritten.
-template <bool BF16>
+template <bool BF16, int NT>
 __device__ void fold_block(const KvqView& v, const BlockAppend& a, FoldSmem& sm, int b, int h, int T0, int wbase, int t0) {
   constexpr int N = items_held<BF16>();
   const int np = v.D / kCh, lp = __ffs(np) - 1, G = v.kgroup, items = G << lp;
-  const bool held = items <= N * kThreads;
+  const bool held = items <= N * NT;
   Item<BF16> k[N], w[N];
   float mk = 0.f, mv = 0.f;
-  for (int base = 0; base < items; base += N * kThreads) {
+  for (int base = 0; base < items; base += N * NT) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int e = base + j * kThreads + threadIdx.x;
+      const int e = base + j * NT + threadIdx.x;
       k[j].zero();
       w[j].zero();
       if (e < items) {
@@ -298,7 +336,7 @@ __device__ void fold_block(const KvqView& v, const BlockAppend& a, FoldSmem& sm,
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
+  for (int i = 0; i < NT / 32; ++i) {
     mk = fmaxf(mk, sm.mk[i]);
     mv = fmaxf(mv, sm.mv[i]);
   }
@@ -317,10 +355,10 @@ __device__ void fold_block(const KvqView& v, const BlockAppend& a, FoldSmem& sm,
       store_meta(hb + v.off_vm, slot, vs, v.meta16);
     }
   }
-  for (int base = 0; base < items; base += N * kThreads) {
+  for (int base = 0; base < items; base += N * NT) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int e = base + j * kThreads + threadIdx.x;
+      const int e = base + j * NT + threadIdx.x;
       if (e >= items) continue;
       const int t = t0 + (e >> lp), p = e & (np - 1);
       if (!held) {
@@ -339,13 +377,15 @@ __device__ void fold_block(const KvqView& v, const BlockAppend& a, FoldSmem& sm,
   __syncthreads();
 }
 
-// The new rows of head h that stay in the window: tokens [max(T1 / R * R, T0), T1).
+// The new rows that stay in the window, tokens [max(T1 / R * R, T0), T1) of heads [h0, h1): thread `at` of `n`.
 template <bool BF16>
-__device__ __forceinline__ void write_window(const KvqView& v, const BlockAppend& a, int b, int h, int T0, int T1) {
+__device__ __forceinline__ void write_window(const KvqView& v, const BlockAppend& a, int b, int h0, int h1, int T0, int T1, int at,
+                                             int n) {
   const int base = T1 / v.R * v.R, first = max(base, T0);
-  const int np = v.D / kCh, lp = __ffs(np) - 1;
-  for (int e = threadIdx.x; e < ((T1 - first) << lp); e += kThreads) {
-    const int t = first + (e >> lp), p = e & (np - 1);
+  const int np = v.D / kCh, lp = __ffs(np) - 1, per = (h1 - h0) << lp;  // items of a token
+#pragma unroll 1
+  for (int e = at; e < (T1 - first) * per; e += n) {
+    const int t = first + e / per, h = h0 + (e % per >> lp), p = e & (np - 1);
     Item<BF16> k, w;
     load_item<BF16, true>(v, a, b, h, T0, base, t, p, k);
     load_item<BF16, false>(v, a, b, h, T0, base, t, p, w);
@@ -359,11 +399,11 @@ __device__ __forceinline__ void write_window(const KvqView& v, const BlockAppend
 
 // Queries [i0, i1) of sequence b, heads [h0, h1): a thread takes one item of a group of HG heads
 // of a token, so that its cosines and sines are read once a group.
-template <bool BF16, int HG>
+template <bool BF16, int NT, int HG>
 __device__ __forceinline__ void rotate_queries(const KvqView& v, const BlockAppend& a, int b, int T0, int i0, int i1,
                                                int h0, int h1) {
   const int np = v.D / kCh, lp = __ffs(np) - 1;
-  const int p = threadIdx.x & (np - 1), slot = threadIdx.x >> lp, slots = kThreads >> lp;
+  const int p = threadIdx.x & (np - 1), slot = threadIdx.x >> lp, slots = NT >> lp;
   const int groups = (h1 - h0 + HG - 1) / HG;
   const bool rot = p < a.r.rot / kCh;
   int cl, ch;
@@ -394,7 +434,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // A cluster of `ranks` CTAs per sequence.  whole: the blocks and queries too (a decode step);
 // otherwise only the window rows and the length, behind the grid that did the rest.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) block_step_kernel(KvqView v, BlockAppend a, int ranks, int whole) {
+__global__ void __launch_bounds__(kThreads, 4) block_step_kernel(KvqView v, BlockAppend a, int ranks, int whole) {
   __shared__ FoldSmem sm;
   if (!whole) ptx::grid_dep_wait();
   const int b = blockIdx.x / ranks, rank = blockIdx.x % ranks;
@@ -407,14 +447,16 @@ __global__ void __launch_bounds__(kThreads) block_step_kernel(KvqView v, BlockAp
     const int T1 = T0 + n;
     if (whole && a.q) {
       const int per = (v.Hq + ranks - 1) / ranks;
-      rotate_queries<BF16, 1>(v, a, b, T0, 0, n, min(v.Hq, rank * per), min(v.Hq, rank * per + per));
+      rotate_queries<BF16, kThreads, 1>(v, a, b, T0, 0, n, min(v.Hq, rank * per), min(v.Hq, rank * per + per));
     }
-    for (int h = rank; h < v.Hkv; h += ranks) {
-      if (whole && T1 / v.R > T0 / v.R) {  // n <= R: one window fills at most
-        const int wbase = T0 / v.R * v.R;
-        for (int t = wbase; t < wbase + v.R; t += v.kgroup) fold_block<BF16>(v, a, sm, b, h, T0, wbase, t);
+    if (whole && T1 / v.R > T0 / v.R) {  // n <= R: one window fills at most
+      const int wbase = T0 / v.R * v.R;
+      for (int h = rank; h < v.Hkv; h += ranks) {
+        for (int t = wbase; t < wbase + v.R; t += v.kgroup) fold_block<BF16, kThreads>(v, a, sm, b, h, T0, wbase, t);
+        write_window<BF16>(v, a, b, h, h + 1, T0, T1, threadIdx.x, kThreads);  // after this head's rows were read
       }
-      write_window<BF16>(v, a, b, h, T0, T1);
+    } else {
+      write_window<BF16>(v, a, b, 0, v.Hkv, T0, T1, rank * kThreads + threadIdx.x, ranks * kThreads);
     }
   }
   cluster_wait();
@@ -426,7 +468,7 @@ constexpr int kQTask = 8;  // heads a thread takes of a token in a prompt
 // Blocks and queries of a prompt: CTAs [0, nfold) take one (sequence, block, head) each, the
 // rest q_tok tokens of a sequence's queries.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) block_prompt_kernel(KvqView v, BlockAppend a, unsigned nfold, int blocks, int q_tok,
+__global__ void __launch_bounds__(kThreads, 4) block_prompt_kernel(KvqView v, BlockAppend a, unsigned nfold, int blocks, int q_tok,
                                                                 int q_units) {
   __shared__ FoldSmem sm;
   ptx::grid_dep_launch();
@@ -439,12 +481,12 @@ __global__ void __launch_bounds__(kThreads) block_prompt_kernel(KvqView v, Block
     if (bad && j == 0 && h == 0 && threadIdx.x == 0) atomicOr(v.status, KVQ_DEV_OVERFLOW);
     if (!live) return;
     const int wbase = T0 / v.R * v.R, t = wbase + j * v.kgroup;
-    if (t < (T0 + n) / v.R * v.R) fold_block<BF16>(v, a, sm, b, h, T0, wbase, t);
+    if (t < (T0 + n) / v.R * v.R) fold_block<BF16, kThreads>(v, a, sm, b, h, T0, wbase, t);
   } else {
     const unsigned x = u - nfold;
     const int b = x / q_units, i0 = x % q_units * q_tok;
     if (!sequence_step(v, a, b, T0, n, &bad)) return;
-    if (i0 < n) rotate_queries<BF16, kQTask / 2>(v, a, b, T0, i0, min(n, i0 + q_tok), 0, v.Hq);
+    if (i0 < n) rotate_queries<BF16, kThreads, kQTask / 2>(v, a, b, T0, i0, min(n, i0 + q_tok), 0, v.Hq);
   }
 }
 
@@ -454,7 +496,7 @@ __global__ void __launch_bounds__(kThreads) rope_query_kernel(KvqView v, BlockAp
   int T0, n;
   bool bad;
   if (!sequence_step(v, a, b, T0, n, &bad) || i0 >= n) return;
-  rotate_queries<BF16, 1>(v, a, b, T0, i0, min(n, i0 + q_tok), 0, v.Hq);
+  rotate_queries<BF16, kThreads, 1>(v, a, b, T0, i0, min(n, i0 + q_tok), 0, v.Hq);
 }
 
 // Tokens of queries a CTA takes: about 8 passes of its threads over groups of kQTask / 2 heads.
@@ -464,12 +506,7 @@ int query_tokens(const KvqView& v) {
   return t < 1 ? 1 : t;
 }
 
-// CTAs per cluster: a power of two up to 8 (the portable limit) and the kv-heads.
-int step_ranks(const KvqView& v) {
-  int r = 8;
-  while (r > v.Hkv) r >>= 1;
-  return r;
-}
+constexpr int kRanks = 8;  // CTAs per cluster (the portable limit)
 
 // Calls of up to this many rows a sequence take the one-launch kernel.
 constexpr int kStepRows = 16;
@@ -477,7 +514,7 @@ constexpr int kStepRows = 16;
 template <bool BF16>
 kvq_status launch_block_t(const KvqView& v, const BlockAppend& a, cudaStream_t st) {
   const bool step = a.n_new <= kStepRows && a.n_new <= v.R;
-  const int ranks = step_ranks(v);
+  const int ranks = kRanks;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;

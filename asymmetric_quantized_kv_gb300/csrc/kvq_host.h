@@ -35,8 +35,8 @@ enum SetupSlot {
   kSlotFp8 = kSlotFast + 4,       // FP8 tensor-core kernel, 2 instances
   kSlotInt2 = kSlotFp8 + 2,       // 2-bit tensor-core kernel, 2 instances
   kSlotRopeAppend = kSlotInt2 + 2,  // append kernel of kvq_rope_append
-  kSlotQueryFew,                    // few-row attention kernel, 36 instances: CTAs per SM
-  kSlotQueryTc = kSlotQueryFew + 36,  // many-row attention kernel, 6 instances
+  kSlotQueryFew,                    // few-row attention kernel, 72 instances at most: CTAs per SM
+  kSlotQueryTc = kSlotQueryFew + 72,  // many-row attention kernel, 6 instances
   kSlotCount = kSlotQueryTc + 6
 };
 

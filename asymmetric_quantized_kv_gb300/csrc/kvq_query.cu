@@ -165,20 +165,39 @@ bool query_tc_eligible(const KvqView& v) {
   return query_tc_shape(v) && (long long)v.n_pages * v.page_bytes / 128 < (1LL << 31) && tensor_map_encoder() != nullptr;
 }
 
+// Which of the two: the few-row kernel reads the cache once per 32 rows (16 at head_dim 256) at close to the
+// memory's rate; the many-row kernel reads it once per 256 and multiplies at the tensor cores' rate, but a unit of
+// its work starts and ends slowly.  head_dim 256 and fp32 output exceed the latter's shared and tensor memory.
+static bool takes_few(const KvqView& v, long long rows, int out_f32) { return rows <= kFewPass || v.D > 128 || out_f32; }
+
+static size_t few_bytes(const KvqView& v, int batch, long long rows) {
+  const size_t units = (size_t)kFewUnits + (size_t)batch * v.Hkv, r = (size_t)(rows < kFewPass ? rows : kFewPass);
+  return few_header_bytes(batch) + units * r * (v.D + 4) * sizeof(float);
+}
+
 size_t query_workspace_bytes(const KvqView& v, int batch, int n_q) {
   KvqView b = v;
   b.batch = batch;
   if (!query_tc_shape(b)) return 256;
-  if ((long long)n_q * v.n_rep <= kFewRows) return query_few_workspace_bytes(v, batch);
-  return v.D <= 128 ? query_many_workspace_bytes(v, batch, n_q) : 256;
+  const long long rows = (long long)n_q * v.n_rep;
+  return takes_few(v, rows, 0) ? few_bytes(v, batch, rows) : query_many_workspace_bytes(v, batch, n_q);
+}
+
+// A decode call's (fp32 output, in passes of at most 16 rows).
+size_t decode_workspace_bytes(const KvqView& v, int batch) {
+  KvqView b = v;
+  b.batch = batch;
+  return query_tc_shape(b) ? few_bytes(v, batch, v.n_rep < 16 ? v.n_rep : 16) : 256;
 }
 
 kvq_status launch_query(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st) {
-  if (query_tc_eligible(v)) {
-    if ((long long)a.n_q * v.n_rep <= kFewRows) return launch_query_few(v, a, ws, st);
-    if (v.D <= 128 && !a.out_f32 && (long long)a.n_q * v.n_rep < (1LL << 30)) return launch_query_many(v, a, ws, st);
-  }
-  return launch_query_plain(v, a, st);
+  const long long rows = (long long)a.n_q * v.n_rep;
+  if (!query_tc_eligible(v) || rows >= (1LL << 30) || (long long)v.batch * v.Hkv * kFewPass > 0x7FFFFFFFLL)
+    return launch_query_plain(v, a, st);
+  if (!takes_few(v, rows, a.out_f32)) return launch_query_many(v, a, ws, st);
+  return v.kfmt == KVQ_INT8 ? launch_query_few_i8(v, a, ws, st)
+         : v.kfmt == KVQ_FP8_E4M3 ? launch_query_few_e4(v, a, ws, st)
+                                  : launch_query_few_e5(v, a, ws, st);
 }
 
 }  // namespace kvq

@@ -28,14 +28,21 @@ __device__ __forceinline__ int query_end(const QueryArgs& a, int T, int n, int i
   return a.causal ? max(0, T - n + i + 1) : T;
 }
 
-constexpr int kFewRows = 8;     // rows of the few-row kernel: one column block of its products
+constexpr int kFewPass = 32;    // rows of the few-row kernel's widest pass
+constexpr int kFewUnits = 8192;  // its units beyond one per (sequence, kv-head)
 constexpr int kManyGrid = 160;  // CTAs of the many-row kernel at most (one per SM)
 
 bool query_tc_shape(const KvqView& v);      // config only: the tensor-core kernels take it
 bool query_tc_eligible(const KvqView& v);   // and the cache's pool
-size_t query_few_workspace_bytes(const KvqView& v, int batch);
+
+// The few-row kernel's workspace: int C, int units, pref[B + 1], u64 counter, then a record (M, l, 2 pad, o[D])
+// per (unit, row of a pass).
+__host__ __device__ inline size_t few_counter_offset(int B) { return ((size_t)(B + 3) * 4 + 7) & ~(size_t)7; }
+__host__ __device__ inline size_t few_header_bytes(int B) { return (few_counter_offset(B) + 8 + 255) / 256 * 256; }
 size_t query_many_workspace_bytes(const KvqView& v, int batch, int n_q);
-kvq_status launch_query_few(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st);
+kvq_status launch_query_few_i8(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st);
+kvq_status launch_query_few_e4(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st);
+kvq_status launch_query_few_e5(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st);
 kvq_status launch_query_many(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st);
 
 }  // namespace kvq

@@ -1,5 +1,6 @@
-// Attention of at most 8 rows (query token x query head) per kv-head over a PER_BLOCK
-// cache: decode steps and short drafts, bf16 sources, head_dim 64, 128 or 256.
+// Attention of few rows (query token x query head) per kv-head over a PER_BLOCK cache:
+// decode steps and drafts, bf16 sources, head_dim 64, 128 or 256.  The kernel takes 8, 16,
+// 24 or 32 rows a pass (16 at head_dim 256); more rows take several passes.
 //
 // Mathematics, for a 16-token tile (it lies in one block of the cache, so one key scale ks
 // and one value scale vs = 2^e f, f in [1, 2)): with code matrices C_k, C_v,
@@ -18,10 +19,12 @@
 // TMA copies of the pool seen as rows of 128 bytes with the 128-byte swizzle, so warps
 // never wait for one another.  Keys are the M operand of m16n8k16 (16 tokens x 8 rows),
 // values, transposed on the way from shared memory, that of the second product (16
-// channels x 8 rows); p crosses from one layout to the other with movmatrix.  The window's
+// channels x 8 rows); with more rows a converted operand serves up to four products.  p crosses from one layout to the other with movmatrix.  The window's
 // tokens (bf16) take the same path from registers, scaled by a power of two per tile.
 // Units are sized so that they fill the warps of the GPU a whole number of times (up to
 // 4); a second kernel merges a (sequence, kv-head)'s chunks.
+#pragma once
+
 #include <math.h>
 
 #include "kvq_code.cuh"
@@ -39,7 +42,7 @@ constexpr int kFWarps = 4;
 constexpr int kFThreads = kFWarps * 32;
 constexpr int kFStages = 3;
 constexpr int kRounds = 4;          // units per warp at most
-constexpr int kMaxUnits = 8192;     // units beyond one per (sequence, kv-head)
+constexpr int kMaxUnits = kFewUnits;
 constexpr int kUnitTokens = 512;    // a warp takes several units only if they are this long
 constexpr int kMinUnit = 64;        // tokens of the smallest chunk
 constexpr float kLazy = 8.f;
@@ -52,87 +55,66 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
 }
 
 // ---- plan: per sequence ceil(T / C) chunks (over pages and window alike) for each kv-head;
-// unit = pref[b] + kvh * chunks + chunk.  Workspace: int C, int units, pref[B + 1], u64 counter,
-// then a record (M, l, 2 pad, o[D]) per (unit, row).
-__host__ __device__ inline size_t few_counter_offset(int B) { return ((size_t)(B + 3) * 4 + 7) & ~(size_t)7; }
-__host__ __device__ inline size_t few_header_bytes(int B) { return (few_counter_offset(B) + 8 + 255) / 256 * 256; }
-
-// Whole CTA.  workers: warps of the grid.
+// unit = pref[b] + kvh * chunks + chunk.
+// One warp; pref: B + 1 ints of shared memory.  workers: warps of the grid.  Lanes over the sequences, whose
+// lengths are read once (a decode step's time is a chain of such latencies).
 __device__ inline void few_plan(const KvqView& v, int workers, int* pref, int* s_C, int* s_units) {
-  __shared__ unsigned long long s_sum;
-  __shared__ int s_part[kFThreads];
-  const int B = v.batch, nt = kFThreads;
-  const int seg = (B + nt - 1) / nt, b0 = min(B, (int)threadIdx.x * seg), b1 = min(B, b0 + seg);
-  auto total = [&](unsigned long long mine) {
-    if (threadIdx.x == 0) s_sum = 0ull;
-    __syncthreads();
+  const int B = v.batch, lane = threadIdx.x & 31;
+  unsigned long long sum = 0;
+  for (int b = lane; b < B; b += 32) {
+    const int T = seq_tokens(v, b);
+    pref[b] = T;
+    sum += (unsigned)T;
+  }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if ((threadIdx.x & 31) == 0) atomicAdd(&s_sum, mine);
-    __syncthreads();
-    const unsigned long long s = s_sum;
-    __syncthreads();
-    return s;
-  };
-  unsigned long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += (unsigned long long)seq_tokens(v, b);
-  const unsigned long long work = total(mine) * v.Hkv;
-  const unsigned long long each = work / workers;
-  const int rounds = (int)min(max(each / kUnitTokens, 1ull), (unsigned long long)min(kRounds, max(1, kMaxUnits / workers)));
-  const unsigned long long most = min((unsigned long long)rounds * workers, (unsigned long long)kMaxUnits);
-  unsigned long long C = (work + most - 1) / most;
-  C = max((unsigned long long)kMinUnit, (C + kTile - 1) / kTile * kTile);
-  // the cut ends of the sequences may push the units past a whole number of rounds: longer chunks
-  for (int k = 0; k < 6; ++k) {
-    unsigned long long units = 0;
-    for (int b = b0; b < b1; ++b) units += ((unsigned long long)seq_tokens(v, b) + C - 1) / C;
-    if (total(units) * v.Hkv <= most) break;
-    C = (C + C / 16 + kTile - 1) / kTile * kTile;
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const unsigned long long work = sum * v.Hkv;
+  const unsigned each = (unsigned)min(work / (unsigned)workers, 0xffffffffull);
+  const unsigned rounds = min(max(each / kUnitTokens, 1u), (unsigned)min(kRounds, max(1, kMaxUnits / workers)));
+  const unsigned most = min(rounds * (unsigned)workers, (unsigned)kMaxUnits);
+  unsigned C = (unsigned)min((work + most - 1) / most, 1ull << 30);
+  C = max((unsigned)kMinUnit, (C + kTile - 1) / kTile * kTile);
+  // the cut ends of the sequences may push the units past a whole number of rounds, or past what the
+  // workspace holds: longer chunks (a chunk as long as the longest sequence always fits)
+  const unsigned cap = kMaxUnits / v.Hkv + B;
+#pragma unroll 1
+  for (int k = 0;; ++k) {
+    unsigned units = 0;
+#pragma unroll 1
+    for (int b = lane; b < B; b += 32) units += ((unsigned)pref[b] + C - 1) / C;
+    units = __reduce_add_sync(0xffffffffu, units);
+    const bool fits = units <= cap;
+    if (fits && (k >= 6 || (unsigned long long)units * v.Hkv <= most)) break;
+    C = k < 6 ? (C + C / 16 + kTile - 1) / kTile * kTile : min(2 * C, 1u << 30);
   }
-  for (;;) {  // never more units than the workspace holds
-    unsigned long long units = 0;
-    for (int b = b0; b < b1; ++b) units += ((unsigned long long)seq_tokens(v, b) + C - 1) / C;
-    if (total(units) <= (unsigned long long)kMaxUnits / v.Hkv + B) break;  // true once C covers every sequence
-    C *= 2;
-  }
-  int local = 0;
-  for (int b = b0; b < b1; ++b) local += (int)((seq_tokens(v, b) + (long long)C - 1) / (long long)C) * v.Hkv;
-  s_part[threadIdx.x] = local;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int per = nt / 32, i0 = threadIdx.x * per;
-    int s = 0;
-    for (int i = i0; i < i0 + per; ++i) s += s_part[i];
-    int incl = s;
+  int run = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int b = b0 + lane, x = b < B ? (int)(((unsigned)pref[b] + C - 1) / C) * v.Hkv : 0;
+    int incl = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if ((int)threadIdx.x >= o) incl += y;
+      if (lane >= o) incl += y;
     }
-    int run = incl - s;
-    for (int i = i0; i < i0 + per; ++i) {
-      const int x = s_part[i];
-      s_part[i] = run;
-      run += x;
-    }
-    if (threadIdx.x == 31) {
-      *s_units = incl;
-      *s_C = (int)min(C, (unsigned long long)(1 << 30));
-    }
+    if (b < B) pref[b] = run + incl - x;
+    run += __shfl_sync(0xffffffffu, incl, 31);
   }
-  __syncthreads();
-  int run = s_part[threadIdx.x];
-  for (int b = b0; b < b1; ++b) {
-    pref[b] = run;
-    run += (int)((seq_tokens(v, b) + (long long)C - 1) / (long long)C) * v.Hkv;
+  if (lane == 0) {
+    pref[B] = run;
+    *s_units = run;
+    *s_C = (int)C;
   }
-  if (threadIdx.x == 0) pref[B] = *s_units;
-  __syncthreads();
 }
 
-template <int D>
+// Rows of a pass: 8 NB.  The query operand stays in registers up to 32 of them, else in shared memory.
+template <int D, int NB>
+constexpr bool query_in_smem() { return NB * (D / 16) > 16; }
+
+template <int D, int NB>
 struct __align__(1024) FewSmem {
   uint8_t kv[kFWarps][kFStages][2][kTile * D];
+  uint2 bq[query_in_smem<D, NB>() ? kFWarps : 1][query_in_smem<D, NB>() ? NB : 1][D / 16][32];
   uint64_t bar[kFWarps][kFStages];
   int valid[kFWarps][kFStages];
 };
@@ -140,21 +122,22 @@ struct __align__(1024) FewSmem {
 // Byte o of a 1024-byte aligned tile under the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swz(uint32_t o) { return o ^ (((o >> 7) & 7u) << 4); }
 
-template <int F, int D, bool kF32>
-__global__ void __launch_bounds__(kFThreads)
-    query_few_kernel(KvqView v, QueryArgs a, float* ws, int dynamic, const __grid_constant__ CUtensorMap tmap) {
+template <int F, int D, int NB, bool kF32>
+__global__ void __launch_bounds__(kFThreads, NB == 3 ? 3 : 1)
+    query_few_kernel(KvqView v, QueryArgs a, int row0, float* ws, int dynamic, const __grid_constant__ CUtensorMap tmap) {
   constexpr int NS = D / 16;      // steps of the first product, and channel tiles of the second
   constexpr int LC = D / 4;       // channels a lane holds of a key row
   constexpr int GC = D / 8;       // channels a lane holds of a value row
   constexpr int KB = kTile * D;   // bytes of a tile
   extern __shared__ unsigned char dyn_raw[];
   unsigned char* dyn = dyn_raw + ((1024 - (smem_u32(dyn_raw) & 1023)) & 1023);
-  FewSmem<D>& sm = *reinterpret_cast<FewSmem<D>*>(dyn);
-  int* pref = reinterpret_cast<int*>(dyn + sizeof(FewSmem<D>));
+  FewSmem<D, NB>& sm = *reinterpret_cast<FewSmem<D, NB>*>(dyn);
+  int* pref = reinterpret_cast<int*>(dyn + sizeof(FewSmem<D, NB>));
   __shared__ int s_C, s_units;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int workers = gridDim.x * kFWarps;
-  few_plan(v, workers, pref, &s_C, &s_units);
+  if (warp == 0) few_plan(v, workers, pref, &s_C, &s_units);
+  __syncthreads();
   if (blockIdx.x == 0) {
     int* hd = reinterpret_cast<int*>(ws);
     if (threadIdx.x == 0) {
@@ -169,7 +152,7 @@ __global__ void __launch_bounds__(kFThreads)
     fence_mbar_init();
   }
   __syncwarp();
-  const int C = s_C, n_units = s_units, rows_max = a.n_q * v.n_rep;
+  const int C = s_C, n_units = s_units, rows_max = min(8 * NB, a.n_q * v.n_rep - row0);
   unsigned long long* counter =
       reinterpret_cast<unsigned long long*>(reinterpret_cast<char*>(ws) + few_counter_offset(v.batch));
   float* part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + few_header_bytes(v.batch));
@@ -188,7 +171,7 @@ __global__ void __launch_bounds__(kFThreads)
     }
     const int b = lo, nc = (pref[b + 1] - pref[b]) / v.Hkv;
     const int h = (unit - pref[b]) / nc, chunk = (unit - pref[b]) % nc;
-    const int T = seq_tokens(v, b), nq = n_quantized(T, v.R), n = query_count(v, a, b), rows = n * v.n_rep;
+    const int T = seq_tokens(v, b), nq = n_quantized(T, v.R), n = query_count(v, a, b), rows = n * v.n_rep - row0;
     const int t0 = chunk * C, t1 = min(T, t0 + C);
     const int tq = min(t1, nq);                                // tiles before tq come from the pages
     const int qtiles = tq > t0 ? (tq - t0) / kTile : 0;        // nq and t0 are multiples of 16
@@ -256,14 +239,18 @@ __global__ void __launch_bounds__(kFThreads)
 
     // ---- queries: column g is row g; lane (g, t) holds its channels t LC .. t LC + LC - 1, brought into
     // f16 by the row's power of two
-    uint32_t bq[NS][2];
-    float up = 1.f;
-    {
+    constexpr bool kQS = query_in_smem<D, NB>();
+    uint32_t bq[kQS ? 1 : NB][NS][2];
+    float fct[NB][2];  // this lane's logits are those of rows 2t, 2t + 1 of each block: their factor,
+    int end[NB][2];    // and the tokens they see
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
       uint32_t u[LC / 2];
 #pragma unroll
       for (int i = 0; i < LC / 2; ++i) u[i] = 0u;
-      if (g < rows) {
-        const long long qi = (((long long)b * a.n_q + g / v.n_rep) * v.Hq + h * v.n_rep + g % v.n_rep) * D + t * LC;
+      if (8 * nb + g < rows) {
+        const int row = row0 + 8 * nb + g;
+        const long long qi = (((long long)b * a.n_q + row / v.n_rep) * v.Hq + h * v.n_rep + row % v.n_rep) * D + t * LC;
         const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + qi);
 #pragma unroll
         for (int i = 0; i < LC / 8; ++i) {
@@ -277,72 +264,97 @@ __global__ void __launch_bounds__(kFThreads)
       uint32_t top = max(m2 & 0xffffu, m2 >> 16);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      float down;
+      float down, up;
       norm_factors(top, down, up);
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        bq[s][0] = bf16x2_scaled(u[2 * s], down);
-        bq[s][1] = bf16x2_scaled(u[2 * s + 1], down);
-      }
-    }
-    // this lane's logits are those of rows 2t, 2t + 1: their factor and the tokens they see
-    const float fct[2] = {__shfl_sync(0xffffffffu, up, 8 * t) * a.scale * 1.4426950408889634f,
-                          __shfl_sync(0xffffffffu, up, 8 * t + 4) * a.scale * 1.4426950408889634f};
-    int end[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) end[e] = 2 * t + e < rows ? query_end(a, T, n, (2 * t + e) / v.n_rep) : 0;
-
-    float O[NS][4];
-#pragma unroll
-    for (int m = 0; m < NS; ++m) O[m][0] = O[m][1] = O[m][2] = O[m][3] = 0.f;
-    float m_run[2] = {kMinit, kMinit}, l_run[2] = {0.f, 0.f};
-
-    // logits of the tile at token tok (acc: token g / g + 8 x row 2t / 2t + 1) -> B operand of the second
-    // product; kf, vf: scale of the keys, and of the values as 2^e f
-    auto softmax = [&](const float (&acc)[4], int tok, float kf, int e, float f, uint32_t (&ph)[2], uint32_t (&pl)[2]) {
-      float x[2][2];  // [token g / g + 8][row]
-      const float fe = (float)e;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float c = kf * fct[r];
-        x[0][r] = tok + g < end[r] ? fmaf(acc[r], c, fe) : -INFINITY;
-        x[1][r] = tok + g + 8 < end[r] ? fmaf(acc[2 + r], c, fe) : -INFINITY;
-      }
-      const bool need = fmaxf(x[0][0], x[1][0]) > m_run[0] + kLazy || fmaxf(x[0][1], x[1][1]) > m_run[1] + kLazy;
-      if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float mx = fmaxf(x[0][r], x[1][r]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float mn = fmaxf(m_run[r], mx), al = ex2(m_run[r] - mn);
-          m_run[r] = mn;
-          l_run[r] *= al;
-#pragma unroll
-          for (int m = 0; m < NS; ++m) {  // columns 2t, 2t + 1 of the outputs are the same rows
-            O[m][r] *= al;
-            O[m][2 + r] *= al;
-          }
+        const uint32_t x = bf16x2_scaled(u[2 * s], down), y = bf16x2_scaled(u[2 * s + 1], down);
+        if constexpr (kQS) {
+          sm.bq[warp][nb][s][lane] = make_uint2(x, y);
+        } else {
+          bq[nb][s][0] = x;
+          bq[nb][s][1] = y;
         }
       }
-      const float ie = pow2i(-e);
-      float p[2][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        p[0][r] = ex2(x[0][r] - m_run[r]);
-        p[1][r] = ex2(x[1][r] - m_run[r]);
-        l_run[r] = fmaf(p[0][r] + p[1][r], ie, l_run[r]);
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * nb + 2 * t + e;
+        fct[nb][e] = __shfl_sync(0xffffffffu, up, 8 * t + 4 * e) * a.scale * 1.4426950408889634f;
+        end[nb][e] = r < rows ? query_end(a, T, n, (row0 + r) / v.n_rep) : 0;
+      }
+    }
+    __syncwarp();
+    auto query = [&](int nb, int s) -> uint2 {
+      if constexpr (kQS) return sm.bq[warp][nb][s][lane];
+      else return make_uint2(bq[nb][s][0], bq[nb][s][1]);
+    };
+
+    float O[NB][NS][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int m = 0; m < NS; ++m) O[nb][m][0] = O[nb][m][1] = O[nb][m][2] = O[nb][m][3] = 0.f;
+    float m_run[NB][2], l_run[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      m_run[nb][0] = m_run[nb][1] = kMinit;
+      l_run[nb][0] = l_run[nb][1] = 0.f;
+    }
+
+    // logits of the tile at token tok (acc: token g / g + 8 x row 2t / 2t + 1) -> B operands of the second
+    // product; kf, vf: scale of the keys, and of the values as 2^e f
+    auto softmax = [&](const float (&acc)[NB][4], int tok, float kf, int e, float f, uint32_t (&ph)[NB][2],
+                       uint32_t (&pl)[NB][2]) {
+      const float fe = (float)e, ie = pow2i(-e);
+      float x[NB][2][2];  // [block][token g / g + 8][row]
+      bool need = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float c = kf * fct[nb][r];
+          x[nb][0][r] = tok + g < end[nb][r] ? fmaf(acc[nb][r], c, fe) : -INFINITY;
+          x[nb][1][r] = tok + g + 8 < end[nb][r] ? fmaf(acc[nb][2 + r], c, fe) : -INFINITY;
+          need = need || fmaxf(x[nb][0][r], x[nb][1][r]) > m_run[nb][r] + kLazy;
+        }
+      if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float mx = fmaxf(x[nb][0][r], x[nb][1][r]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mn = fmaxf(m_run[nb][r], mx), al = ex2(m_run[nb][r] - mn);
+            m_run[nb][r] = mn;
+            l_run[nb][r] *= al;
+#pragma unroll
+            for (int m = 0; m < NS; ++m) {  // columns 2t, 2t + 1 of the outputs are the same rows
+              O[nb][m][r] *= al;
+              O[nb][m][2 + r] *= al;
+            }
+          }
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if constexpr (kF32) {
-          uint32_t hi2, lo2;
-          split_hi_lo(p[k][0] * f, p[k][1] * f, hi2, lo2);
-          ph[k] = movmatrix(hi2);
-          pl[k] = movmatrix(lo2);
-        } else {
-          ph[k] = movmatrix(pack_f16x2(p[k][0] * f, p[k][1] * f));
+      for (int nb = 0; nb < NB; ++nb) {
+        float p[2][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          p[0][r] = ex2(x[nb][0][r] - m_run[nb][r]);
+          p[1][r] = ex2(x[nb][1][r] - m_run[nb][r]);
+          l_run[nb][r] = fmaf(p[0][r] + p[1][r], ie, l_run[nb][r]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if constexpr (kF32) {
+            uint32_t hi2, lo2;
+            split_hi_lo(p[k][0] * f, p[k][1] * f, hi2, lo2);
+            ph[nb][k] = movmatrix(hi2);
+            pl[nb][k] = movmatrix(lo2);
+          } else {
+            ph[nb][k] = movmatrix(pack_f16x2(p[k][0] * f, p[k][1] * f));
+          }
         }
       }
     };
@@ -373,7 +385,9 @@ __global__ void __launch_bounds__(kFThreads)
       if (__all_sync(0xffffffffu, valid)) {  // a tile without its page, or its scales, takes no weight
         const uint8_t* kt = sm.kv[warp][stage][0];
         const uint8_t* vt = sm.kv[warp][stage][1];
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        float acc[NB][4], odd[4] = {0.f, 0.f, 0.f, 0.f};  // one block: two chains of half the length
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
 #pragma unroll
         for (int c = 0; c < LC / 16; ++c) {
           const uint4 k0 = *reinterpret_cast<const uint4*>(kt + swz(g * D + t * LC + 16 * c));
@@ -384,12 +398,20 @@ __global__ void __launch_bounds__(kFThreads)
             uint32_t a0, a1, a2, a3;
             codes_to_f16<F>(w0[j], a0, a2);
             codes_to_f16<F>(w1[j], a1, a3);
-            mma_16816(acc, a0, a1, a2, a3, bq[4 * c + j][0], bq[4 * c + j][1]);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              const uint2 b2 = query(nb, 4 * c + j);
+              mma_16816(NB == 1 && (j & 1) ? odd : acc[nb], a0, a1, a2, a3, b2.x, b2.y);
+            }
           }
+        }
+        if constexpr (NB == 1) {
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) acc[0][i4] += odd[i4];
         }
         const int e = vf == 0.f ? 0 : min(126, max(kMinExp, exponent_of(vf)));
         const float f = vf * pow2i(-e);  // in [1, 2), or less below 2^kMinExp
-        uint32_t ph[2], pl[2] = {0u, 0u};
+        uint32_t ph[NB][2], pl[NB][2];
         softmax(acc, tok, kf, e, f, ph, pl);
         // ---- second product: rows g / g + 8 of channel tile m = channels g GC + 2m / + 1,
         //      k-slots = tokens 2t, 2t + 1, 2t + 8, 2t + 9
@@ -417,8 +439,11 @@ __global__ void __launch_bounds__(kFThreads)
           uint32_t a0, a1, a2, a3;
           codes_to_f16<F>(prmt(wv[0][m >> 1], wv[1][m >> 1], sel), a0, a1);
           codes_to_f16<F>(prmt(wv[2][m >> 1], wv[3][m >> 1], sel), a2, a3);
-          mma_16816(O[m], a0, a1, a2, a3, ph[0], ph[1]);
-          if constexpr (kF32) mma_16816(O[m], a0, a1, a2, a3, pl[0], pl[1]);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma_16816(O[nb][m], a0, a1, a2, a3, ph[nb][0], ph[nb][1]);
+            if constexpr (kF32) mma_16816(O[nb][m], a0, a1, a2, a3, pl[nb][0], pl[nb][1]);
+          }
         }
       }
       __syncwarp();
@@ -435,7 +460,9 @@ __global__ void __launch_bounds__(kFThreads)
       const uint16_t* vw = static_cast<const uint16_t*>(v.v_win) + (((long long)b * v.R + (tok - nq)) * v.Hkv + h) * D;
       const long long pitch = (long long)v.Hkv * D;
       const uint4 z4 = make_uint4(0u, 0u, 0u, 0u);
-      float acc[4] = {0.f, 0.f, 0.f, 0.f}, down, kf, f;
+      float acc[NB][4], down, kf, f;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
       {
         uint32_t x0[LC / 2], x1[LC / 2], m2 = 0u;
 #pragma unroll
@@ -449,9 +476,15 @@ __global__ void __launch_bounds__(kFThreads)
         for (int c = 0; c < LC / 2; ++c) m2 = bf16x2_absmax(bf16x2_absmax(m2, x0[c]), x1[c]);
         norm_factors(warp_max(max(m2 & 0xffffu, m2 >> 16)), down, kf);
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
-          mma_16816(acc, bf16x2_scaled(x0[2 * s], down), bf16x2_scaled(x1[2 * s], down), bf16x2_scaled(x0[2 * s + 1], down),
-                    bf16x2_scaled(x1[2 * s + 1], down), bq[s][0], bq[s][1]);
+        for (int s = 0; s < NS; ++s) {
+          const uint32_t a0 = bf16x2_scaled(x0[2 * s], down), a1 = bf16x2_scaled(x1[2 * s], down);
+          const uint32_t a2 = bf16x2_scaled(x0[2 * s + 1], down), a3 = bf16x2_scaled(x1[2 * s + 1], down);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const uint2 b2 = query(nb, s);
+            mma_16816(acc[nb], a0, a1, a2, a3, b2.x, b2.y);
+          }
+        }
       }
       constexpr int W = GC / 2;  // bf16 pairs of a value row a lane holds
       uint32_t wv[4][W], m2 = 0u;
@@ -469,7 +502,7 @@ __global__ void __launch_bounds__(kFThreads)
       norm_factors(warp_max(max(m2 & 0xffffu, m2 >> 16)), down, f);
       const int e = max(kMinExp, exponent_of(f));
       f *= pow2i(-e);
-      uint32_t ph[2], pl[2] = {0u, 0u};
+      uint32_t ph[NB][2], pl[NB][2];
       softmax(acc, tok, kf, e, f, ph, pl);
 #pragma unroll
       for (int m = 0; m < NS; ++m) {  // channels g GC + 2m, + 1 are pair m of each row
@@ -477,27 +510,34 @@ __global__ void __launch_bounds__(kFThreads)
         const uint32_t y2 = bf16x2_scaled(wv[2][m], down), y3 = bf16x2_scaled(wv[3][m], down);
         const uint32_t a0 = prmt(y0, y1, 0x5410u), a1 = prmt(y0, y1, 0x7632u);
         const uint32_t a2 = prmt(y2, y3, 0x5410u), a3 = prmt(y2, y3, 0x7632u);
-        mma_16816(O[m], a0, a1, a2, a3, ph[0], ph[1]);
-        if constexpr (kF32) mma_16816(O[m], a0, a1, a2, a3, pl[0], pl[1]);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          mma_16816(O[nb][m], a0, a1, a2, a3, ph[nb][0], ph[nb][1]);
+          if constexpr (kF32) mma_16816(O[nb][m], a0, a1, a2, a3, pl[nb][0], pl[nb][1]);
+        }
       }
     }
 
     // ---- the unit's records
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], o);
-      if (2 * t + r < rows) {
-        float* rec = part + ((long long)unit * rows_max + 2 * t + r) * (D + 4);
-        if (g == 0) {
-          rec[0] = m_run[r];
-          rec[1] = l_run[r];
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l_run[nb][r] += __shfl_xor_sync(0xffffffffu, l_run[nb][r], o);
+        const int row = 8 * nb + 2 * t + r;
+        if (row < rows) {
+          float* rec = part + ((long long)unit * rows_max + row) * (D + 4);
+          if (g == 0) {
+            rec[0] = m_run[nb][r];
+            rec[1] = l_run[nb][r];
+          }
+#pragma unroll
+          for (int m = 0; m < NS; ++m)
+            *reinterpret_cast<float2*>(rec + 4 + g * GC + 2 * m) = make_float2(O[nb][m][r], O[nb][m][2 + r]);
         }
-#pragma unroll
-        for (int m = 0; m < NS; ++m)
-          *reinterpret_cast<float2*>(rec + 4 + g * GC + 2 * m) = make_float2(O[m][r], O[m][2 + r]);
       }
-    }
+    __syncwarp();
     unit = dynamic ? workers + (int)__shfl_sync(0xffffffffu, (unsigned)nxt, 0) : unit + workers;
   }
   if (lane == 0) {  // copies issued and not consumed (a stalled ring): wait for them, bounded, before leaving
@@ -512,23 +552,24 @@ __global__ void __launch_bounds__(kFThreads)
   }
 }
 
-// One CTA of 4 warps per (sequence, query, head): the warps take every fourth record of the row's
-// chunks, lanes over channel pairs or quads, and merge through shared memory.
+// One CTA of 4 warps per (sequence, kv-head, row of the pass): the warps take every fourth record of the
+// row's chunks, lanes over channel pairs or quads, and merge through shared memory.
 constexpr int kMWarps = 4;
 template <int D, bool kF32>
-__global__ void __launch_bounds__(kMWarps * 32) few_merge_kernel(KvqView v, QueryArgs a, const float* ws) {
+__global__ void __launch_bounds__(kMWarps * 32) few_merge_kernel(KvqView v, QueryArgs a, int row0, int rows_max, const float* ws) {
   constexpr int PER = D / 32;  // channels per lane: 2, 4 or 8
   __shared__ float o_s[kMWarps][D];
   __shared__ float m_s[kMWarps], l_s[kMWarps];
-  const int hq = blockIdx.x % v.Hq, x = blockIdx.x / v.Hq, i = x % a.n_q, b = x / a.n_q;
+  const int r = blockIdx.x % rows_max, x = blockIdx.x / rows_max, h = x % v.Hkv, b = x / v.Hkv;
+  const int i = (row0 + r) / v.n_rep, hq = h * v.n_rep + (row0 + r) % v.n_rep;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dep_wait();
   if (i >= query_count(v, a, b)) return;
   const int* pref = reinterpret_cast<const int*>(ws) + 2;
-  const int nc = (pref[b + 1] - pref[b]) / v.Hkv, h = hq / v.n_rep, row = i * v.n_rep + hq % v.n_rep;
-  const long long rows_max = (long long)a.n_q * v.n_rep, stride = rows_max * (D + 4);
+  const int nc = (pref[b + 1] - pref[b]) / v.Hkv;
+  const long long stride = (long long)rows_max * (D + 4);
   const float* rec = reinterpret_cast<const float*>(reinterpret_cast<const char*>(ws) + few_header_bytes(v.batch)) +
-                     ((long long)(pref[b] + h * nc) * rows_max + row) * (D + 4);
+                     ((long long)(pref[b] + h * nc) * rows_max + r) * (D + 4);
   float m = kMinit, l = 0.f, o[PER];
 #pragma unroll
   for (int c = 0; c < PER; ++c) o[c] = 0.f;
@@ -543,13 +584,13 @@ __global__ void __launch_bounds__(kMWarps * 32) few_merge_kernel(KvqView v, Quer
 #pragma unroll
       for (int c = 0; c < PER; ++c) y[j][c] = 0.f;
       if (k < nc) {
-        const float* r = rec + (long long)k * stride;
-        const float2 ml = *reinterpret_cast<const float2*>(r);
+        const float* rk = rec + (long long)k * stride;
+        const float2 ml = *reinterpret_cast<const float2*>(rk);
         rm[j] = ml.x;
         rl[j] = ml.y;
 #pragma unroll
         for (int c = 0; c < PER; c += 2) {
-          const float2 z = *reinterpret_cast<const float2*>(r + 4 + lane * PER + c);
+          const float2 z = *reinterpret_cast<const float2*>(rk + 4 + lane * PER + c);
           y[j][c] = z.x;
           y[j][c + 1] = z.y;
         }
@@ -598,15 +639,16 @@ __global__ void __launch_bounds__(kMWarps * 32) few_merge_kernel(KvqView v, Quer
   }
 }
 
-template <int F, int D, bool kF32>
-kvq_status launch_few_t(const KvqView& v, const QueryArgs& a, float* ws, const CUtensorMap& tmap, cudaStream_t st) {
+template <int F, int D, int NB, bool kF32>
+kvq_status launch_few_t(const KvqView& v, const QueryArgs& a, int row0, float* ws, const CUtensorMap& tmap, cudaStream_t st) {
   constexpr int kMaxBatch = 4096;  // the plan's prefix in shared memory (query_tc_shape)
-  const auto kern = query_few_kernel<F, D, kF32>;
-  const size_t smem = sizeof(FewSmem<D>) + 1024 + sizeof(int) * (v.batch + 1);
+  constexpr int kNB = NB - 1, kDi = D == 64 ? 0 : D == 128 ? 1 : 2;
+  const auto kern = query_few_kernel<F, D, NB, kF32>;
+  const size_t smem = sizeof(FewSmem<D, NB>) + 1024 + sizeof(int) * (v.batch + 1);
   int occ = 0;
-  const int slot = kSlotQueryFew + (F * 3 + (D == 64 ? 0 : D == 128 ? 1 : 2)) * 2 + (kF32 ? 1 : 0);
-  const kvq_status so = occupancy_once(slot, kern, kFThreads, sizeof(FewSmem<D>) + 1024 + sizeof(int) * 65,
-                                       sizeof(FewSmem<D>) + 1024 + sizeof(int) * (kMaxBatch + 1), &occ);
+  const kvq_status so = occupancy_once(kSlotQueryFew + ((F * 3 + kDi) * 4 + kNB) * 2 + (kF32 ? 1 : 0), kern, kFThreads,
+                                       sizeof(FewSmem<D, NB>) + 1024 + sizeof(int) * 65,
+                                       sizeof(FewSmem<D, NB>) + 1024 + sizeof(int) * (kMaxBatch + 1), &occ);
   if (so != KVQ_OK) return so;
   int grid = num_sms() * occ;
   if (grid > kMaxUnits / kFWarps) grid = kMaxUnits / kFWarps;
@@ -616,10 +658,12 @@ kvq_status launch_few_t(const KvqView& v, const QueryArgs& a, float* ws, const C
   const int dynamic = most > (long long)grid * kFWarps * kUnitTokens;
   if (dynamic && cudaMemsetAsync(reinterpret_cast<char*>(ws) + few_counter_offset(v.batch), 0, 8, st) != cudaSuccess)
     return KVQ_ERR_CUDA;
-  kern<<<grid, kFThreads, smem, st>>>(v, a, ws, dynamic, tmap);
+  kern<<<grid, kFThreads, smem, st>>>(v, a, row0, ws, dynamic, tmap);
   if (cudaGetLastError() != cudaSuccess) return KVQ_ERR_CUDA;
+  const long long rows = (long long)a.n_q * v.n_rep - row0;
+  const int rows_max = (int)(rows < 8 * NB ? rows : 8 * NB);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)v.batch * a.n_q * v.Hq));
+  cfg.gridDim = dim3((unsigned)((long long)v.batch * v.Hkv * rows_max));
   cfg.blockDim = dim3(kMWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -627,24 +671,40 @@ kvq_status launch_few_t(const KvqView& v, const QueryArgs& a, float* ws, const C
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_merge_kernel<D, kF32>, v, a, (const float*)ws) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, few_merge_kernel<D, kF32>, v, a, row0, rows_max, (const float*)ws) == cudaSuccess
+             ? KVQ_OK
+             : KVQ_ERR_CUDA;
 }
 
-template <int F, bool kF32>
-kvq_status launch_few_d(const KvqView& v, const QueryArgs& a, float* ws, const CUtensorMap& tmap, cudaStream_t st) {
-  if (v.D == 64) return launch_few_t<F, 64, kF32>(v, a, ws, tmap, st);
-  if (v.D == 128) return launch_few_t<F, 128, kF32>(v, a, ws, tmap, st);
-  return launch_few_t<F, 256, kF32>(v, a, ws, tmap, st);
+// Rows in passes of 32 (16 at head_dim 256, or with fp32 output, whose second product doubles): a pass reads the
+// whole cache, so the last ones take the smallest block that holds what is left.
+template <int F, int D, bool kF32>
+kvq_status launch_few_rows(const KvqView& v, const QueryArgs& a, float* ws, const CUtensorMap& tmap, cudaStream_t st) {
+  constexpr bool kFour = D <= 128 && !kF32;
+  const long long rows = (long long)a.n_q * v.n_rep;
+  for (long long r = 0; r < rows;) {
+    const long long left = rows - r;
+    kvq_status s;
+    if (left <= 8) {
+      s = launch_few_t<F, D, 1, kF32>(v, a, (int)r, ws, tmap, st);
+      r += 8;
+    } else if (!kFour || left <= 16) {
+      s = launch_few_t<F, D, 2, kF32>(v, a, (int)r, ws, tmap, st);
+      r += 16;
+    } else if (left <= 24) {
+      s = launch_few_t<F, D, kFour ? 3 : 2, kF32>(v, a, (int)r, ws, tmap, st);
+      r += 24;
+    } else {
+      s = launch_few_t<F, D, kFour ? 4 : 2, kF32>(v, a, (int)r, ws, tmap, st);
+      r += 32;
+    }
+    if (s != KVQ_OK) return s;
+  }
+  return KVQ_OK;
 }
 
-}  // namespace
-
-size_t query_few_workspace_bytes(const KvqView& v, int batch) {
-  const size_t units = (size_t)kMaxUnits + (size_t)batch * v.Hkv;
-  return few_header_bytes(batch) + units * kFewRows * (v.D + 4) * sizeof(float);
-}
-
-kvq_status launch_query_few(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st) {
+template <int F>
+kvq_status launch_few_format(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st) {
   CUtensorMap tmap;  // the pool as rows of 128 bytes, read in tiles of 16 tokens
   const cuuint64_t dims[2] = {128, (cuuint64_t)((long long)v.n_pages * v.page_bytes / 128)};
   const cuuint64_t strides[1] = {128};
@@ -655,14 +715,15 @@ kvq_status launch_query_few(const KvqView& v, const QueryArgs& a, void* ws, cuda
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return KVQ_ERR_CUDA;
   float* w = static_cast<float*>(ws);
-  switch (fmt_index(v.kfmt) * 2 + a.out_f32) {
-    case 0: return launch_few_d<kI8, false>(v, a, w, tmap, st);
-    case 1: return launch_few_d<kI8, true>(v, a, w, tmap, st);
-    case 2: return launch_few_d<kE4, false>(v, a, w, tmap, st);
-    case 3: return launch_few_d<kE4, true>(v, a, w, tmap, st);
-    case 4: return launch_few_d<kE5, false>(v, a, w, tmap, st);
-    default: return launch_few_d<kE5, true>(v, a, w, tmap, st);
+  if (a.out_f32) {
+    if (v.D == 64) return launch_few_rows<F, 64, true>(v, a, w, tmap, st);
+    if (v.D == 128) return launch_few_rows<F, 128, true>(v, a, w, tmap, st);
+    return launch_few_rows<F, 256, true>(v, a, w, tmap, st);
   }
+  if (v.D == 64) return launch_few_rows<F, 64, false>(v, a, w, tmap, st);
+  if (v.D == 128) return launch_few_rows<F, 128, false>(v, a, w, tmap, st);
+  return launch_few_rows<F, 256, false>(v, a, w, tmap, st);
 }
 
+}  // namespace
 }  // namespace kvq
