@@ -123,7 +123,7 @@ struct __align__(1024) FewSmem {
 __device__ __forceinline__ uint32_t swz(uint32_t o) { return o ^ (((o >> 7) & 7u) << 4); }
 
 template <int F, int D, int NB, bool kF32>
-__global__ void __launch_bounds__(kFThreads, NB == 3 ? 3 : 1)
+__global__ void __launch_bounds__(kFThreads)
     query_few_kernel(KvqView v, QueryArgs a, int row0, float* ws, int dynamic, const __grid_constant__ CUtensorMap tmap) {
   constexpr int NS = D / 16;      // steps of the first product, and channel tiles of the second
   constexpr int LC = D / 4;       // channels a lane holds of a key row
