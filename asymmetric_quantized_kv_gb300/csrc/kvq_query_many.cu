@@ -63,10 +63,11 @@ template <int D>
 struct Lay {
   static constexpr int kTileB = 128 * D * 2;
   static constexpr int kRawB = 128 * D;
-  // the second Q tile also carries the join of two streams: 32 channels and the statistics of 128 rows
-  static constexpr int kQ1B = kTileB > 17 * 1024 ? kTileB : 17 * 1024;
-  static constexpr int kQ = 0, kK = kTileB + kQ1B, kV = kK + 2 * kTileB, kRawK = kV + 2 * kTileB, kRawV = kRawK + kRawB;
+  static constexpr int kQ = 0, kK = 2 * kTileB, kV = kK + 2 * kTileB, kRawK = kV + 2 * kTileB, kRawV = kRawK + kRawB;
   static constexpr int kMisc = kRawV + kRawB;
+  // Raw stage: one with 256 rows, two with 128, whose second Q tile is free
+  static __device__ __forceinline__ int raw_k(int stage) { return stage ? kQ + kTileB : kRawK; }
+  static __device__ __forceinline__ int raw_v(int stage) { return stage ? kQ + kTileB + kRawB : kRawV; }
 };
 
 struct Misc {
@@ -74,7 +75,7 @@ struct Misc {
   float4 scale[kSlots][kPieces];
   uint32_t skip_k[kSlots];      // pieces to fill with zeros
   uint32_t skip_v[kSlots];
-  uint64_t raw_k_full, raw_v_full, raw_k_empty, raw_v_empty;
+  uint64_t raw_k_full[2], raw_v_full[2], raw_k_empty[2], raw_v_empty[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2], q_full[2];
   float row_x[2][kRows];        // exchange between the two threads of a row
@@ -416,7 +417,9 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
   const unsigned long long total = mi.total * v.Hkv;
   // no CTA between two others is left without a tile: the merge walks from one to the next
   const unsigned long long runs = min((unsigned long long)gridDim.x, total), me = blockIdx.x;
-  const unsigned long long w0 = me < runs ? total * me / runs : 0ull, w1 = me < runs ? total * (me + 1) / runs : 0ull;
+  const unsigned long long each = total / max(runs, 1ull), more = total - each * runs;  // `more` runs get one place more
+  const unsigned long long w0 = me < runs ? each * me + min(me, more) : 0ull;
+  const unsigned long long w1 = me < runs ? w0 + each + (me < more ? 1 : 0) : 0ull;
   RecHeader* hdr = reinterpret_cast<RecHeader*>(ws) + 2 * blockIdx.x;
   if (threadIdx.x < 2) hdr[threadIdx.x].used = 0;
   if (w0 == w1) return;
@@ -475,11 +478,11 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
   if (warp == kMmaWarp) {
     tc::tmem_alloc(&mi.tmem, 512);
     if (lane == 0) {
-      mbar_init(&mi.raw_k_full, 1);
-      mbar_init(&mi.raw_v_full, 1);
-      mbar_init(&mi.raw_k_empty, kConvWarps);
-      mbar_init(&mi.raw_v_empty, kConvWarps);
       for (int i = 0; i < 2; ++i) {
+        mbar_init(&mi.raw_k_full[i], 1);
+        mbar_init(&mi.raw_v_full[i], 1);
+        mbar_init(&mi.raw_k_empty[i], kConvWarps);
+        mbar_init(&mi.raw_v_empty[i], kConvWarps);
         mbar_init(&mi.k_full[i], kConvWarps);
         mbar_init(&mi.k_empty[i], 1);
         mbar_init(&mi.v_full[i], kConvWarps);
@@ -521,7 +524,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
     bool todo = true;  // tiles not yet looked up: j of the run's unit
     int j = run.j0;
     bool ok = true;
-    uint32_t it = 0;  // tiles copied: phase of the single raw stage, slot of the scales
+    uint32_t it = 0;  // tiles copied
     for (;;) {
       p2.some = todo;
       if (todo) {
@@ -533,15 +536,16 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
       }
       if (p1.some) p1.read_scales(v, D, lane);
       if (p0.some) {
-        const int slot = it % kSlots;
+        const int slot = it % kSlots, rs = two ? 0 : it & 1;  // raw stage and its phase
+        const uint32_t rp = two ? it & 1 : (it >> 1) & 1;
         const uint32_t bytes = p0.good ? (uint32_t)(p0.p1 - p0.p0) * D : 0u;
         const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
         const uint8_t* src = v.pages + p0.page + (long long)p0.row0 * D;
-        ok = __all_sync(0xffffffffu, wait(&mi.raw_k_empty, (it & 1) ^ 1));
+        ok = __all_sync(0xffffffffu, wait(&mi.raw_k_empty[rs], rp ^ 1));
         if (!ok) break;
-        if (lane == 0 && sum) mbar_expect_tx(&mi.raw_k_full, sum);
+        if (lane == 0 && sum) mbar_expect_tx(&mi.raw_k_full[rs], sum);
         __syncwarp();
-        if (bytes) bulk_g2s(sm + L::kRawK + (p0.p0 - p0.t0) * D, src, bytes, &mi.raw_k_full);
+        if (bytes) bulk_g2s(sm + L::raw_k(rs) + (p0.p0 - p0.t0) * D, src, bytes, &mi.raw_k_full[rs]);
         float4 sc = make_float4(0.f, -INFINITY, 0.f, 0.f);
         bool drop_v = false;
         uint32_t bad = p0.missing;
@@ -562,12 +566,12 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           if (bad) atomicOr(v.status, KVQ_DEV_BAD_PAGE);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&mi.raw_k_full);
-        ok = __all_sync(0xffffffffu, wait(&mi.raw_v_empty, (it & 1) ^ 1));
+        if (lane == 0) mbar_arrive(&mi.raw_k_full[rs]);
+        ok = __all_sync(0xffffffffu, wait(&mi.raw_v_empty[rs], rp ^ 1));
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&mi.raw_v_full, sum);
+        if (lane == 0) mbar_arrive_expect_tx(&mi.raw_v_full[rs], sum);
         __syncwarp();
-        if (bytes) bulk_g2s(sm + L::kRawV + (p0.p0 - p0.t0) * D, src + v.off_vc, bytes, &mi.raw_v_full);
+        if (bytes) bulk_g2s(sm + L::raw_v(rs) + (p0.p0 - p0.t0) * D, src + v.off_vc, bytes, &mi.raw_v_full[rs]);
         ++it;
       } else if (!p1.some && !p2.some) {
         break;
@@ -581,15 +585,16 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
     do {
       for (int j = run.j0; j < run.j1; ++j, ++it) {
         const int t0 = j * kTok, slot = it % kSlots, st = it & 1;
-        const uint32_t ph = (it >> 1) & 1;
+        const uint32_t ph = (it >> 1) & 1, rp = two ? it & 1 : ph;
+        const int rs = two ? 0 : st;
         uint8_t* kd = sm + L::kK + st * L::kTileB;
         uint8_t* vd = sm + L::kV + st * L::kTileB;
-        ok = wait(&mi.raw_k_full, it & 1) && wait(&mi.k_empty[st], ph ^ 1);
+        ok = wait(&mi.raw_k_full[rs], rp) && wait(&mi.k_empty[st], ph ^ 1);
         if (!ok) break;
         const uint32_t skip_k = mi.skip_k[slot], skip_v = mi.skip_v[slot];
         const bool plain = t0 + kTok <= w.nq;  // every piece is a page's
         if (plain && skip_k == 0) {
-          convert_pieces<F, D>(sm + L::kRawK, kd, warp - kConv0, lane);
+          convert_pieces<F, D>(sm + L::raw_k(rs), kd, warp - kConv0, lane);
         } else
 #pragma unroll 1
         for (int i = 0; i < kPieces / kConvWarps; ++i) {
@@ -597,7 +602,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           if (tok >= w.T || ((skip_k >> piece) & 1u)) {
             zero_piece<D>(kd, piece, lane);
           } else if (tok < w.nq) {
-            convert_piece<F, D>(sm + L::kRawK, kd, piece, lane);
+            convert_piece<F, D>(sm + L::raw_k(rs), kd, piece, lane);
           } else {
             const int kk = window_piece<D>(v.k_win, v, w.b, w.h, tok, w.T, w.nq, kd, piece, lane, true);
             const int kv = window_piece<D>(v.v_win, v, w.b, w.h, tok, w.T, w.nq, vd, piece, lane, false);
@@ -605,12 +610,12 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&mi.raw_k_empty);
+        if (lane == 0) mbar_arrive(&mi.raw_k_empty[rs]);
         hand_over(&mi.k_full[st], lane);
-        ok = wait(&mi.raw_v_full, it & 1) && wait(&mi.v_empty[st], ph ^ 1);
+        ok = wait(&mi.raw_v_full[rs], rp) && wait(&mi.v_empty[st], ph ^ 1);
         if (!ok) break;
         if (plain && skip_v == 0) {
-          convert_pieces<F, D>(sm + L::kRawV, vd, warp - kConv0, lane);
+          convert_pieces<F, D>(sm + L::raw_v(rs), vd, warp - kConv0, lane);
         } else
 #pragma unroll 1
         for (int i = 0; i < kPieces / kConvWarps; ++i) {
@@ -618,13 +623,13 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           if (tok >= w.T || (tok < w.nq && ((skip_v >> piece) & 1u))) {
             zero_piece<D>(vd, piece, lane);
           } else if (tok < w.nq) {
-            convert_piece<F, D>(sm + L::kRawV, vd, piece, lane);
+            convert_piece<F, D>(sm + L::raw_v(rs), vd, piece, lane);
           } else {
             window_piece<D>(v.v_win, v, w.b, w.h, tok, w.T, w.nq, vd, piece, lane, true);
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&mi.raw_v_empty);
+        if (lane == 0) mbar_arrive(&mi.raw_v_empty[rs]);
         hand_over(&mi.v_full[st], lane);
       }
     } while (ok && run.next(v, a, RT));
@@ -751,7 +756,8 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         // until both halves of every row have agreed to it.
         uint32_t pk[32];
         float top, sum;
-        sum = masked ? half_weights<true>(tS, sc, fct, M, lim, pk, top) : half_weights<false>(tS, sc, fct, M, lim, pk, top);
+        if (!any) top = INFINITY;  // nothing stands yet
+        else sum = masked ? half_weights<true>(tS, sc, fct, M, lim, pk, top) : half_weights<false>(tS, sc, fct, M, lim, pk, top);
         // (a stream whose wait gave up stops as one: the barrier carries that too)
         if (stream_any(kBarStream + s, top > kLazyM || !ok)) {
           if (stream_any(kBarStream + s, !ok)) {
@@ -809,9 +815,11 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
       named_bar_sync(kBarStream + s, 2 * kRows);
       if (hf) l = *rx;
       if (!two) {
-        // stream 1's (M, l, O) through the second half's place in shared memory, 16 channels a thread at a time
-        float* ex = reinterpret_cast<float*>(sm + L::kQ + L::kTileB) + hf * (16 * kRows);
-        float* ml = reinterpret_cast<float*>(sm + L::kQ + L::kTileB) + 32 * kRows;
+        // stream 1's (M, l, O) to stream 0, O through the Q tile (its products are done), 16 channels a thread at
+        // a time
+        float* ex = reinterpret_cast<float*>(sm + L::kQ) + hf * (16 * kRows);
+        float* ml = mi.row_x[0];
+        named_bar_sync(kBarJoin, 4 * kRows);  // both streams' sums have been read
         if (s == 1 && !hf) {
           ml[row_l] = any ? M : kMinitM;
           ml[kRows + row_l] = any ? l : 0.f;
@@ -845,6 +853,8 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
             }
             named_bar_sync(kBarJoin, 4 * kRows);
           }
+        } else {
+          named_bar_sync(kBarJoin, 4 * kRows);  // stream 0 has read the statistics
         }
       }
       const bool begins = j0 == 0, ends = j1 == w.tiles;
