@@ -12,12 +12,12 @@
 // power of two; p is rounded to f16 once (2^-11 against the output's own 2^-8).
 //
 // What bounds it: the tensor cores and the softmax's exponentials for many rows, the codes'
-// traffic for few.  One persistent CTA per SM of 22 warps, each with one task:
+// traffic for few.  One persistent CTA per SM of 23 warps, each with one task:
 //   20     copies the tiles' codes into shared memory (bulk copies, a page each) and reads
 //          the scales, two tiles ahead;
 //   16-19  turn codes (and the window's bf16 rows) into f16 tiles with the 128-byte swizzle;
-//   21     issues the products: S = Q K^T from shared memory, O += P V with P in tensor
-//          memory;
+//   21, 22 issue the products of a stream each: S = Q K^T from shared memory, O += P V with
+//          P in tensor memory;
 //   0-7, 8-15  two streams of 128 rows: two threads own a row, half of its columns each,
 //          read S from tensor memory, write P over it and rescale O.
 // The two streams' products alternate, so that one runs while the other's softmax does.
@@ -43,7 +43,7 @@ constexpr int kTok = 128;     // tokens of a tile
 constexpr int kPieces = kTok / 16;
 constexpr int kSoftWarps = 16;           // 8 a stream: 4 warps reach the 128 rows, twice, for half the columns each
 constexpr int kConv0 = kSoftWarps, kConvWarps = 4, kLoadWarp = kConv0 + kConvWarps, kMmaWarp = kLoadWarp + 1;
-constexpr int kMThreads = (kMmaWarp + 1) * 32;
+constexpr int kMThreads = (kMmaWarp + 2) * 32;
 constexpr int kBarStream = 1, kBarJoin = 3;  // named barriers: of the streams (and the next), of both
 constexpr int kSlots = 8;     // tiles whose scales are kept
 constexpr float kLazyM = 256.f;  // a piece's weights may sum to this before the maximum is raised
@@ -77,7 +77,7 @@ struct Misc {
   uint32_t skip_v[kSlots];
   uint64_t raw_k_full[2], raw_v_full[2], raw_k_empty[2], raw_v_empty[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], o_full[2], q_full[2];
+  uint64_t s_full[2], p_full[2], o_full[2], q_full[2], turn[2];
   float row_x[2][kRows];        // exchange between the two threads of a row
   uint32_t tmem;
   int abort;
@@ -484,10 +484,11 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         mbar_init(&mi.raw_k_empty[i], kConvWarps);
         mbar_init(&mi.raw_v_empty[i], kConvWarps);
         mbar_init(&mi.k_full[i], kConvWarps);
-        mbar_init(&mi.k_empty[i], 1);
+        mbar_init(&mi.k_empty[i], two ? 2 : 1);  // each stream that multiplies by the tile
         mbar_init(&mi.v_full[i], kConvWarps);
-        mbar_init(&mi.v_empty[i], 1);
+        mbar_init(&mi.v_empty[i], two ? 2 : 1);
         mbar_init(&mi.s_full[i], 1);
+        mbar_init(&mi.turn[i], 1);
         mbar_init(&mi.p_full[i], 8);
         mbar_init(&mi.o_full[i], 1);
         mbar_init(&mi.q_full[i], 8);
@@ -633,60 +634,62 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         hand_over(&mi.v_full[st], lane);
       }
     } while (ok && run.next(v, a, RT));
-  } else if (warp == kMmaWarp) {
-    // The whole warp walks the steps with values it knows to be uniform, and one elected lane issues: the
-    // descriptors then stay in uniform registers (issued from a divergent lane, a product cost 160 cycles).
+  } else if (warp >= kMmaWarp) {
+    // A warp a stream, so that one's waits do not hold up the other's products (issuing blocks until the
+    // products before are nearly done).  The whole warp walks the steps with values it knows to be uniform,
+    // and one elected lane issues: the descriptors then stay in uniform registers (issued from a divergent
+    // lane, a product cost 160 cycles).
     constexpr uint32_t id_s = tc::f16_idesc(128, 128, false), id_o = tc::f16_idesc(128, D, true);
     constexpr uint32_t kPanel = 128 * 128;
-    const uint64_t dq = tc::smem_desc(smem_u32(sm + L::kQ), 16), dk = tc::smem_desc(smem_u32(sm + L::kK), 16);
-    const uint64_t dv = tc::smem_desc(smem_u32(sm + L::kV), kPanel);
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const int s = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0), by = two ? 1 : 2;
+    const uint64_t dq = tc::smem_desc(smem_u32(sm + L::kQ + (two ? s : 0) * L::kTileB), 16);
+    const uint64_t dk = tc::smem_desc(smem_u32(sm + L::kK), 16), dv = tc::smem_desc(smem_u32(sm + L::kV), kPanel);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + 128 * s;
+    const uint32_t to = __shfl_sync(0xffffffffu, tmem, 0) + 256 + D * s;
     const bool elected = tc::elect_one();
-    uint32_t it0 = 0;                // tiles before this segment
-    uint32_t np = 0, nseg = 0;       // phase bits of the streams' hand-overs; segments
+    uint32_t it0 = 0, np = 0, nseg = 0, turns = 0;  // tiles before this segment; phases of the weights; segments; turns
     bool ok = true;
-    // Step u of a segment is stream u & 1's: P V of its tile, then S of step u + 2, which takes P's place.
     do {
       const int nt = __shfl_sync(0xffffffffu, run.j1 - run.j0, 0);
-      const int steps = two ? 2 * nt : nt;
-      ok = wait(&mi.q_full[0], nseg & 1) && (!two || wait(&mi.q_full[1], nseg & 1));
-      ok = __all_sync(0xffffffffu, ok);
+      const int i0 = two ? 0 : s;  // the stream's tiles: i0, i0 + by, ...
+      ok = __all_sync(0xffffffffu, wait(&mi.q_full[two ? s : 0], nseg & 1));
       ++nseg;
+      // step i: P V of tile i (not at first), then S of tile i + by, which takes P's place
 #pragma unroll 1
-      for (int u = -2; u < steps && ok; ++u) {
-        const int s = u & 1;
-        const bool last_use = !two || s == 1;  // of the step's tiles
-        const uint32_t it = it0 + (two ? u >> 1 : u), nx = it + (two ? 1 : 2);
-        const bool now = u >= 0, more = u + 2 < steps;
-        const uint64_t b = dv + (it & 1) * (L::kTileB >> 4);
-        const uint64_t q = dq + (two ? s : 0) * (L::kTileB >> 4), k = dk + (nx & 1) * (L::kTileB >> 4);
-        // what is ready early is waited for first (256 rows: once for both streams), the weights last
-        if (more && !(two && s)) ok = wait(&mi.k_full[nx & 1], (nx >> 1) & 1);
+      for (int i = i0 - by; i < nt && ok; i += by) {
+        const uint32_t it = it0 + i, nx = it + by;
+        const bool now = i >= i0, more = i + by < nt;
+        const uint64_t b = dv + (it & 1) * (L::kTileB >> 4), k = dk + (nx & 1) * (L::kTileB >> 4);
+        // what is ready early is waited for first, the weights last
+        if (more) ok = wait(&mi.k_full[nx & 1], (nx >> 1) & 1);
         if (now) {
-          if (!(two && s)) ok = ok && wait(&mi.v_full[it & 1], (it >> 1) & 1);
-          ok = ok && wait(&mi.p_full[s], (np >> s) & 1);
-          np ^= 1u << s;
+          ok = ok && wait(&mi.v_full[it & 1], (it >> 1) & 1) && wait(&mi.p_full[s], np & 1);
+          ++np;
         }
+        // The streams issue in turn (256 rows): one's softmax then runs beside the other's products.  Left to
+        // themselves they fall into step, and products and softmax alternate (4100 cycles a tile, not 3300).
+        if (two) ok = ok && wait(&mi.turn[s], (turns++ & 1) ^ (s ^ 1));
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc::fence_after();
         if (elected) {
           if (now) {
 #pragma unroll
             for (int x = 0; x < kTok / 16; ++x)
-              tc::mma_ts(tm + 256 + D * s, tm + 128 * s + 8 * x + (x < 4 ? 0 : 32), b + x * (2048 >> 4), id_o, u > 1 || x > 0);
-            if (last_use) tc::commit(&mi.v_empty[it & 1]);
+              tc::mma_ts(to, tm + 8 * x + (x < 4 ? 0 : 32), b + x * (2048 >> 4), id_o, i > i0 || x > 0);
+            tc::commit(&mi.v_empty[it & 1]);
           }
           if (more) {
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
               const uint32_t off = ((x >> 2) * kPanel + (x & 3) * 32) >> 4;
-              tc::mma_ss(tm + 128 * s, q + off, k + off, id_s, x > 0);
+              tc::mma_ss(tm, dq + off, k + off, id_s, x > 0);
             }
             tc::commit(&mi.s_full[s]);
-            if (last_use) tc::commit(&mi.k_empty[nx & 1]);
+            tc::commit(&mi.k_empty[nx & 1]);
           } else if (now) {
             tc::commit(&mi.o_full[s]);
           }
+          if (two) mbar_arrive(&mi.turn[s ^ 1]);
         }
         __syncwarp();
       }
