@@ -4,7 +4,7 @@
 //
 // Mathematics (include/kvq.h gives the exact roundings): rotated keys and the values
 // go to the residual window; a window that fills is cut into blocks of G tokens x D
-// channels, s = max|x| / qmax over the block, code = x / s rounded.
+// channels, s = max|x| * (1 / qmax) over the block, code = x / s rounded.
 //
 // What bounds it: memory for prompts (each row is read once and written once, 16
 // bytes a thread and access), launch latency for decode steps.  A thread owns items of
@@ -291,8 +291,8 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int cl, int ch, const 
   *reinterpret_cast<uint2*>(row + ch) = make_uint2(c.z, c.w);
 }
 
-__device__ __forceinline__ float block_qmax(int fmt) {
-  return fmt == KVQ_FP8_E4M3 ? 448.f : fmt == KVQ_FP8_E5M2 ? 57344.f : 127.f;
+__device__ __forceinline__ float block_rqmax(int fmt) {  // the fp32 numbers nearest to 1 / qmax
+  return fmt == KVQ_FP8_E4M3 ? 1.f / 448.f : fmt == KVQ_FP8_E5M2 ? 1.f / 57344.f : 1.f / 127.f;
 }
 
 struct FoldSmem {
@@ -340,7 +340,7 @@ __device__ void fold_block(const KvqView& v, const BlockAppend& a, FoldSmem& sm,
     mk = fmaxf(mk, sm.mk[i]);
     mv = fmaxf(mv, sm.mv[i]);
   }
-  float ks = __fdiv_rn(mk, block_qmax(v.kfmt)), vs = __fdiv_rn(mv, block_qmax(v.vfmt));
+  float ks = __fmul_rn(mk, block_rqmax(v.kfmt)), vs = __fmul_rn(mv, block_rqmax(v.vfmt));
   if (v.meta16) {
     ks = f16_up(ks);
     vs = f16_up(vs);

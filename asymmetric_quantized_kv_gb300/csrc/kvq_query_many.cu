@@ -46,6 +46,7 @@ constexpr int kConv0 = kSoftWarps, kConvWarps = 4, kLoadWarp = kConv0 + kConvWar
 constexpr int kMThreads = (kMmaWarp + 2) * 32;
 constexpr int kBarStream = 1, kBarJoin = 3;  // named barriers: of the streams (and the next), of both
 constexpr int kSlots = 8;     // tiles whose scales are kept
+constexpr int kSegs = 8;      // segments that are told of
 constexpr float kLazyM = 256.f;  // a piece's weights may sum to this before the maximum is raised
 constexpr float kMinitM = -1e30f;
 
@@ -70,6 +71,17 @@ struct Lay {
   static __device__ __forceinline__ int raw_v(int stage) { return stage ? kQ + kTileB + kRawB : kRawV; }
 };
 
+// A CTA's tiles of one unit, as the copying warp tells the others (who then need no plan of their own).
+struct Seg {
+  int b, h, qt;
+  int T, nq, n, rows;  // of sequence b
+  int j0, j1;          // tiles (none: the run is empty)
+  int ends;            // j1 is the unit's last
+  int i, r;            // the unit's first row: query and head in the group
+  int last;            // nothing follows
+  int pad[3];
+};
+
 struct Misc {
   // of each piece: key scale, log2 of the value scale (-inf: it has no tokens to see), 1 / value scale
   float4 scale[kSlots][kPieces];
@@ -78,19 +90,19 @@ struct Misc {
   uint64_t raw_k_full[2], raw_v_full[2], raw_k_empty[2], raw_v_empty[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2], q_full[2], turn[2];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  Seg seg[kSegs];
   float row_x[2][kRows];        // exchange between the two threads of a row
   uint32_t tmem;
   int abort;
-  int start_b, start_h, start_qt, start_tile;
-  unsigned long long total;
 };
 
 // ---- units
 
 struct Walk {  // one unit, and the CTA's place in it
   int b, h, qt;
-  int T, nq, n, rows, nqt;  // of sequence b
-  int tiles;                // of the unit
+  int T, n, rows, nqt;  // of sequence b
+  int tiles;            // of the unit
 };
 
 // Out of line, like everything that a tile's loop does not run: the tasks' loops share the SM's instruction
@@ -103,7 +115,6 @@ static __device__ __noinline__ int unit_tiles(int causal, int n_rep, int T, int 
 
 static __device__ __noinline__ void load_sequence(const KvqView& v, const QueryArgs& a, int RT, Walk& w) {
   w.T = seq_tokens(v, w.b);
-  w.nq = n_quantized(w.T, v.R);
   w.n = query_count(v, a, w.b);
   w.rows = w.n * v.n_rep;
   w.nqt = (w.rows + RT - 1) / RT;
@@ -136,10 +147,10 @@ struct Pending {
   long long head_off;
   float ks, vs;
 
-  __device__ __forceinline__ void look_up(const KvqView& v, const Walk& w, int j, int lane) {
+  __device__ __forceinline__ void look_up(const KvqView& v, const Walk& w, int nq, int j, int lane) {
     const int32_t* bt = v.block_table + (long long)w.b * v.max_pages;
     t0 = j * kTok;
-    t1 = min(t0 + kTok, w.nq);
+    t1 = min(t0 + kTok, nq);
     const int pg = t0 / v.P + lane;
     p0 = (int)max((long long)t0, min((long long)t1, (long long)pg * v.P));
     p1 = (int)min((long long)t1, ((long long)pg + 1) * v.P);
@@ -177,7 +188,7 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) { 
 
 // A CTA's run over the units.  A unit counts its tiles and kUnitCost more, for what its start and end cost
 // (queries in, outputs out, and products and softmax without each other); these stand before its tiles.
-constexpr int kUnitCost = 2;
+constexpr int kUnitCost = 5;
 struct Run {
   Walk w;
   unsigned long long left;  // of the run, from place p of unit w on
@@ -189,7 +200,7 @@ struct Run {
     j1 = max(0, p + n - kUnitCost);
   }
   // To the next unit with tiles; false at the run's end.
-  __device__ __forceinline__ bool next(const KvqView& v, const QueryArgs& a, int RT) {
+  __device__ __noinline__ bool next(const KvqView& v, const QueryArgs& a, int RT) {
     do {
       const unsigned long long n = min((unsigned long long)(w.tiles + kUnitCost - p), left);
       left -= n;
@@ -200,7 +211,101 @@ struct Run {
     } while (j0 == j1);
     return true;
   }
+  // Whether no unit with tiles follows this one: a next one's first kUnitCost places have none.
+  __device__ __forceinline__ bool last() const {
+    return left - min((unsigned long long)(w.tiles + kUnitCost - p), left) <= kUnitCost;
+  }
 };
+
+static __device__ __noinline__ unsigned long long divide(unsigned long long a, unsigned long long b) { return a / b; }
+
+// This CTA's run (one warp; wb: a number per sequence in shared memory).  False: none.
+static __device__ __noinline__ bool plan_run(const KvqView& v, const QueryArgs& a, int RT, unsigned long long* wb, Run& run) {
+  const int lane = threadIdx.x & 31;
+  auto sum64 = [](unsigned long long x) {
+#pragma unroll 1
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+  };
+  unsigned long long total = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < v.batch; b0 += 32) {  // places of a kv-head of each sequence
+    const int b = b0 + lane;
+    const int T = b < v.batch ? seq_tokens(v, b) : 0, n = b < v.batch ? query_count(v, a, b) : 0, rows = n * v.n_rep;
+    const int nqt = (rows + RT - 1) / RT;
+    unsigned long long s = 0;
+    if (__reduce_max_sync(0xffffffffu, nqt) <= 4) {
+#pragma unroll 1
+      for (int qt = 0; qt < nqt; ++qt) s += unit_tiles(a.causal, v.n_rep, T, n, rows, qt, RT) + kUnitCost;
+    } else {  // long ones: the lanes over a sequence's units
+#pragma unroll 1
+      for (int k = 0; k < min(32, v.batch - b0); ++k) {
+        const int Tk = __shfl_sync(0xffffffffu, T, k), nk = __shfl_sync(0xffffffffu, n, k);
+        const int rk = __shfl_sync(0xffffffffu, rows, k), qk = __shfl_sync(0xffffffffu, nqt, k);
+        unsigned long long x = 0;
+#pragma unroll 1
+        for (int qt = lane; qt < qk; qt += 32) x += unit_tiles(a.causal, v.n_rep, Tk, nk, rk, qt, RT) + kUnitCost;
+        x = sum64(x);
+        if (lane == k) s = x;
+      }
+    }
+    if (b < v.batch) wb[b] = s;
+    total += s;
+  }
+  total = sum64(total) * v.Hkv;
+  // no CTA between two others is left without a place: the merge walks from one to the next
+  const unsigned long long runs = min((unsigned long long)gridDim.x, total), me = blockIdx.x;
+  if (me >= runs) return false;
+  const unsigned long long each = divide(total, runs), more = total - each * runs;  // `more` runs get one place more
+  unsigned long long left = each * me + min(me, more);
+  run.left = each + (me < more ? 1 : 0);
+  Walk& w = run.w;
+  w.b = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < v.batch; b0 += 32) {  // the sequence that holds the first place
+    const unsigned long long x = b0 + lane < v.batch ? wb[b0 + lane] * v.Hkv : 0ull;
+    unsigned long long incl = x;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, incl > left);
+    if (hit) {
+      const int k = __ffs(hit) - 1;
+      w.b = b0 + k;
+      left -= __shfl_sync(0xffffffffu, incl - x, k);
+      break;
+    }
+    left -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+  load_sequence(v, a, RT, w);
+  w.h = (int)divide(left, wb[w.b]);
+  left -= (unsigned long long)w.h * wb[w.b];
+  w.qt = 0;
+#pragma unroll 1
+  for (int q0 = 0; q0 < w.nqt; q0 += 32) {
+    const unsigned x = q0 + lane < w.nqt ? unit_tiles(a.causal, v.n_rep, w.T, w.n, w.rows, q0 + lane, RT) + kUnitCost : 0;
+    unsigned incl = x;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, incl > left);
+    if (hit) {
+      const int k = __ffs(hit) - 1;
+      w.qt = q0 + k;
+      left -= __shfl_sync(0xffffffffu, incl - x, k);
+      break;
+    }
+    left -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+  w.tiles = unit_tiles(a.causal, v.n_rep, w.T, w.n, w.rows, w.qt, RT);
+  run.p = (int)left;
+  run.open();
+  return run.j0 < run.j1 || run.next(v, a, RT);  // a run may lie in what stands before the tiles
+}
 
 // Bounded wait of a task; after a wait that gave up nothing more is waited for.
 struct Waiter {
@@ -297,6 +402,29 @@ __device__ __noinline__ int window_piece(const void* win, const KvqView& v, int 
   return k;
 }
 
+// Place of a row in q and out: rows follow one another head by head within a query, then to the next query's
+// heads of the same kv-head.
+struct RowAt {
+  long long e;
+  int row, r;  // of the sequence and kv-head; its head in the group
+  __device__ __forceinline__ void start(const KvqView& v, const QueryArgs& a, const Seg& g, int RT, int off, int D) {
+    const int x = g.r + off, q = x / v.n_rep;
+    row = g.qt * RT + off;
+    r = x - q * v.n_rep;
+    e = (((long long)g.b * a.n_q + g.i + q) * v.Hq + g.h * v.n_rep + r) * D;
+  }
+  __device__ __forceinline__ void step(const KvqView& v, int n, int D) {
+    row += n;
+    r += n;
+    e += n * D;
+#pragma unroll 1
+    while (r >= v.n_rep) {
+      r -= v.n_rep;
+      e += (v.Hq - v.n_rep) * D;
+    }
+  }
+};
+
 // Arrive once per warp on a barrier that hands shared memory written here to the tensor cores.
 __device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
   fence_proxy_async();
@@ -308,19 +436,24 @@ __device__ __forceinline__ void hand_over(uint64_t* bar, int lane) {
 // Loops are short: the tasks' code together has to stay in the instruction caches.
 
 // Largest x.
+template <bool kMasked>
 __device__ __noinline__ float half_max(uint32_t tS, const float4* sc, float fct, int lim) {
   float mx = -INFINITY;
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t r[16];
-    tc::tmem_ld16(tS + 16 * c, r);
+  for (int c = 0; c < 2; ++c) {
+    uint32_t r[32];
+    tc::tmem_ld32(tS + 32 * c, r);
     tc::wait_ld(r);
-    float m = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) m = 16 * c + e < lim ? fmaxf(m, __uint_as_float(r[e])) : m;
-    // an all-masked piece times a zero scale is NaN, which fmaxf passes over
-    const float4 k = sc[c];
-    mx = fmaxf(mx, fmaf(m, k.x * fct, k.y));
+    for (int h = 0; h < 2; ++h) {
+      float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (!kMasked || 32 * c + 16 * h + e < lim) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(r[16 * h + e]));
+      // an all-masked piece times a zero scale is NaN, which fmaxf passes over
+      const float4 k = sc[2 * c + h];
+      mx = fmaxf(mx, fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), k.x * fct, k.y));
+    }
   }
   return mx;
 }
@@ -360,13 +493,14 @@ __device__ __forceinline__ float half_weights(uint32_t tS, const float4* sc, flo
   return l;
 }
 
-// Barrier of a stream's 256 threads that also says whether any of them asks.
-__device__ __forceinline__ bool stream_any(int bar, bool ask) {
+// Barrier of kThreads threads that also says whether any of them asks.
+template <int kThreads>
+__device__ __forceinline__ bool any_of(int bar, bool ask) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"(bar), "r"((uint32_t)ask)
+      : "r"(bar), "r"((uint32_t)ask), "n"(kThreads)
       : "memory");
   return r != 0;
 }
@@ -383,98 +517,12 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
   const bool two = RT == 2 * kRows;  // a stream per half of the unit; else both over one half
   grid_dep_launch();
 
-  // ---- the CTA's run of tiles
-  unsigned long long* wb = reinterpret_cast<unsigned long long*>(sm);  // places of a kv-head of each sequence
-  if (threadIdx.x == 0) {
-    mi.total = 0ull;
-    mi.abort = 0;
-  }
-  __syncthreads();
-  {
-    // a thread a sequence, or, for few of them, a warp
-    const bool warps = v.batch < kMThreads / 32;
-    unsigned long long mine = 0;
-#pragma unroll 1
-    for (int b = warps ? warp : threadIdx.x; b < v.batch; b += warps ? kMThreads / 32 : kMThreads) {
-      Walk w;
-      w.b = b;
-      load_sequence(v, a, RT, w);
-      unsigned long long s = 0;
-#pragma unroll 1
-      for (int qt = warps ? lane : 0; qt < w.nqt; qt += warps ? 32 : 1) s += unit_tiles(a.causal, v.n_rep, w.T, w.n, w.rows, qt, RT) + kUnitCost;
-      if (warps) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      }
-      if (!warps || lane == 0) {
-        wb[b] = s;
-        mine += s;
-      }
-    }
-    if (mine) atomicAdd(&mi.total, mine);
-  }
-  __syncthreads();
-  const unsigned long long total = mi.total * v.Hkv;
-  // no CTA between two others is left without a tile: the merge walks from one to the next
-  const unsigned long long runs = min((unsigned long long)gridDim.x, total), me = blockIdx.x;
-  const unsigned long long each = total / max(runs, 1ull), more = total - each * runs;  // `more` runs get one place more
-  const unsigned long long w0 = me < runs ? each * me + min(me, more) : 0ull;
-  const unsigned long long w1 = me < runs ? w0 + each + (me < more ? 1 : 0) : 0ull;
   RecHeader* hdr = reinterpret_cast<RecHeader*>(ws) + 2 * blockIdx.x;
   if (threadIdx.x < 2) hdr[threadIdx.x].used = 0;
-  if (w0 == w1) return;
-  if (warp == 0) {
-    unsigned long long left = w0;
-    int b = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < v.batch; b0 += 32) {  // the sequence that holds tile w0
-      const unsigned long long x = b0 + lane < v.batch ? wb[b0 + lane] * v.Hkv : 0ull;
-      unsigned long long incl = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, incl > left);
-      if (hit) {
-        const int k = __ffs(hit) - 1;
-        b = b0 + k;
-        left -= __shfl_sync(0xffffffffu, incl - x, k);
-        break;
-      }
-      left -= __shfl_sync(0xffffffffu, incl, 31);
-    }
-    Walk w;
-    w.b = b;
-    load_sequence(v, a, RT, w);
-    const int h = (int)(left / wb[b]);
-    left -= (unsigned long long)h * wb[b];
-    int qt = 0;
-#pragma unroll 1
-    for (int q0 = 0; q0 < w.nqt; q0 += 32) {
-      const unsigned x = q0 + lane < w.nqt ? unit_tiles(a.causal, v.n_rep, w.T, w.n, w.rows, q0 + lane, RT) + kUnitCost : 0;
-      unsigned incl = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, incl > left);
-      if (hit) {
-        const int k = __ffs(hit) - 1;
-        qt = q0 + k;
-        left -= __shfl_sync(0xffffffffu, incl - x, k);
-        break;
-      }
-      left -= __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) {
-      mi.start_b = b;
-      mi.start_h = h;
-      mi.start_qt = qt;
-      mi.start_tile = (int)left;
-    }
-  }
+  if (threadIdx.x == 0) mi.abort = 0;
+  Run run;
+  bool some = false;
+  if (warp == kLoadWarp) some = plan_run(v, a, RT, reinterpret_cast<unsigned long long*>(sm), run);
   if (warp == kMmaWarp) {
     tc::tmem_alloc(&mi.tmem, 512);
     if (lane == 0) {
@@ -493,6 +541,10 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         mbar_init(&mi.o_full[i], 1);
         mbar_init(&mi.q_full[i], 8);
       }
+      for (int i = 0; i < kSegs; ++i) {
+        mbar_init(&mi.seg_full[i], 1);
+        mbar_init(&mi.seg_empty[i], kSoftWarps + kConvWarps + 2);
+      }
       fence_mbar_init();
     }
   }
@@ -502,37 +554,57 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
   const uint32_t tmem = mi.tmem;
   const Waiter wait{mi, v.status};
 
-  Run run;
-  Walk& w = run.w;
-  w.b = mi.start_b;
-  w.h = mi.start_h;
-  w.qt = mi.start_qt;
-  load_sequence(v, a, RT, w);
-  w.tiles = unit_tiles(a.causal, v.n_rep, w.T, w.n, w.rows, w.qt, RT);
-  run.p = mi.start_tile;
-  run.left = w1 - w0;
-  run.open();
-  const bool some = run.j0 < run.j1 || run.next(v, a, RT);  // a run may lie in what stands before the tiles
+  // The next segment (every warp but the copying one): it is read whole and its place given back.
+  uint32_t nseg = 0;
+  auto segment = [&](Seg& g) -> bool {
+    const uint32_t k = nseg % kSegs;
+    const bool ok = wait(&mi.seg_full[k], (nseg / kSegs) & 1);
+    g = mi.seg[k];
+    ++nseg;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&mi.seg_empty[k]);
+    return __all_sync(0xffffffffu, ok);
+  };
 
-  // Every task walks the same segments: tiles [j0, j1) of unit w.
-  if (!some) {
-  } else
   if (warp == kLoadWarp) {
     // Tiles pass through three steps, one tile apart, so that no load's latency is waited for: page ids
     // (lane i: the tile's i-th page, and the page of piece i's scales), then scales, then the copies.
     Pending p2, p1, p0;
     p1.some = p0.some = false;
-    bool todo = true;  // tiles not yet looked up: j of the run's unit
-    int j = run.j0;
+    const Walk& w = run.w;
     bool ok = true;
     uint32_t it = 0;  // tiles copied
+    int nq = 0, j = 0;
+    auto tell = [&]() {
+      const uint32_t k = nseg % kSegs;
+      ok = ok && __all_sync(0xffffffffu, wait(&mi.seg_empty[k], ((nseg / kSegs) & 1) ^ 1));
+      ++nseg;
+      nq = n_quantized(w.T, v.R);
+      j = run.j0;
+      if (lane == 0) {
+        const int i = w.qt * RT / v.n_rep;
+        mi.seg[k] = Seg{w.b, w.h, w.qt, w.T, nq, w.n, w.rows, run.j0, run.j1, run.j1 == w.tiles,
+                        i, w.qt * RT - i * v.n_rep, run.last(), {0, 0, 0}};
+        mbar_arrive(&mi.seg_full[k]);
+      }
+      __syncwarp();
+    };
+    if (some) {
+      tell();
+    } else if (lane == 0) {
+      mi.seg[0] = Seg{};
+      mi.seg[0].last = 1;
+      mbar_arrive(&mi.seg_full[0]);
+    }
+    bool todo = some;  // tiles not yet looked up: j of the run's unit
     for (;;) {
       p2.some = todo;
       if (todo) {
-        p2.look_up(v, w, j, lane);
+        p2.look_up(v, w, nq, j, lane);
         if (++j == run.j1) {
           todo = run.next(v, a, RT);
-          j = run.j0;
+          if (todo) tell();
+          if (!ok) break;
         }
       }
       if (p1.some) p1.read_scales(v, D, lane);
@@ -583,8 +655,10 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
   } else if (warp >= kConv0 && warp < kConv0 + kConvWarps) {
     uint32_t it = 0;
     bool ok = true;
+    Seg w;
     do {
-      for (int j = run.j0; j < run.j1; ++j, ++it) {
+      if (!(ok = segment(w))) break;
+      for (int j = w.j0; j < w.j1; ++j, ++it) {
         const int t0 = j * kTok, slot = it % kSlots, st = it & 1;
         const uint32_t ph = (it >> 1) & 1, rp = two ? it & 1 : ph;
         const int rs = two ? 0 : st;
@@ -633,7 +707,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         if (lane == 0) mbar_arrive(&mi.raw_v_empty[rs]);
         hand_over(&mi.v_full[st], lane);
       }
-    } while (ok && run.next(v, a, RT));
+    } while (ok && !w.last);
   } else if (warp >= kMmaWarp) {
     // A warp a stream, so that one's waits do not hold up the other's products (issuing blocks until the
     // products before are nearly done).  The whole warp walks the steps with values it knows to be uniform,
@@ -647,13 +721,14 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + 128 * s;
     const uint32_t to = __shfl_sync(0xffffffffu, tmem, 0) + 256 + D * s;
     const bool elected = tc::elect_one();
-    uint32_t it0 = 0, np = 0, nseg = 0, turns = 0;  // tiles before this segment; phases of the weights; segments; turns
+    uint32_t it0 = 0, np = 0, turns = 0;  // tiles before this segment; phases of the weights; turns
     bool ok = true;
+    Seg w;
     do {
-      const int nt = __shfl_sync(0xffffffffu, run.j1 - run.j0, 0);
+      if (!segment(w) || w.j0 == w.j1) break;
+      const int nt = __shfl_sync(0xffffffffu, w.j1 - w.j0, 0);
       const int i0 = two ? 0 : s;  // the stream's tiles: i0, i0 + by, ...
-      ok = __all_sync(0xffffffffu, wait(&mi.q_full[two ? s : 0], nseg & 1));
-      ++nseg;
+      ok = __all_sync(0xffffffffu, wait(&mi.q_full[two ? s : 0], (nseg - 1) & 1));
       // step i: P V of tile i (not at first), then S of tile i + by, which takes P's place
 #pragma unroll 1
       for (int i = i0 - by; i < nt && ok; i += by) {
@@ -694,7 +769,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         __syncwarp();
       }
       it0 += nt;
-    } while (ok && run.next(v, a, RT));
+    } while (ok && !w.last);
   } else {  // ---- softmax streams: warp = 8 stream + 4 half + quarter of the rows
     const int s = __shfl_sync(0xffffffffu, warp >> 3, 0), hf = (warp >> 2) & 1, row_l = threadIdx.x & (kRows - 1);
     const uint32_t lane_off = (uint32_t)(warp & 3) << 21;  // 32 lanes a warp, in the address's upper half
@@ -703,41 +778,50 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
     float* rx = &mi.row_x[s][row_l];
     uint32_t ns = 0, it0 = 0, no = 0;
     bool ok = true;
+    // Query rows come, and outputs leave, 16 rows a warp with the lanes along them.
+    constexpr int CPR = D / 8, RPP = 32 / CPR, NP = 16 / RPP;  // chunks a row, rows a pass, passes
+    const int r0 = (warp & 7) * 16 + lane / CPR, c8 = lane % CPR;
+    uint8_t* const qd = sm + L::kQ + (two ? s : 0) * L::kTileB;
+    Seg w;
     do {
-      const int j0 = run.j0, j1 = run.j1, nt = j1 - j0;
-      const int row = w.qt * RT + (two ? s * kRows : 0) + row_l;  // of the sequence and kv-head
-      const bool live = row < w.rows;
-      const int qi = live ? row / v.n_rep : 0;
-      // ---- the stream's query rows into f16, K-major, 16 rows a warp with the lanes along them; rows past the
-      // last are zeros.  Each row's power of two goes to its threads.
+      // (threads that share barriers give up together)
+      ok = segment(w);
+      if (any_of<2 * kRows>(kBarStream + s, !ok) || w.j0 == w.j1) break;
+      const int j0 = w.j0, nt = w.j1 - w.j0;
+      const int off = two ? s * kRows : 0;                     // the stream's first row in the unit
+      const bool live = w.qt * RT + off + row_l < w.rows;
+      const int qi = w.i + (w.r + off + row_l) / v.n_rep;
+      // ---- the stream's query rows into f16, K-major; rows past the last are zeros.  Each row's power of two goes
+      // to its threads.
+      RowAt at;  // row r0
+      at.start(v, a, w, RT, off + r0, D);
       {
-        constexpr int CPR = D / 8, RPP = 32 / CPR, NP = 16 / RPP;  // chunks a row, rows a pass, passes
-        const int r0 = (warp & 7) * 16 + lane / CPR, c = lane % CPR;
-        uint8_t* qd = sm + L::kQ + (two ? s : 0) * L::kTileB;
-        uint4 x[NP];
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const int rr = w.qt * RT + (two ? s * kRows : 0) + r0 + i * RPP;
-          x[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (rr < w.rows) {
-            const long long e = (((long long)w.b * a.n_q + rr / v.n_rep) * v.Hq + w.h * v.n_rep + rr % v.n_rep) * D + 8 * c;
-            x[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + e);
-          }
-        }
+        RowAt k = at;
         if (it0 > 0) named_bar_sync(kBarStream + s, 2 * kRows);  // the last segment's rows have left the tile
+#pragma unroll 1
+        for (int i0 = 0; i0 < NP; i0 += 4) {
+          uint4 x[4];
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const uint32_t m2 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(0u, x[i].x), x[i].y), x[i].z), x[i].w);
-          uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+          for (int i = 0; i < 4; ++i) {
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (k.row < w.rows) x[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + k.e + 8 * c8);
+            k.step(v, RPP, D);
+          }
 #pragma unroll
-          for (int o = CPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          float down, up;
-          norm_factors(top, down, up);
-          if (c == 0) mi.row_x[s][r0 + i * RPP] = up;
-          if (two || s == 0)
-            *reinterpret_cast<uint4*>(qd + tile_chunk(r0 + i * RPP, c)) =
-                make_uint4(bf16x2_scaled(x[i].x, down), bf16x2_scaled(x[i].y, down), bf16x2_scaled(x[i].z, down),
-                           bf16x2_scaled(x[i].w, down));
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t m2 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(0u, x[i].x), x[i].y), x[i].z), x[i].w);
+            uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+            for (int o = CPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            float down, up;
+            norm_factors(top, down, up);
+            const int r = r0 + (i0 + i) * RPP;
+            if (c8 == 0) mi.row_x[s][r] = up;
+            if (two || s == 0)
+              *reinterpret_cast<uint4*>(qd + tile_chunk(r, c8)) =
+                  make_uint4(bf16x2_scaled(x[i].x, down), bf16x2_scaled(x[i].y, down), bf16x2_scaled(x[i].z, down),
+                             bf16x2_scaled(x[i].w, down));
+          }
         }
         if (two || s == 0) hand_over(&mi.q_full[s], lane);
         named_bar_sync(kBarStream + s, 2 * kRows);
@@ -758,16 +842,15 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         // With the standing maximum first: it holds for nearly every tile.  The weights stay in registers
         // until both halves of every row have agreed to it.
         uint32_t pk[32];
-        float top, sum;
-        if (!any) top = INFINITY;  // nothing stands yet
-        else sum = masked ? half_weights<true>(tS, sc, fct, M, lim, pk, top) : half_weights<false>(tS, sc, fct, M, lim, pk, top);
+        float top = INFINITY, sum = 0.f;  // nothing stands before the first tile
+        if (any) sum = masked ? half_weights<true>(tS, sc, fct, M, lim, pk, top) : half_weights<false>(tS, sc, fct, M, lim, pk, top);
         // (a stream whose wait gave up stops as one: the barrier carries that too)
-        if (stream_any(kBarStream + s, top > kLazyM || !ok)) {
-          if (stream_any(kBarStream + s, !ok)) {
+        if (any_of<2 * kRows>(kBarStream + s, top > kLazyM || !ok)) {
+          if (any_of<2 * kRows>(kBarStream + s, !ok)) {
             ok = false;
             break;
           }
-          const float mx = half_max(tS, sc, fct, lim);
+          const float mx = masked ? half_max<true>(tS, sc, fct, lim) : half_max<false>(tS, sc, fct, lim);
           if (hf) *rx = mx;
           named_bar_sync(kBarStream + s, 2 * kRows);
           float mn = M;
@@ -791,7 +874,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
               tc::tmem_st16(tO + c, r);
             }
           }
-          sum = half_weights<true>(tS, sc, fct, M, lim, pk, top);
+          sum = masked ? half_weights<true>(tS, sc, fct, M, lim, pk, top) : half_weights<false>(tS, sc, fct, M, lim, pk, top);
         }
         any = true;
         l += sum;
@@ -807,8 +890,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         ++no;
         tc::fence_after();
       }
-      ok = __all_sync(0xffffffffu, ok);
-      named_bar_sync(kBarStream + s, 2 * kRows);
+      ok = !any_of<2 * kRows>(kBarStream + s, !ok);
       if (hf) *rx = l;
       named_bar_sync(kBarStream + s, 2 * kRows);
       if (!hf) {
@@ -822,7 +904,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         // a time
         float* ex = reinterpret_cast<float*>(sm + L::kQ) + hf * (16 * kRows);
         float* ml = mi.row_x[0];
-        named_bar_sync(kBarJoin, 4 * kRows);  // both streams' sums have been read
+        ok = !any_of<4 * kRows>(kBarJoin, !ok);  // both streams' sums have been read
         if (s == 1 && !hf) {
           ml[row_l] = any ? M : kMinitM;
           ml[kRows + row_l] = any ? l : 0.f;
@@ -860,7 +942,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           named_bar_sync(kBarJoin, 4 * kRows);  // stream 0 has read the statistics
         }
       }
-      const bool begins = j0 == 0, ends = j1 == w.tiles;
+      const bool begins = j0 == 0, ends = w.ends;
       if (ok && (two || s == 0)) {
         const bool first = it0 == 0;
         const bool whole = begins && ends;
@@ -874,7 +956,6 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           if (live && !hf) *reinterpret_cast<float4*>(rec) = make_float4(M, l, 0.f, 0.f);
         }
         // a whole unit's rows leave through the Q tile (its products are done), lanes along the rows
-        uint8_t* qd = sm + L::kQ + (two ? s : 0) * L::kTileB;
 #pragma unroll 1
         for (int c = 0; c < kOutC; c += 16) {
           uint32_t r[16];
@@ -901,22 +982,18 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         }
         if (whole) {
           named_bar_sync(kBarStream + s, 2 * kRows);
-          constexpr int CPR = D / 8, RPP = 32 / CPR, NP = 16 / RPP;
-          const int r0 = (warp & 7) * 16 + lane / CPR, c = lane % CPR;
-#pragma unroll 4
+#pragma unroll 1
           for (int i = 0; i < NP; ++i) {
-            const int rr = w.qt * RT + (two ? s * kRows : 0) + r0 + i * RPP;
-            if (rr < w.rows) {
-              const long long e = (((long long)w.b * a.n_q + rr / v.n_rep) * v.Hq + w.h * v.n_rep + rr % v.n_rep) * D + 8 * c;
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + e) =
-                  *reinterpret_cast<const uint4*>(qd + tile_chunk(r0 + i * RPP, c));
-            }
+            if (at.row < w.rows)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at.e + 8 * c8) =
+                  *reinterpret_cast<const uint4*>(qd + tile_chunk(r0 + i * RPP, c8));
+            at.step(v, RPP, D);
           }
         }
       }
       tc::fence_before();
       it0 += nt;
-    } while (ok && run.next(v, a, RT));
+    } while (ok && !w.last);
   }
   tc::fence_before();
   __syncthreads();

@@ -85,9 +85,10 @@
  *   PER_BLOCK:  one scale per (kv-head, block of `group` tokens), over all
  *               head_dim channels, blocks aligned to absolute token index
  *               multiples of `group` (a multiple of 16).  Formats of 8 bits
- *               only: sym INT8 (s = a/127, the sym INT-b rule over the block)
- *               and FP8 (s = a/448 for E4M3, a/57344 for E5M2, a = max|x| over
- *               the block; y = x/s and the encoding as above).  Keys and values
+ *               only, sym INT8 and FP8, by the rules above with the block as the
+ *               group and s = a*r in place of the division: a = max|x| over the
+ *               block, r the fp32 number nearest to 1/127 (INT8), 1/448 (E4M3),
+ *               1/57344 (E5M2).  Keys and values
  *               are PER_BLOCK together, with one `group`; their formats may
  *               differ.  Source tensors and windows are 16-byte aligned.
  *               A non-finite key or value makes its block's scale, and with it

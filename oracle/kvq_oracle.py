@@ -39,8 +39,8 @@ Everything here is the plain definition, written for a reader to check by eye:
   d = max(mx - mn16, 1e-8), so the top code never clips.  Values beyond the
   binary16 range saturate (scale 65504, minimum -65504).
 * Block scales (axis PER_BLOCK; 8-bit formats): one scale per block of G tokens and
-  kv-head, over all channels: sym INT8 by the absmax rule above, FP8 with
-  s = absmax / (448 or 57344) and the byte of x/s.
+  kv-head, over all channels, s = fl32(absmax * fl32(1 / qmax)) with qmax 127, 448
+  or 57344; sym INT8 codes by the rule above, FP8 the byte of x/s.
 * Position rotation on append (rope_rows): the table's cosine and sine, one fp32
   operation per product and sum, then one rounding to the source dtype.
 * Axes: K per channel over G-token groups, V per token ("Why Keys Are More
@@ -432,13 +432,14 @@ def _quant_block(x, spec: QSpec, meta16=False):
     n, D = x.shape
     xg = x.reshape(n // spec.group, spec.group * D)
     a = np.max(np.abs(xg), axis=1, keepdims=True) if n else np.zeros((0, 1))
+    s = fl32(a * fl32(1.0 / (fp8_max(spec.fmt) if is_fp8(spec.fmt) else 127.0)))
+    if meta16:
+        s = f16_up(s)
     if is_fp8(spec.fmt):
-        s = fl32(a / fp8_max(spec.fmt))
-        if meta16:
-            s = f16_up(s)
         c = quant_fp8(xg, s, spec.fmt)
     else:
-        c, s = (quant_sym16 if meta16 else quant_sym)(xg, a, 8)
+        with np.errstate(divide="ignore", invalid="ignore"):
+            c = np.where(s == 0.0, 0.0, np.clip(np.rint(fl32(xg / s)), -127, 127)).astype(np.int64)
     return c.reshape(n, D), s[:, 0], None
 
 
