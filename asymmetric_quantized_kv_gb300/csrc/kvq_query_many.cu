@@ -737,16 +737,14 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         const uint64_t b = dv + (it & 1) * (L::kTileB >> 4), k = dk + (nx & 1) * (L::kTileB >> 4);
         // what is ready early is waited for first, the weights last
         if (more) ok = wait(&mi.k_full[nx & 1], (nx >> 1) & 1);
-        if (now) {
-          ok = ok && wait(&mi.v_full[it & 1], (it >> 1) & 1) && wait(&mi.p_full[s], np & 1);
-          ++np;
-        }
+        if (now) ok = ok && wait(&mi.v_full[it & 1], (it >> 1) & 1);
         // The streams issue in turn (256 rows): one's softmax then runs beside the other's products.  Left to
         // themselves they fall into step, and products and softmax alternate (4100 cycles a tile, not 3300).
         if (two) ok = ok && wait(&mi.turn[s], (turns++ & 1) ^ (s ^ 1));
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        ok = __all_sync(0xffffffffu, ok);
+        if (now) ok = ok && wait(&mi.p_full[s], np++ & 1);
         tc::fence_after();
-        if (elected) {
+        if (elected && ok) {
           if (now) {
 #pragma unroll
             for (int x = 0; x < kTok / 16; ++x)
@@ -766,7 +764,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           }
           if (two) mbar_arrive(&mi.turn[s ^ 1]);
         }
-        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
       }
       it0 += nt;
     } while (ok && !w.last);
