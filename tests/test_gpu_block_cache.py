@@ -55,6 +55,10 @@ CASES = {
     "meta16_int8_p16": (cfg_of(8, 8, 64, I8, I8, 32, 32, 16, meta_dtype=O.F16), [40, 33, 0]),
     "f32": (cfg_of(8, 2, 128, E4, E4, 64, 64, 64, src=O.F32), [1, 64, 130]),
     "f32_int8_d64": (cfg_of(4, 4, 64, I8, I8, 16, 48, 16, src=O.F32), [47, 48, 100]),
+    "p48_g16": (cfg_of(8, 2, 128, E4, E4, 16, 48, 48), [47, 48, 49, 500]),     # pages that end inside a tile
+    "p80_g16_d64": (cfg_of(12, 4, 64, I8, I8, 16, 32, 80), [79, 80, 161, 640]),
+    "p48_g48": (cfg_of(8, 2, 128, I8, I8, 48, 96, 48), [95, 96, 300]),         # blocks that end inside a tile
+    "p96_g48_d64": (cfg_of(4, 4, 64, E5, E5, 48, 48, 96), [100, 480]),
     "group_512": (cfg_of(8, 2, 128, I8, I8, 512, 512, 64), [511, 512, 1300]),  # more than registers hold
 }
 
@@ -242,6 +246,8 @@ ROT = {  # name: (config, rot, halves, chunk sizes)
     "one_head": (cfg_of(3, 1, 128, E4, E4, 64, 64, 256), 96, False, [2, 70]),
     "many_heads": (cfg_of(24, 12, 64, E4, E4, 64, 64, 64), 64, True, [1, 66]),
     "f32": (cfg_of(4, 2, 128, E4, E4, 32, 64, 32, src=O.F32), 128, True, [4, 40, 1]),
+    "p48_g16": (cfg_of(8, 2, 128, E4, E4, 16, 48, 48), 128, True, [40, 1, 90]),
+    "p48_g48": (cfg_of(4, 2, 128, I8, I8, 48, 96, 48), 32, False, [3, 100]),
     "meta16": (cfg_of(4, 2, 128, I8, I8, 32, 64, 32, meta_dtype=O.F16), 32, False, [1, 33]),
     "group_512": (cfg_of(4, 2, 128, I8, I8, 512, 512, 64), 128, True, [300]),
     "other_kivi2": (OTHER["kivi2"][0], 128, True, [1, 100, 30]),
@@ -437,3 +443,159 @@ def test_binding_refusals():
             f()
             print("not refused:", i)
     assert c.seq_lens.tolist() == [10, 20]
+
+
+# --------------------------------------------------------------- what must not be read, or lies far
+
+SOILED = ["e4m3_p64", "int8_p16", "e5m2_p256", "d64", "nrep16", "d256", "f32", "p48_g16"]
+
+
+@pytest.mark.parametrize("name", SOILED)
+def test_what_lies_behind_a_sequence_is_not_read(name):
+    """NaN bytes in unused pages and slots, NaN and infinities in unused window rows, page ids of no page behind
+    each sequence's last: the outputs are those of a clean cache, bit for bit, in every kernel."""
+    cfg, lens = CASES[name]
+    c = Case(cfg, lens, seed=21)
+    c.name = name
+    n_pages, P = c.cache.n_pages, cfg.page_size
+    calls = [(1, True), (5, True), (5, False), (48, True), (48, False)]
+    q = {n: torch_src(O.bf16(np.random.default_rng(n).standard_normal((len(lens), n, cfg.num_q_heads, cfg.head_dim))), cfg)
+         for n in (1, 5, 48)}
+    clean = [c.cache.query_attention(q[n], causal=k) for n, k in calls] + [c.cache.attention(q[1][:, 0].contiguous())]
+    pages, defined = c.oracle_pages()
+    soiled = c.cache.page_view().cpu().numpy().copy()
+    soiled[~defined] = 0xFF
+    c.cache.page_view().copy_(torch.from_numpy(soiled))
+    for b, T in enumerate(lens):
+        r = T % cfg.residual
+        c.cache.k_win[b, r:] = float("nan")
+        c.cache.v_win[b, r:] = float("inf")
+        used = -(-(T - r) // P)
+        c.cache.block_table[b, used:] = torch.tensor([n_pages + 7, -3] * c.maxp, dtype=torch.int32)[:c.maxp - used].cuda()
+    again = [c.cache.query_attention(q[n], causal=k) for n, k in calls] + [c.cache.attention(q[1][:, 0].contiguous())]
+    for (n, k), a, b in zip(calls + [("decode", 0)], clean, again):
+        assert torch.equal(a, b), (n, k)
+    assert int(c.cache.status.item()) == 0
+
+
+def test_pool_beyond_four_gigabytes():
+    """The same cache at the start of a small pool and at the end of one of 5 GB."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(16, 4, 128, E4, E4, 64, 64, 64)
+    _, tt = rope_setup(1024, 128)
+    rope = K.make_rope(tt, 128, K.KVQ_ROPE_HALVES)
+    small = Case(cfg, [0, 0], seed=1, extra_pages=12, permute_pages=False).cache
+    n_pages = 5 * (1 << 30) // small.page_bytes
+    far = K.PagedKVCache.over(small.cfg, torch.empty(n_pages * small.page_bytes, dtype=torch.uint8, device="cuda"),
+                              small.block_table + (n_pages - small.n_pages), small.seq_lens.clone(), small.k_win.clone(),
+                              small.v_win.clone())
+    for n in (400, 1, 60, 1):
+        x = torch.randn(2, n, 24, 128, device="cuda").bfloat16()
+        outs = []
+        for cache in (small, far):
+            q = cache.append_rope(rope, x[:, :, :16], x[:, :, 16:20], x[:, :, 20:])
+            outs.append((q, cache.query_attention(q), cache.query_attention(q[:, :1].contiguous(), causal=False),
+                         cache.attention(q[:, 0].contiguous())))
+        assert all(torch.equal(a, b) for a, b in zip(*outs)), n
+        assert bool(torch.isfinite(outs[1][1]).all())
+    used = far.page_view()[n_pages - small.n_pages:]
+    nq = 462 // 64 * 64
+    for b in range(2):
+        rows = small.block_table[b, :nq // 64].long()
+        assert torch.equal(used[rows], small.page_view()[rows])
+    assert int(small.status.item()) == 0 and int(far.status.item()) == 0
+
+
+def test_another_stream():
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(8, 2, 128, E4, E4, 64, 64, 64)
+    _, tt = rope_setup(512, 128)
+    rope = K.make_rope(tt, 128)
+    a, b = (Case(cfg, [100, 70], seed=6, extra_pages=4).cache for _ in range(2))
+    x = torch.randn(2, 70, 12, 128, device="cuda").bfloat16()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    qa = a.append_rope(rope, x[:, :, :8], x[:, :, 8:10], x[:, :, 10:])
+    oa = a.query_attention(qa)
+    qb, ob = torch.empty_like(qa), torch.empty_like(oa)
+    b.append_rope(rope, x[:, :, :8], x[:, :, 8:10], x[:, :, 10:], q_out=qb, stream=side)
+    b.query_attention(qb, out=ob, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(qa, qb) and torch.equal(oa, ob) and torch.equal(a.pages, b.pages)
+
+
+def test_decode_without_a_workspace():
+    import asymmetric_quantized_kv_gb300 as K
+    cfg, lens = CASES["int8_p16"]
+    c = Case(cfg, lens, seed=3)
+    q = torch_src(c.queries(), cfg)
+    out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    K.kvq_decode_attention_noalloc(c.c_cfg, c.cache.c, q, out, 0.0)
+    assert torch.equal(out, c.cache.attention(q))
+
+
+def test_append_to_a_missing_page():
+    """Rows and scales of a block-table entry outside the pool are not written anywhere; the rest is."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(8, 2, 128, E4, E4, 32, 64, 32)
+    for n in (1, 130):
+        c = Case(cfg, [127, 127], seed=5, extra_pages=8)
+        good = Case(cfg, [127, 127], seed=5, extra_pages=8)
+        c.cache.block_table[1, 3] = c.cache.n_pages + 5   # tokens 96 .. 127
+        k, v = (torch.randn(2, n, 2, 128, device="cuda").bfloat16() for _ in range(2))
+        for x in (c, good):
+            x.cache.append(k, v)
+        assert int(c.cache.status.item()) == K.KVQ_DEV_BAD_PAGE
+        assert c.cache.seq_lens.tolist() == [127 + n] * 2
+        keep = torch.ones(c.cache.n_pages, dtype=torch.bool)
+        keep[int(c.block_table[1, 3])] = False
+        assert torch.equal(c.cache.page_view()[keep.cuda()], good.cache.page_view()[keep.cuda()])
+        assert torch.equal(c.cache.k_win, good.cache.k_win)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -60, 2.0 ** -20, 2.0 ** 30, 2.0 ** 90])
+def test_values_of_any_magnitude(scale):
+    """Value blocks whose scales differ by far, and all of them far from 1: the weights carry the scale's exponent."""
+    cfg = cfg_of(8, 2, 128, E4, E4, 64, 64, 64)
+    g = np.random.default_rng(4)
+    lens = [300, 200]
+    Ks = [[O.bf16(g.standard_normal((T, 128))) for _ in range(2)] for T in lens]
+    Vs = [[O.bf16(g.standard_normal((T, 128)) * scale * np.where((np.arange(T) // 64) % 2, 2.0 ** -12, 1.0)[:, None])
+           for _ in range(2)] for T in lens]
+    c = Case(cfg, lens, seed=1, streams=(Ks, Vs))
+    c.name = "magnitude"
+    for n in (1, 7, 40):
+        check_queries(c, n, True)
+        check_queries(c, n, False)
+    c.check_attention()
+
+
+def test_zero_keys_values_and_queries():
+    cfg = cfg_of(8, 2, 128, E4, E4, 64, 64, 64)
+    z = [[np.zeros((T, 128)) for _ in range(2)] for T in (130, 64)]
+    c = Case(cfg, [130, 64], seed=1, streams=(z, z))
+    c.name = "zeros"
+    for n in (1, 40):
+        check_queries(c, n, True)
+        q = torch.zeros(2, n, 8, 128, device="cuda").bfloat16()
+        assert not bool(c.cache.query_attention(q).any())
+
+
+def test_logits_far_apart():
+    """Each tile's logits far above the last's (and then far below): the running maximum moves in every tile."""
+    cfg = cfg_of(8, 2, 128, I8, I8, 16, 16, 64)
+    T = 640
+    up = np.arange(T) / 20.0
+    for ramp in (up, up[::-1].copy(), np.where(np.arange(T) == 500, 60.0, 0.0)):
+        K_ = np.zeros((T, 128))
+        K_[:, 0] = ramp
+        Ks = [[O.bf16(K_), O.bf16(-K_)]]
+        Vs = [[O.bf16(np.random.default_rng(h).standard_normal((T, 128))) for h in range(2)]]
+        c = Case(cfg, [T], seed=1, streams=(Ks, Vs))
+        c.name = "ramp"
+        for n in (2, 40, 80):
+            q = np.zeros((1, n, 8, 128), np.float32)
+            q[..., 0] = 24.0
+            check_queries(c, n, True, q=q)
+            check_queries(c, n, False, q=q)
