@@ -165,13 +165,25 @@ bool query_tc_eligible(const KvqView& v) {
   return query_tc_shape(v) && (long long)v.n_pages * v.page_bytes / 128 < (1LL << 31) && tensor_map_encoder() != nullptr;
 }
 
-// Which of the two: the few-row kernel reads the cache once per 32 rows (16 at head_dim 256) at close to the
-// memory's rate; the many-row kernel reads it once per 256 and multiplies at the tensor cores' rate, but a unit of
-// its work starts and ends slowly.  head_dim 256 and fp32 output exceed the latter's shared and tensor memory.
-static bool takes_few(const KvqView& v, long long rows, int out_f32) { return rows <= kFewPass || v.D > 128 || out_f32; }
+// Which of the two: the few-row kernel reads the cache once per 32 rows (16 at head_dim 256 or with fp32 output) at
+// close to the memory's rate; the many-row kernel reads it once per 256 and multiplies at the tensor cores' rate, but
+// a unit of its work starts and ends slowly.  So the former takes up to 32 rows, and more where the call is small
+// by the tokens that its block table could hold (few-row against many-row kernel, us): 40 rows over 8 heads x 2,992
+// tokens 15 and 29, 64 rows over 512 x 224 40 and 50, 160 rows over 16 x 458 17 and 19; beyond the bounds 36 rows over
+// 128 x 4,096 97 and 84, 64 rows over 56 x 5,666 75 and 58, 264 rows over 216 x 128 55 and 32.  head_dim 256 and
+// fp32 output exceed the many-row kernel's shared and tensor memory.
+static bool takes_few(const KvqView& v, int batch, long long rows, int out_f32, long long tokens) {
+  if (rows <= kFewPass || v.D > 128 || out_f32) return true;
+  const long long pairs = (long long)batch * v.Hkv, units = pairs * ((rows + kFewPass - 1) / kFewPass);
+  const double products = (double)rows * (double)pairs * (double)tokens * v.D;
+  return rows <= 2 * kFewPass ? units <= 4096 && products <= 2147483648.0
+                              : rows <= kFewPasses * kFewPass && units <= 1024 && products <= 536870912.0;
+}
 
-static size_t few_bytes(const KvqView& v, int batch, long long rows) {
-  const size_t units = (size_t)kFewUnits + (size_t)batch * v.Hkv, r = (size_t)(rows < kFewPass ? rows : kFewPass);
+static size_t few_bytes(const KvqView& v, int batch, long long rows, int out_f32) {
+  const long long pass = v.D > 128 || out_f32 ? 16 : kFewPass;
+  const size_t passes = (size_t)(rows < pass * kFewPasses ? (rows + pass - 1) / pass : kFewPasses);
+  const size_t units = (size_t)kFewUnits + (size_t)batch * v.Hkv * passes, r = (size_t)(rows < pass ? rows : pass);
   return few_header_bytes(batch) + units * r * (v.D + 4) * sizeof(float);
 }
 
@@ -180,21 +192,24 @@ size_t query_workspace_bytes(const KvqView& v, int batch, int n_q) {
   b.batch = batch;
   if (!query_tc_shape(b)) return 256;
   const long long rows = (long long)n_q * v.n_rep;
-  return takes_few(v, rows, 0) ? few_bytes(v, batch, rows) : query_many_workspace_bytes(v, batch, n_q);
+  const size_t few = takes_few(v, batch, rows, 0, 0) ? few_bytes(v, batch, rows, 0) : 0;
+  if (takes_few(v, batch, rows, 0, 1LL << 62)) return few;
+  const size_t many = query_many_workspace_bytes(v, batch, n_q);
+  return few > many ? few : many;
 }
 
-// A decode call's (fp32 output, in passes of at most 16 rows).
+// A decode call's (fp32 output, in passes of 16 rows).
 size_t decode_workspace_bytes(const KvqView& v, int batch) {
   KvqView b = v;
   b.batch = batch;
-  return query_tc_shape(b) ? few_bytes(v, batch, v.n_rep < 16 ? v.n_rep : 16) : 256;
+  return query_tc_shape(b) ? few_bytes(v, batch, v.n_rep, 1) : 256;
 }
 
 kvq_status launch_query(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st) {
   const long long rows = (long long)a.n_q * v.n_rep;
-  if (!query_tc_eligible(v) || rows >= (1LL << 30) || (long long)v.batch * v.Hkv * kFewPass > 0x7FFFFFFFLL)
+  if (!query_tc_eligible(v) || rows >= (1LL << 30) || (long long)v.batch * v.Hkv * kFewPasses * kFewPass > 0x7FFFFFFFLL)
     return launch_query_plain(v, a, st);
-  if (!takes_few(v, rows, a.out_f32)) return launch_query_many(v, a, ws, st);
+  if (!takes_few(v, v.batch, rows, a.out_f32, (long long)v.max_pages * v.P)) return launch_query_many(v, a, ws, st);
   return v.kfmt == KVQ_INT8 ? launch_query_few_i8(v, a, ws, st)
          : v.kfmt == KVQ_FP8_E4M3 ? launch_query_few_e4(v, a, ws, st)
                                   : launch_query_few_e5(v, a, ws, st);

@@ -29,15 +29,16 @@ __device__ __forceinline__ int query_end(const QueryArgs& a, int T, int n, int i
 }
 
 constexpr int kFewPass = 32;    // rows of the few-row kernel's widest pass
-constexpr int kFewUnits = 8192;  // its units beyond one per (sequence, kv-head)
+constexpr int kFewPasses = 8;   // and passes of a launch
+constexpr int kFewUnits = 8192;  // its units beyond one per (sequence, kv-head, pass)
 constexpr int kManyGrid = 160;  // CTAs of the many-row kernel at most (one per SM)
 
 bool query_tc_shape(const KvqView& v);      // config only: the tensor-core kernels take it
 bool query_tc_eligible(const KvqView& v);   // and the cache's pool
 
-// The few-row kernel's workspace: int C, int units, pref[B + 1], u64 counter, then a record (M, l, 2 pad, o[D])
-// per (unit, row of a pass).
-__host__ __device__ inline size_t few_counter_offset(int B) { return ((size_t)(B + 3) * 4 + 7) & ~(size_t)7; }
+// The few-row kernel's workspace: its plan (4 ints), pref[B + 1], the counter, then records
+// (M, l, 2 pad, o[D]) for each row of a pass.
+__host__ __device__ inline size_t few_counter_offset(int B) { return (16 + ((size_t)B + 1) * 4 + 7) & ~(size_t)7; }
 __host__ __device__ inline size_t few_header_bytes(int B) { return (few_counter_offset(B) + 8 + 255) / 256 * 256; }
 size_t query_many_workspace_bytes(const KvqView& v, int batch, int n_q);
 kvq_status launch_query_few_i8(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st);

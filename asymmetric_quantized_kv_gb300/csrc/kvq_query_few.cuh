@@ -19,10 +19,10 @@
 // TMA copies of the pool seen as rows of 128 bytes with the 128-byte swizzle, so warps
 // never wait for one another.  Keys are the M operand of m16n8k16 (16 tokens x 8 rows),
 // values, transposed on the way from shared memory, that of the second product (16
-// channels x 8 rows); with more rows a converted operand serves up to four products.  p crosses from one layout to the other with movmatrix.  The window's
-// tokens (bf16) take the same path from registers, scaled by a power of two per tile.
-// Units are sized so that they fill the warps of the GPU a whole number of times (up to
-// 4); a second kernel merges a (sequence, kv-head)'s chunks.
+// channels x 8 rows); with more rows a converted operand serves up to four products.  p
+// crosses from one layout to the other with movmatrix.  The window's tokens (bf16) take the same path from registers, scaled by a power of two per tile.
+// All work lies in one row that is cut into equal runs, one a warp or up to four; a second
+// kernel merges a row's records.
 #pragma once
 
 #include <math.h>
@@ -54,56 +54,79 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   return r;
 }
 
-// ---- plan: per sequence ceil(T / C) chunks (over pages and window alike) for each kv-head;
-// unit = pref[b] + kvh * chunks + chunk.
-// One warp; pref: B + 1 ints of shared memory.  workers: warps of the grid.  Lanes over the sequences, whose
-// lengths are read once (a decode step's time is a chain of such latencies).
-__device__ inline void few_plan(const KvqView& v, int workers, int* pref, int* s_C, int* s_units) {
+// ---- plan: a sequence's work is its places (of 16 tokens, or 16 << sh where their number would pass 31 bits),
+// for each of `heads` pairs of a kv-head and a pass of its rows.  All pairs' places lie in one row, cut into runs
+// of the same length, a warp's work each; a pair that is cut leaves a record per run, which the merge joins.
+// Where a warp gets one run, pairs are padded to whole runs if runs up to a quarter longer allow that (no warp
+// then starts two units: 16 drafts of 5 tokens take 46 us, not 47.5); else a pair has kUnitCost places before its
+// own, for its unit's start, and runs cross pairs: the warps' work is then even (64 sequences of 1,024 to 65,536
+// tokens take 387 us, not 407; 128 of 466 tokens with 24 rows fill the warps once, not twice).
+struct FewPlan {
+  unsigned run;  // places of a run
+  int runs, aligned, pad;
+};
+constexpr unsigned kUnitCost = 3;
+
+__device__ __forceinline__ unsigned few_units(int T, int sh) { return ((unsigned)T + (kTile << sh) - 1) >> (4 + sh); }
+__device__ __forceinline__ unsigned few_places(const FewPlan& p, unsigned n) {
+  if (n == 0) return 0;
+  return p.aligned ? (n + p.run - 1) / p.run * p.run : n + kUnitCost;
+}
+
+// One warp; pref: B + 1 ints of shared memory, the places before a sequence.  workers: warps of the grid.  Lanes over
+// the sequences, whose lengths are read once (a decode step's time is a chain of such latencies).
+__device__ inline void few_plan(const KvqView& v, int heads, int sh, int workers, unsigned* pref, FewPlan* plan) {
   const int B = v.batch, lane = threadIdx.x & 31;
-  unsigned long long sum = 0;
+  unsigned sum = 0, some = 0;
   for (int b = lane; b < B; b += 32) {
-    const int T = seq_tokens(v, b);
-    pref[b] = T;
-    sum += (unsigned)T;
+    const unsigned n = few_units(seq_tokens(v, b), sh);
+    pref[b] = n;
+    sum += n;
+    some += n > 0;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const unsigned long long work = sum * v.Hkv;
-  const unsigned each = (unsigned)min(work / (unsigned)workers, 0xffffffffull);
-  const unsigned rounds = min(max(each / kUnitTokens, 1u), (unsigned)min(kRounds, max(1, kMaxUnits / workers)));
+  const unsigned work = __reduce_add_sync(0xffffffffu, sum) * heads;
+  const unsigned rounds = min(max(work / workers / (unsigned)max(1, kUnitTokens >> (4 + sh)), 1u),
+                              (unsigned)min(kRounds, max(1, kMaxUnits / workers)));
   const unsigned most = min(rounds * (unsigned)workers, (unsigned)kMaxUnits);
-  unsigned C = (unsigned)min((work + most - 1) / most, 1ull << 30);
-  C = max((unsigned)kMinUnit, (C + kTile - 1) / kTile * kTile);
-  // the cut ends of the sequences may push the units past a whole number of rounds, or past what the
-  // workspace holds: longer chunks (a chunk as long as the longest sequence always fits)
-  const unsigned cap = kMaxUnits / v.Hkv + B;
+  FewPlan p;
+  p.run = max((work + most - 1) / most, (unsigned)(kMinUnit / kTile));
+  p.aligned = rounds == 1;
+  const unsigned longest = p.run + p.run / 4;
+  unsigned runs = 0;
 #pragma unroll 1
-  for (int k = 0;; ++k) {
-    unsigned units = 0;
+  while (p.aligned) {
+    runs = 0;
 #pragma unroll 1
-    for (int b = lane; b < B; b += 32) units += ((unsigned)pref[b] + C - 1) / C;
-    units = __reduce_add_sync(0xffffffffu, units);
-    const bool fits = units <= cap;
-    if (fits && (k >= 6 || (unsigned long long)units * v.Hkv <= most)) break;
-    C = k < 6 ? (C + C / 16 + kTile - 1) / kTile * kTile : min(2 * C, 1u << 30);
+    for (int b = lane; b < B; b += 32) runs += (pref[b] + p.run - 1) / p.run;
+    runs = __reduce_add_sync(0xffffffffu, runs) * heads;
+    if (runs <= most) break;
+    p.run += p.run / 16 + 1;
+    p.aligned = p.run <= longest;
   }
-  int run = 0;
+  if (!p.aligned) {
+    const unsigned places = work + __reduce_add_sync(0xffffffffu, some) * heads * kUnitCost;
+    p.run = max((places + most - 1) / most, 1u);
+    runs = (places + p.run - 1) / p.run;
+  }
+  p.runs = (int)runs;
+  p.pad = 0;
+  unsigned before = 0;
 #pragma unroll 1
   for (int b0 = 0; b0 < B; b0 += 32) {
-    const int b = b0 + lane, x = b < B ? (int)(((unsigned)pref[b] + C - 1) / C) * v.Hkv : 0;
-    int incl = x;
+    const int b = b0 + lane;
+    const unsigned x = b < B ? few_places(p, pref[b]) * heads : 0;
+    unsigned incl = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      const unsigned y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    if (b < B) pref[b] = run + incl - x;
-    run += __shfl_sync(0xffffffffu, incl, 31);
+    if (b < B) pref[b] = before + incl - x;
+    before += __shfl_sync(0xffffffffu, incl, 31);
   }
   if (lane == 0) {
-    pref[B] = run;
-    *s_units = run;
-    *s_C = (int)C;
+    pref[B] = before;
+    *plan = p;
   }
 }
 
@@ -124,7 +147,8 @@ __device__ __forceinline__ uint32_t swz(uint32_t o) { return o ^ (((o >> 7) & 7u
 
 template <int F, int D, int NB, bool kF32>
 __global__ void __launch_bounds__(kFThreads)
-    query_few_kernel(KvqView v, QueryArgs a, int row0, float* ws, int dynamic, const __grid_constant__ CUtensorMap tmap) {
+    query_few_kernel(KvqView v, QueryArgs a, int row_base, int passes, int sh, float* ws, int dynamic,
+                     const __grid_constant__ CUtensorMap tmap) {
   constexpr int NS = D / 16;      // steps of the first product, and channel tiles of the second
   constexpr int LC = D / 4;       // channels a lane holds of a key row
   constexpr int GC = D / 8;       // channels a lane holds of a value row
@@ -132,19 +156,16 @@ __global__ void __launch_bounds__(kFThreads)
   extern __shared__ unsigned char dyn_raw[];
   unsigned char* dyn = dyn_raw + ((1024 - (smem_u32(dyn_raw) & 1023)) & 1023);
   FewSmem<D, NB>& sm = *reinterpret_cast<FewSmem<D, NB>*>(dyn);
-  int* pref = reinterpret_cast<int*>(dyn + sizeof(FewSmem<D, NB>));
-  __shared__ int s_C, s_units;
+  unsigned* pref = reinterpret_cast<unsigned*>(dyn + sizeof(FewSmem<D, NB>));
+  __shared__ FewPlan s_plan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int workers = gridDim.x * kFWarps;
-  if (warp == 0) few_plan(v, workers, pref, &s_C, &s_units);
+  const int workers = gridDim.x * kFWarps, heads = v.Hkv * passes;
+  if (warp == 0) few_plan(v, heads, sh, workers, pref, &s_plan);
   __syncthreads();
   if (blockIdx.x == 0) {
-    int* hd = reinterpret_cast<int*>(ws);
-    if (threadIdx.x == 0) {
-      hd[0] = s_C;
-      hd[1] = s_units;
-    }
-    for (int b = threadIdx.x; b <= v.batch; b += kFThreads) hd[2 + b] = pref[b];
+    if (threadIdx.x == 0) *reinterpret_cast<FewPlan*>(ws) = s_plan;
+    unsigned* hd = reinterpret_cast<unsigned*>(reinterpret_cast<char*>(ws) + sizeof(FewPlan));
+    for (int b = threadIdx.x; b <= v.batch; b += kFThreads) hd[b] = pref[b];
   }
   grid_dep_launch();
   if (lane == 0) {
@@ -152,27 +173,46 @@ __global__ void __launch_bounds__(kFThreads)
     fence_mbar_init();
   }
   __syncwarp();
-  const int C = s_C, n_units = s_units, rows_max = min(8 * NB, a.n_q * v.n_rep - row0);
-  unsigned long long* counter =
-      reinterpret_cast<unsigned long long*>(reinterpret_cast<char*>(ws) + few_counter_offset(v.batch));
+  const FewPlan plan = s_plan;
+  const int rows_max = min(8 * NB, a.n_q * v.n_rep - row_base);
+  unsigned* counter = reinterpret_cast<unsigned*>(reinterpret_cast<char*>(ws) + few_counter_offset(v.batch));
   float* part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + few_header_bytes(v.batch));
   int lstage = 0, cstage = 0;
   uint32_t cphase = 0, n_loaded = 0, n_consumed = 0;
   bool stalled = false;
 
-  int unit = blockIdx.x * kFWarps + warp;
-  while (unit < n_units) {
-    unsigned long long nxt = 0;
-    if (dynamic && lane == 0) nxt = atomicAdd(counter, 1ull);
-    int lo = 0, hi = v.batch - 1;  // largest b with pref[b] <= unit (sequences without units share a value)
+  int run = blockIdx.x * kFWarps + warp;
+  unsigned pos = 0, stop = 0, nxt = 0;
+  while (true) {
+    if (pos >= stop) {
+      if (stop) run = dynamic ? workers + (int)__shfl_sync(0xffffffffu, nxt, 0) : run + workers;
+      if (run >= plan.runs) break;
+      if (dynamic && lane == 0) nxt = atomicAdd(counter, 1u);  // the next run, known by the time this one ends
+      pos = run * plan.run;
+      stop = min(pos + plan.run, pref[v.batch]);
+    }
+    int lo = 0, hi = v.batch - 1;  // largest b with pref[b] <= pos (sequences without places share a value)
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (pref[mid] <= unit) lo = mid; else hi = mid - 1;
+      if (pref[mid] <= pos) lo = mid; else hi = mid - 1;
     }
-    const int b = lo, nc = (pref[b + 1] - pref[b]) / v.Hkv;
-    const int h = (unit - pref[b]) / nc, chunk = (unit - pref[b]) % nc;
-    const int T = seq_tokens(v, b), nq = n_quantized(T, v.R), n = query_count(v, a, b), rows = n * v.n_rep - row0;
-    const int t0 = chunk * C, t1 = min(T, t0 + C);
+    const int b = lo, T = seq_tokens(v, b);
+    const unsigned units = few_units(T, sh), skip = plan.aligned ? 0 : kUnitCost;
+    const unsigned places = (pref[b + 1] - pref[b]) / heads, off = pos - pref[b], hp = off / places, at = off - hp * places;
+    const unsigned here = min(places - at, stop - pos);
+    const unsigned j0 = max(at, skip) - skip, j1 = min(units, max(at + here, skip) - skip);  // its share of the pair
+    pos += here;
+    if (j0 >= j1) continue;
+    int h = hp, row0 = row_base;
+    if (passes > 1) {
+      h = (int)hp / passes;
+      row0 += ((int)hp - h * passes) * 8 * NB;
+    }
+    const int nq = n_quantized(T, v.R), n = query_count(v, a, b), rows = n * v.n_rep - row0;
+    // no token that the pass's last row does not see (the call's last row sees them all)
+    const int seen = rows <= 0 ? 0 : rows <= 8 * NB ? T : query_end(a, T, n, (row0 + 8 * NB - 1) / v.n_rep);
+    const int t0 = (int)(j0 << (4 + sh));
+    const int t1 = max(t0, (int)min(min((unsigned)T, few_units(seen, 0) * kTile), j1 << (4 + sh)));
     const int tq = min(t1, nq);                                // tiles before tq come from the pages
     const int qtiles = tq > t0 ? (tq - t0) / kTile : 0;        // nq and t0 are multiples of 16
     const int tiles = (t1 - t0 + kTile - 1) / kTile;
@@ -527,7 +567,7 @@ __global__ void __launch_bounds__(kFThreads)
         for (int o = 4; o < 32; o <<= 1) l_run[nb][r] += __shfl_xor_sync(0xffffffffu, l_run[nb][r], o);
         const int row = 8 * nb + 2 * t + r;
         if (row < rows) {
-          float* rec = part + ((long long)unit * rows_max + row) * (D + 4);
+          float* rec = part + ((long long)(run + b * heads + (int)hp) * rows_max + row) * (D + 4);
           if (g == 0) {
             rec[0] = m_run[nb][r];
             rec[1] = l_run[nb][r];
@@ -538,7 +578,6 @@ __global__ void __launch_bounds__(kFThreads)
         }
       }
     __syncwarp();
-    unit = dynamic ? workers + (int)__shfl_sync(0xffffffffu, (unsigned)nxt, 0) : unit + workers;
   }
   if (lane == 0) {  // copies issued and not consumed (a stalled ring): wait for them, bounded, before leaving
     while (n_consumed < n_loaded) {
@@ -552,33 +591,49 @@ __global__ void __launch_bounds__(kFThreads)
   }
 }
 
-// One CTA of 4 warps per (sequence, kv-head, row of the pass): the warps take every fourth record of the
-// row's chunks, lanes over channel pairs or quads, and merge through shared memory.
+// Few rows: a CTA of 4 warps each, the warps over every fourth record, lanes over channel pairs or quads, merged
+// through shared memory (32 rows of 65 records: a decode step of 4,101 tokens takes 13.6 us so, 18.4 with a warp a
+// row).  Many rows, with few records each: a warp a row (24,576 rows: 49 us with the products, 76 with a CTA a row).
 constexpr int kMWarps = 4;
+constexpr long long kSoloRows = 4096;
 template <int D, bool kF32>
-__global__ void __launch_bounds__(kMWarps * 32) few_merge_kernel(KvqView v, QueryArgs a, int row0, int rows_max, const float* ws) {
+__global__ void __launch_bounds__(kMWarps * 32) few_merge_kernel(KvqView v, QueryArgs a, int row_base, int passes, int sh, int rows_max,
+                                                                    int solo, const float* ws) {
   constexpr int PER = D / 32;  // channels per lane: 2, 4 or 8
   __shared__ float o_s[kMWarps][D];
   __shared__ float m_s[kMWarps], l_s[kMWarps];
-  const int r = blockIdx.x % rows_max, x = blockIdx.x / rows_max, h = x % v.Hkv, b = x / v.Hkv;
-  const int i = (row0 + r) / v.n_rep, hq = h * v.n_rep + (row0 + r) % v.n_rep;
+  const int heads = v.Hkv * passes;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned idx = solo ? blockIdx.x * kMWarps + warp : blockIdx.x;
+  const int r = idx % rows_max, x = idx / rows_max, hp = x % heads, b = x / heads;
+  int h = hp, row = row_base + r;
+  if (passes > 1) {
+    h = hp / passes;
+    row += (hp - h * passes) * rows_max;
+  }
+  const int i = row / v.n_rep, hq = h * v.n_rep + (row - i * v.n_rep);
+  if (b >= v.batch || i >= query_count(v, a, b)) return;
+  const unsigned units = few_units(seq_tokens(v, b), sh);
   grid_dep_wait();
-  if (i >= query_count(v, a, b)) return;
-  const int* pref = reinterpret_cast<const int*>(ws) + 2;
-  const int nc = (pref[b + 1] - pref[b]) / v.Hkv;
+  const FewPlan plan = *reinterpret_cast<const FewPlan*>(ws);
+  const unsigned* pref =
+      reinterpret_cast<const unsigned*>(reinterpret_cast<const char*>(ws) + sizeof(FewPlan));
+  const unsigned first = pref[b] + hp * few_places(plan, units) + (plan.aligned ? 0 : kUnitCost);
+  const int run0 = (int)(first / plan.run), nc = units ? (int)((first + units - 1) / plan.run) - run0 + 1 : 0;
   const long long stride = (long long)rows_max * (D + 4);
   const float* rec = reinterpret_cast<const float*>(reinterpret_cast<const char*>(ws) + few_header_bytes(v.batch)) +
-                     ((long long)(pref[b] + h * nc) * rows_max + r) * (D + 4);
+                     ((long long)(run0 + b * heads + hp) * rows_max + r) * (D + 4);
   float m = kMinit, l = 0.f, o[PER];
 #pragma unroll
   for (int c = 0; c < PER; ++c) o[c] = 0.f;
   constexpr int kBatch = 4;
-  for (int k0 = warp; k0 < nc; k0 += kMWarps * kBatch) {
+  const int stepk = solo ? 1 : kMWarps;
+#pragma unroll 1
+  for (int k0 = solo ? 0 : warp; k0 < nc; k0 += stepk * kBatch) {
     float rm[kBatch], rl[kBatch], y[kBatch][PER];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int k = k0 + j * kMWarps;
+      const int k = k0 + j * stepk;
       rm[j] = kMinit;
       rl[j] = 0.f;
 #pragma unroll
@@ -612,6 +667,22 @@ __global__ void __launch_bounds__(kMWarps * 32) few_merge_kernel(KvqView v, Quer
     }
     m = mn;
   }
+  const long long out0 = (((long long)b * a.n_q + i) * v.Hq + hq) * D;
+  if (solo) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int c = 0; c < PER; c += 2) {
+      const long long at = out0 + lane * PER + c;
+      if (kF32) {
+        static_cast<float*>(a.out)[at] = o[c] * inv;
+        static_cast<float*>(a.out)[at + 1] = o[c + 1] * inv;
+      } else {
+        *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+            __floats2bfloat162_rn(o[c] * inv, o[c + 1] * inv);
+      }
+    }
+    return;
+  }
   if (lane == 0) {
     m_s[warp] = m;
     l_s[warp] = l;
@@ -625,7 +696,6 @@ __global__ void __launch_bounds__(kMWarps * 32) few_merge_kernel(KvqView v, Quer
 #pragma unroll
   for (int w = 0; w < kMWarps; ++w) L = fmaf(l_s[w], exp2f(m_s[w] - M), L);
   const float inv = L > 0.f ? 1.f / L : 0.f;
-  const long long out0 = (((long long)b * a.n_q + i) * v.Hq + hq) * D;
   for (int c = threadIdx.x; c < D; c += kMWarps * 32) {
     float s = 0.f;
 #pragma unroll
@@ -640,7 +710,8 @@ __global__ void __launch_bounds__(kMWarps * 32) few_merge_kernel(KvqView v, Quer
 }
 
 template <int F, int D, int NB, bool kF32>
-kvq_status launch_few_t(const KvqView& v, const QueryArgs& a, int row0, float* ws, const CUtensorMap& tmap, cudaStream_t st) {
+kvq_status launch_few_t(const KvqView& v, const QueryArgs& a, int row0, int passes, float* ws, const CUtensorMap& tmap,
+                        cudaStream_t st) {
   constexpr int kMaxBatch = 4096;  // the plan's prefix in shared memory (query_tc_shape)
   constexpr int kNB = NB - 1, kDi = D == 64 ? 0 : D == 128 ? 1 : 2;
   const auto kern = query_few_kernel<F, D, NB, kF32>;
@@ -654,16 +725,21 @@ kvq_status launch_few_t(const KvqView& v, const QueryArgs& a, int row0, float* w
   if (grid > kMaxUnits / kFWarps) grid = kMaxUnits / kFWarps;
   // warps take their next unit from a counter where one may come (workers run at unequal speed);
   // a call too small for that saves the counter's clearing
-  const long long most = (long long)v.batch * v.max_pages * v.P * v.Hkv;
+  const long long pairs = (long long)v.batch * v.Hkv * passes;
+  int sh = 0;
+  while (pairs * (((long long)v.max_pages * v.P >> (4 + sh)) + kUnitCost + 1) > (1LL << 30)) ++sh;
+  const long long most = pairs * v.max_pages * v.P;
   const int dynamic = most > (long long)grid * kFWarps * kUnitTokens;
   if (dynamic && cudaMemsetAsync(reinterpret_cast<char*>(ws) + few_counter_offset(v.batch), 0, 8, st) != cudaSuccess)
     return KVQ_ERR_CUDA;
-  kern<<<grid, kFThreads, smem, st>>>(v, a, row0, ws, dynamic, tmap);
+  kern<<<grid, kFThreads, smem, st>>>(v, a, row0, passes, sh, ws, dynamic, tmap);
   if (cudaGetLastError() != cudaSuccess) return KVQ_ERR_CUDA;
   const long long rows = (long long)a.n_q * v.n_rep - row0;
   const int rows_max = (int)(rows < 8 * NB ? rows : 8 * NB);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)v.batch * v.Hkv * rows_max));
+  const long long merged = pairs * rows_max;
+  const int solo = merged >= kSoloRows;
+  cfg.gridDim = dim3((unsigned)(solo ? (merged + kMWarps - 1) / kMWarps : merged));
   cfg.blockDim = dim3(kMWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -671,33 +747,24 @@ kvq_status launch_few_t(const KvqView& v, const QueryArgs& a, int row0, float* w
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_merge_kernel<D, kF32>, v, a, row0, rows_max, (const float*)ws) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, few_merge_kernel<D, kF32>, v, a, row0, passes, sh, rows_max, solo, (const float*)ws) == cudaSuccess
              ? KVQ_OK
              : KVQ_ERR_CUDA;
 }
 
-// Rows in passes of 32 (16 at head_dim 256, or with fp32 output, whose second product doubles): a pass reads the
-// whole cache, so the last ones take the smallest block that holds what is left.
+// Rows in passes of 32 (16 at head_dim 256, or with fp32 output, whose second product doubles), up to kFewPasses of
+// them in a launch, side by side, as blocks of the smallest size that holds them all.
 template <int F, int D, bool kF32>
 kvq_status launch_few_rows(const KvqView& v, const QueryArgs& a, float* ws, const CUtensorMap& tmap, cudaStream_t st) {
-  constexpr bool kFour = D <= 128 && !kF32;
+  constexpr int kBlocks = D <= 128 && !kF32 ? 4 : 2;
   const long long rows = (long long)a.n_q * v.n_rep;
-  for (long long r = 0; r < rows;) {
-    const long long left = rows - r;
-    kvq_status s;
-    if (left <= 8) {
-      s = launch_few_t<F, D, 1, kF32>(v, a, (int)r, ws, tmap, st);
-      r += 8;
-    } else if (!kFour || left <= 16) {
-      s = launch_few_t<F, D, 2, kF32>(v, a, (int)r, ws, tmap, st);
-      r += 16;
-    } else if (left <= 24) {
-      s = launch_few_t<F, D, kFour ? 3 : 2, kF32>(v, a, (int)r, ws, tmap, st);
-      r += 24;
-    } else {
-      s = launch_few_t<F, D, kFour ? 4 : 2, kF32>(v, a, (int)r, ws, tmap, st);
-      r += 32;
-    }
+  for (long long r = 0; r < rows; r += 8 * kBlocks * kFewPasses) {
+    const int now = (int)(rows - r < 8 * kBlocks * kFewPasses ? rows - r : 8 * kBlocks * kFewPasses);
+    const int passes = (now + 8 * kBlocks - 1) / (8 * kBlocks), nb = (now + 8 * passes - 1) / (8 * passes);
+    const kvq_status s = nb == 1   ? launch_few_t<F, D, 1, kF32>(v, a, (int)r, passes, ws, tmap, st)
+                         : nb == 2 ? launch_few_t<F, D, 2, kF32>(v, a, (int)r, passes, ws, tmap, st)
+                         : nb == 3 ? launch_few_t<F, D, kBlocks == 4 ? 3 : 2, kF32>(v, a, (int)r, passes, ws, tmap, st)
+                                   : launch_few_t<F, D, kBlocks, kF32>(v, a, (int)r, passes, ws, tmap, st);
     if (s != KVQ_OK) return s;
   }
   return KVQ_OK;

@@ -599,3 +599,73 @@ def test_logits_far_apart():
             q[..., 0] = 24.0
             check_queries(c, n, True, q=q)
             check_queries(c, n, False, q=q)
+
+
+# ------------------------------------------------- wide block tables: more rows than 32 then take the other kernel
+
+def widened(c, tokens):
+    """A view of Case c whose block table could hold `tokens` a sequence (no page behind those in use)."""
+    import asymmetric_quantized_kv_gb300 as K
+    w = object.__new__(Case)
+    w.__dict__.update(c.__dict__)
+    table = torch.full((len(c.lens), -(-tokens // c.cfg.page_size)), -1, dtype=torch.int32, device="cuda")
+    table[:, :c.cache.block_table.shape[1]] = c.cache.block_table
+    w.cache = K.PagedKVCache.over(c.c_cfg, c.cache.pages, table, c.cache.seq_lens, c.cache.k_win, c.cache.v_win)
+    return w
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n", [9, 33, 64, 150])
+def test_query_attention_wide_table(case, n, causal):
+    check_queries(widened(case, 1 << 21), n, causal)
+
+
+@pytest.mark.parametrize("name", SOILED)
+def test_what_lies_behind_a_sequence_is_not_read_wide_table(name):
+    cfg, lens = CASES[name]
+    c = Case(cfg, lens, seed=22)
+    c.name = name
+    q = torch_src(O.bf16(np.random.default_rng(3).standard_normal((len(lens), 70, cfg.num_q_heads, cfg.head_dim))), cfg)
+    clean = [widened(c, 1 << 21).cache.query_attention(q, causal=k) for k in (True, False)]
+    _, defined = c.oracle_pages()
+    soiled = c.cache.page_view().cpu().numpy().copy()
+    soiled[~defined] = 0xFF
+    c.cache.page_view().copy_(torch.from_numpy(soiled))
+    for b, T in enumerate(lens):
+        c.cache.k_win[b, T % cfg.residual:] = float("nan")
+        c.cache.v_win[b, T % cfg.residual:] = float("inf")
+    again = [widened(c, 1 << 21).cache.query_attention(q, causal=k) for k in (True, False)]
+    assert all(torch.equal(a, b) for a, b in zip(clean, again))
+
+
+@pytest.mark.parametrize("n", [1, 5])
+def test_table_whose_work_passes_31_bits(n):
+    """Tokens that the table could hold x heads / 16 beyond 2^30: the split counts in larger places."""
+    cfg, lens = CASES["e4m3_p64"]
+    c = Case(cfg, lens, seed=2)
+    c.name = "e4m3_p64"
+    w = widened(c, 400_000_000)
+    check_queries(w, n, True)
+    check_queries(w, n, False)
+
+
+@pytest.mark.parametrize("Bn,T,n", [(40, 466, 12), (64, 100, 3), (9, 700, 16), (150, 33, 5), (33, 1200, 8)])
+def test_runs_that_cross_sequences(Bn, T, n):
+    """Batches whose pairs do not divide evenly among the warps, with sequences of no and of one token between."""
+    cfg = cfg_of(16, 8, 64, E4, E4, 64, 64, 64)
+    lens = [T - (b % 5) for b in range(Bn)]
+    lens[1], lens[Bn // 2] = 0, 1
+    c = Case(cfg, lens, seed=8)
+    c.name = "runs"
+    check_queries(c, n, True, [(7 * b) % (n + 1) for b in range(Bn)])
+    check_queries(c, n, False)
+
+
+def test_passes_of_one_launch():
+    """Rows of several passes in one launch and of several launches: head_dim 256 takes 16 a pass, 128 a launch."""
+    cfg, lens = CASES["d256"]
+    c = Case(cfg, lens, seed=5)
+    c.name = "d256"
+    for n in (4, 7, 32, 33, 75):
+        check_queries(c, n, True)
+        check_queries(c, n, False, [n - (b * n) // 3 for b in range(len(lens))])
