@@ -591,14 +591,16 @@ __global__ void __launch_bounds__(kFThreads)
   }
 }
 
-// Few rows: a CTA of 4 warps each, the warps over every fourth record, lanes over channel pairs or quads, merged
-// through shared memory (32 rows of 65 records: a decode step of 4,101 tokens takes 13.6 us so, 18.4 with a warp a
-// row).  Many rows, with few records each: a warp a row (24,576 rows: 49 us with the products, 76 with a CTA a row).
-constexpr int kMWarps = 4;
+// Rows that are merged.  Up to one an SM: a CTA of 16 warps each, the warps over every sixteenth record, lanes over
+// channel pairs or quads, merged through shared memory (32 rows of 65 records: a decode step of 4,101 tokens takes
+// 11.3 us so, 12.5 with 4 warps, 18.4 with a warp a row).  More: 4 warps a row (2,560 rows of 9 records: 45 us with
+// the products, 74 with 16 warps, 51 with a warp a row).  Many, with few records each: a warp a row (24,576 rows:
+// 49 us with the products, 76 with 4 warps a row).
 constexpr long long kSoloRows = 4096;
-template <int D, bool kF32>
-__global__ void __launch_bounds__(kMWarps * 32) few_merge_kernel(KvqView v, QueryArgs a, int row_base, int passes, int sh, int rows_max,
-                                                                    int solo, const float* ws) {
+constexpr int kSoloWarps = 4;
+template <int D, bool kF32, int kMWarps>
+__global__ void __launch_bounds__(kMWarps * 32)
+    few_merge_kernel(KvqView v, QueryArgs a, int row_base, int passes, int sh, int rows_max, int solo, const float* ws) {
   constexpr int PER = D / 32;  // channels per lane: 2, 4 or 8
   __shared__ float o_s[kMWarps][D];
   __shared__ float m_s[kMWarps], l_s[kMWarps];
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(kMWarps * 32) few_merge_kernel(KvqView v, Quer
   float m = kMinit, l = 0.f, o[PER];
 #pragma unroll
   for (int c = 0; c < PER; ++c) o[c] = 0.f;
-  constexpr int kBatch = 4;
+  constexpr int kBatch = kMWarps > 4 ? 8 : 4;
   const int stepk = solo ? 1 : kMWarps;
 #pragma unroll 1
   for (int k0 = solo ? 0 : warp; k0 < nc; k0 += stepk * kBatch) {
@@ -736,18 +738,19 @@ kvq_status launch_few_t(const KvqView& v, const QueryArgs& a, int row0, int pass
   if (cudaGetLastError() != cudaSuccess) return KVQ_ERR_CUDA;
   const long long rows = (long long)a.n_q * v.n_rep - row0;
   const int rows_max = (int)(rows < 8 * NB ? rows : 8 * NB);
-  cudaLaunchConfig_t cfg = {};
   const long long merged = pairs * rows_max;
-  const int solo = merged >= kSoloRows;
-  cfg.gridDim = dim3((unsigned)(solo ? (merged + kMWarps - 1) / kMWarps : merged));
-  cfg.blockDim = dim3(kMWarps * 32);
+  const int solo = merged >= kSoloRows, wide = merged <= num_sms();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(solo ? (merged + kSoloWarps - 1) / kSoloWarps : merged));
+  cfg.blockDim = dim3((wide ? 16 : kSoloWarps) * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_merge_kernel<D, kF32>, v, a, row0, passes, sh, rows_max, solo, (const float*)ws) == cudaSuccess
+  const auto merge = wide ? few_merge_kernel<D, kF32, 16> : few_merge_kernel<D, kF32, kSoloWarps>;
+  return cudaLaunchKernelEx(&cfg, merge, v, a, row0, passes, sh, rows_max, solo, (const float*)ws) == cudaSuccess
              ? KVQ_OK
              : KVQ_ERR_CUDA;
 }
