@@ -165,26 +165,41 @@ bool query_tc_eligible(const KvqView& v) {
   return query_tc_shape(v) && (long long)v.n_pages * v.page_bytes / 128 < (1LL << 31) && tensor_map_encoder() != nullptr;
 }
 
+// A call is small if passes of 8 rows over the tokens that its block table could hold are 2.5 units of 64 tokens, or
+// fewer, for each of the warps that such passes fill the GPU with.  The kernel of 8 rows is the shortest, and what a
+// short call waits for is its instructions (passes of 8 against one of 24 or 32 rows, us, 8 kv-heads of 128: 20 rows
+// over 512 tokens 10.6 and 14.9, over 4 x 2,000 18.6 and 22.3, 32 rows over 4,101 18.5 and 25.8; beyond the bound 20 rows
+// over 16 x 1,000 29.1 and 27.0, 32 over 40,000 57 and 52).
+bool few_small(const KvqView& v, int batch, long long rows, long long tokens) {
+  if (rows > kFewSmallRows) return false;
+  const double units = (double)batch * v.Hkv * (double)((rows + 7) / 8) * (double)tokens / 64.0;
+  return units <= 2.5 * 12 * num_sms();
+}
+
 // Which of the two: the few-row kernel reads the cache once per 32 rows (16 at head_dim 256 or with fp32 output) at
 // close to the memory's rate; the many-row kernel reads it once per 256 and multiplies at the tensor cores' rate, but
-// a unit of its work starts and ends slowly.  So the former takes up to 32 rows, and more where the call is small
-// by the tokens that its block table could hold (few-row against many-row kernel, us): 40 rows over 8 heads x 2,992
-// tokens 15 and 29, 64 rows over 512 x 224 40 and 50, 160 rows over 16 x 458 17 and 19; beyond the bounds 36 rows over
-// 128 x 4,096 97 and 84, 64 rows over 56 x 5,666 75 and 58, 264 rows over 216 x 128 55 and 32.  head_dim 256 and
-// fp32 output exceed the many-row kernel's shared and tensor memory.
+// a unit of its work starts and ends slowly.  So the former takes up to 32 rows, small calls, and up to 64 or 256
+// rows over few tokens (few-row against many-row kernel, us: 40 rows over 8 heads x 2,992 tokens 15 and 29, 64 rows
+// over 512 x 224 40 and 50, 112 rows over 5 x 4,502 22 and 36; beyond the bounds 36 rows over 128 x 4,096 97 and 84,
+// 64 rows over 56 x 5,666 75 and 58, 264 rows over 216 x 128 55 and 32).  head_dim 256 and fp32 output exceed the
+// many-row kernel's shared and tensor memory.
 static bool takes_few(const KvqView& v, int batch, long long rows, int out_f32, long long tokens) {
-  if (rows <= kFewPass || v.D > 128 || out_f32) return true;
-  const long long pairs = (long long)batch * v.Hkv, units = pairs * ((rows + kFewPass - 1) / kFewPass);
-  const double products = (double)rows * (double)pairs * (double)tokens * v.D;
-  return rows <= 2 * kFewPass ? units <= 4096 && products <= 2147483648.0
-                              : rows <= kFewPasses * kFewPass && units <= 1024 && products <= 536870912.0;
+  if (rows <= kFewPass || v.D > 128 || out_f32 || few_small(v, batch, rows, tokens)) return true;
+  const double pairs = (double)batch * v.Hkv, passes = (double)((rows + kFewPass - 1) / kFewPass);
+  const double products = (double)rows * pairs * (double)tokens * v.D;
+  return passes <= 2 ? pairs <= 2048.0 && products <= 2147483648.0
+                     : passes <= kFewPasses && pairs * passes <= 1024.0 && products <= 536870912.0;
 }
 
 static size_t few_bytes(const KvqView& v, int batch, long long rows, int out_f32) {
-  const long long pass = v.D > 128 || out_f32 ? 16 : kFewPass;
-  const size_t passes = (size_t)(rows < pass * kFewPasses ? (rows + pass - 1) / pass : kFewPasses);
-  const size_t units = (size_t)kFewUnits + (size_t)batch * v.Hkv * passes, r = (size_t)(rows < pass ? rows : pass);
-  return few_header_bytes(batch) + units * r * (v.D + 4) * sizeof(float);
+  const long long pass = v.D > 128 || out_f32 ? 16 : kFewPass, pairs = (long long)batch * v.Hkv;
+  const long long passes = rows < pass * kFewPasses ? (rows + pass - 1) / pass : kFewPasses;
+  long long records = (kFewUnits + pairs * passes) * (rows < pass ? rows : pass);
+  if (few_small(v, batch, rows, v.P)) {  // as it may be, with the narrowest table
+    const long long by8 = (kFewUnits + pairs * ((rows + 7) / 8)) * (rows < 8 ? rows : 8);
+    if (by8 > records) records = by8;
+  }
+  return few_header_bytes(batch) + (size_t)records * (v.D + 4) * sizeof(float);
 }
 
 size_t query_workspace_bytes(const KvqView& v, int batch, int n_q) {
@@ -192,7 +207,7 @@ size_t query_workspace_bytes(const KvqView& v, int batch, int n_q) {
   b.batch = batch;
   if (!query_tc_shape(b)) return 256;
   const long long rows = (long long)n_q * v.n_rep;
-  const size_t few = takes_few(v, batch, rows, 0, 0) ? few_bytes(v, batch, rows, 0) : 0;
+  const size_t few = takes_few(v, batch, rows, 0, v.P) ? few_bytes(v, batch, rows, 0) : 0;
   if (takes_few(v, batch, rows, 0, 1LL << 62)) return few;
   const size_t many = query_many_workspace_bytes(v, batch, n_q);
   return few > many ? few : many;

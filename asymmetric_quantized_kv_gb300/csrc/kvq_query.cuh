@@ -30,9 +30,11 @@ __device__ __forceinline__ int query_end(const QueryArgs& a, int T, int n, int i
 
 constexpr int kFewPass = 32;    // rows of the few-row kernel's widest pass
 constexpr int kFewPasses = 8;   // and passes of a launch
+constexpr int kFewSmallRows = 256;  // rows of a small call at most, in passes of 8
 constexpr int kFewUnits = 8192;  // its units beyond one per (sequence, kv-head, pass)
 constexpr int kManyGrid = 160;  // CTAs of the many-row kernel at most (one per SM)
 
+bool few_small(const KvqView& v, int batch, long long rows, long long tokens);  // whether passes of 8 rows take it
 bool query_tc_shape(const KvqView& v);      // config only: the tensor-core kernels take it
 bool query_tc_eligible(const KvqView& v);   // and the cache's pool
 

@@ -756,11 +756,13 @@ kvq_status launch_few_t(const KvqView& v, const QueryArgs& a, int row0, int pass
 }
 
 // Rows in passes of 32 (16 at head_dim 256, or with fp32 output, whose second product doubles), up to kFewPasses of
-// them in a launch, side by side, as blocks of the smallest size that holds them all.
+// them in a launch, side by side, as blocks of the smallest size that holds them all; in a small call in passes of 8.
 template <int F, int D, bool kF32>
 kvq_status launch_few_rows(const KvqView& v, const QueryArgs& a, float* ws, const CUtensorMap& tmap, cudaStream_t st) {
   constexpr int kBlocks = D <= 128 && !kF32 ? 4 : 2;
   const long long rows = (long long)a.n_q * v.n_rep;
+  if (few_small(v, v.batch, rows, (long long)v.max_pages * v.P))
+    return launch_few_t<F, D, 1, kF32>(v, a, 0, (int)(rows + 7) / 8, ws, tmap, st);
   for (long long r = 0; r < rows; r += 8 * kBlocks * kFewPasses) {
     const int now = (int)(rows - r < 8 * kBlocks * kFewPasses ? rows - r : 8 * kBlocks * kFewPasses);
     const int passes = (now + 8 * kBlocks - 1) / (8 * kBlocks), nb = (now + 8 * passes - 1) / (8 * passes);
