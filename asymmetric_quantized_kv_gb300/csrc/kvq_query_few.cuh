@@ -78,6 +78,7 @@ __device__ __forceinline__ unsigned few_places(const FewPlan& p, unsigned n) {
 __device__ inline void few_plan(const KvqView& v, int heads, int sh, int workers, unsigned* pref, FewPlan* plan) {
   const int B = v.batch, lane = threadIdx.x & 31;
   unsigned sum = 0, some = 0;
+#pragma unroll 1
   for (int b = lane; b < B; b += 32) {
     const unsigned n = few_units(seq_tokens(v, b), sh);
     pref[b] = n;
@@ -130,6 +131,14 @@ __device__ inline void few_plan(const KvqView& v, int heads, int sh, int workers
   }
 }
 
+// Whether the ring's phase ended within kWaitPolls tries, each of which suspends for some time.
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitPolls; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+
 // Rows of a pass: 8 NB.  The query operand stays in registers up to 32 of them, else in shared memory.
 template <int D, int NB>
 constexpr bool query_in_smem() { return NB * (D / 16) > 16; }
@@ -165,6 +174,7 @@ __global__ void __launch_bounds__(kFThreads)
   if (blockIdx.x == 0) {
     if (threadIdx.x == 0) *reinterpret_cast<FewPlan*>(ws) = s_plan;
     unsigned* hd = reinterpret_cast<unsigned*>(reinterpret_cast<char*>(ws) + sizeof(FewPlan));
+#pragma unroll 1
     for (int b = threadIdx.x; b <= v.batch; b += kFThreads) hd[b] = pref[b];
   }
   grid_dep_launch();
@@ -256,10 +266,9 @@ __global__ void __launch_bounds__(kFThreads)
     // ---- block scales: lane j holds those of block blk0 + j of the unit
     float ks_l = 0.f, vs_l = 0.f;
     bool sok_l = true;
-    const int blk_first = t0 / v.kgroup;
-    int blk0 = blk_first;
+    int blk0 = t0 / v.kgroup, blk = 0, left = (v.kgroup - (t0 - blk0 * v.kgroup)) / kTile;  // tiles left of block blk0 + blk
     auto load_scales = [&]() {
-      const int blk = blk0 + lane, g0 = blk * v.kgroup;
+      const int g0 = (blk0 + lane) * v.kgroup;
       ks_l = vs_l = 0.f;
       sok_l = true;
       if (g0 < tq) {
@@ -403,7 +412,7 @@ __global__ void __launch_bounds__(kFThreads)
       const int tok = t0 + i * kTile, stage = cstage;
       bool valid = false;
       if (!stalled) {
-        if (!mbar_wait_bounded(&sm.bar[warp][stage], cphase, kWaitPolls)) {
+        if (!ring_wait(&sm.bar[warp][stage], cphase)) {
           atomicOr(v.status, KVQ_DEV_TIMEOUT);
           stalled = true;
         } else {
@@ -415,13 +424,16 @@ __global__ void __launch_bounds__(kFThreads)
         cphase ^= 1u;
       }
       ++n_consumed;
-      const int blk = tok / v.kgroup;
-      if (blk - blk0 >= 32) {
-        blk0 = blk;
-        load_scales();
+      const float kf = __shfl_sync(0xffffffffu, ks_l, blk), vf = __shfl_sync(0xffffffffu, vs_l, blk);
+      valid = valid && __shfl_sync(0xffffffffu, (int)sok_l, blk);
+      if (--left == 0) {
+        left = v.kgroup / kTile;
+        if (++blk == 32) {
+          blk0 += 32;
+          blk = 0;
+          load_scales();
+        }
       }
-      const float kf = __shfl_sync(0xffffffffu, ks_l, blk - blk0), vf = __shfl_sync(0xffffffffu, vs_l, blk - blk0);
-      valid = valid && __shfl_sync(0xffffffffu, (int)sok_l, blk - blk0);
       if (__all_sync(0xffffffffu, valid)) {  // a tile without its page, or its scales, takes no weight
         const uint8_t* kt = sm.kv[warp][stage][0];
         const uint8_t* vt = sm.kv[warp][stage][1];
@@ -581,7 +593,7 @@ __global__ void __launch_bounds__(kFThreads)
   }
   if (lane == 0) {  // copies issued and not consumed (a stalled ring): wait for them, bounded, before leaving
     while (n_consumed < n_loaded) {
-      mbar_wait_bounded(&sm.bar[warp][cstage], cphase, kWaitPolls);
+      ring_wait(&sm.bar[warp][cstage], cphase);
       if (++cstage == kFStages) {
         cstage = 0;
         cphase ^= 1u;
