@@ -164,7 +164,7 @@ def kvq_rope_append(cfg, cache: kvq_cache, rope: kvq_rope, q, k_new, v_new, n_ne
                     q_stride=0, k_stride=0, v_stride=0, stream=None):
     """kvq_quantize_append with q and the keys rotated to their positions; strides in elements between rows."""
     _check("kvq_rope_append",
-           LIB.kvq_rope_append(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(rope), _ptr(q), _ptr(k_new),
+           LIB.kvq_rope_append(cfg, cache, rope, _ptr(q), _ptr(k_new),  # a structure goes by reference
                                _ptr(v_new), int(q_stride), int(k_stride), int(v_stride), int(n_new),
                                _ptr(n_new_per_seq), _ptr(q_out), _stream(stream)))
 
@@ -176,7 +176,7 @@ def kvq_query_workspace_bytes(cfg: kvq_config, batch: int, n_q: int) -> int:
 def kvq_query_attention(cfg, cache: kvq_cache, q, n_q, n_q_per_seq, mask, out, softmax_scale, workspace, stream=None):
     nbytes = workspace.numel() * workspace.element_size()
     _check("kvq_query_attention",
-           LIB.kvq_query_attention(ctypes.byref(cfg), ctypes.byref(cache), _ptr(q), int(n_q), _ptr(n_q_per_seq),
+           LIB.kvq_query_attention(cfg, cache, _ptr(q), int(n_q), _ptr(n_q_per_seq),
                                    int(mask), _ptr(out), float(softmax_scale), _ptr(workspace), nbytes,
                                    _stream(stream)))
 

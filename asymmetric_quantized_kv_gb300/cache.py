@@ -95,7 +95,8 @@ class PagedKVCache:
             max(B.kvq_workspace_bytes(cfg, batch, max_pages_per_seq * cfg.page_size), 256),
             dtype=torch.uint8, device=dev)
         self._outgrown, self._query_bytes = [], {}
-        self._device, self._src = pages.device, src_torch_dtype(cfg)
+        self._device, self._index, self._src = pages.device, pages.get_device(), src_torch_dtype(cfg)
+        self._Hq, self._H, self._D = cfg.num_q_heads, H, cfg.head_dim
         self.rope_table, self.rope_positions = None, 0
         if cfg.rope_pre and rope_table is not False:
             if rope_table is True:
@@ -123,17 +124,17 @@ class PagedKVCache:
 
     def _beside(self, name, t):
         """The library launches on the current device, over the cache's memory."""
-        if t.device != self._device or torch._C._cuda_getDevice() != self._device.index:
+        if t.get_device() != self._index or torch._C._cuda_getDevice() != self._index:
             raise ValueError(f"{name} must be on the cache's device ({self._device}), which must be the current one")
 
     def _counts(self, name, t):
         self._beside(name, t)
-        if tuple(t.shape) != (self.batch,) or t.dtype != torch.int32 or not t.is_contiguous():
+        if t.shape != (self.batch,) or t.dtype != torch.int32 or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous int32 of shape {(self.batch,)}")
 
     def _rows(self, name, t, n, heads):
         """Elements between consecutive tokens of t [batch, n, heads, D]: a token's row contiguous, tokens evenly spaced."""
-        D = self.cfg.head_dim
+        D = self._D
         if t.shape != (self.batch, n, heads, D) or t.dtype != self._src:
             raise ValueError(f"{name} must be {self._src} of shape {(self.batch, n, heads, D)}")
         sb, sn, sh, sd = t.stride()
@@ -147,20 +148,22 @@ class PagedKVCache:
         """append() with the position rotation on the way: k_new, v_new [batch, n_new, Hkv, D] and q
         [batch, n_new, Hq, D] (or None) may be slices of one fused projection (rows of one token contiguous,
         tokens evenly spaced).  Returns the rotated queries."""
-        n, cfg = k_new.shape[1], self.cfg
+        n = k_new.shape[1]
         if n_new_per_seq is not None:
             self._counts("n_new_per_seq", n_new_per_seq)
         qs = 0
         if q is not None:
-            qs = self._rows("q", q, n, cfg.num_q_heads)
+            qs = self._rows("q", q, n, self._Hq)
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
             elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
                 raise ValueError("q_out must be contiguous, of q's shape and dtype")
             else:
                 self._beside("q_out", q_out)
-        ks, vs = self._rows("k_new", k_new, n, cfg.num_kv_heads), self._rows("v_new", v_new, n, cfg.num_kv_heads)
-        B.kvq_rope_append(cfg, self.c, rope, q, k_new, v_new, n, n_new_per_seq, q_out, qs, ks, vs, stream)
+        ks, vs = self._rows("k_new", k_new, n, self._H), self._rows("v_new", v_new, n, self._H)
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(self._index)
+        B.kvq_rope_append(self.cfg, self.c, rope, q, k_new, v_new, n, n_new_per_seq, q_out, qs, ks, vs, stream)
         return q_out
 
     def query_attention(self, q, causal=True, n_q_per_seq=None, out=None, softmax_scale=0.0, stream=None):
@@ -168,7 +171,7 @@ class PagedKVCache:
         own cache (causal), or a decoder's tokens over an encoder's states (causal=False).  The workspace grows
         with n_q on first use and is kept; calls on several streams at once need a cache object each."""
         cfg, n = self.cfg, q.shape[1]
-        if q.shape != (self.batch, n, cfg.num_q_heads, cfg.head_dim) or q.dtype != self._src or not q.is_contiguous():
+        if q.shape != (self.batch, n, self._Hq, self._D) or q.dtype != self._src or not q.is_contiguous():
             raise ValueError(f"q must be contiguous {self._src} of shape {(self.batch, n, cfg.num_q_heads, cfg.head_dim)}")
         self._beside("q", q)
         if out is None:
@@ -185,6 +188,8 @@ class PagedKVCache:
         if self.workspace.numel() < need:
             self._outgrown.append(self.workspace)  # a captured graph may still use it
             self.workspace = torch.empty(need, dtype=torch.uint8, device=self.pages.device)
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(self._index)
         B.kvq_query_attention(cfg, self.c, q, n, n_q_per_seq, B.KVQ_MASK_CAUSAL if causal else B.KVQ_MASK_NONE, out,
                               softmax_scale, self.workspace, stream)
         return out
