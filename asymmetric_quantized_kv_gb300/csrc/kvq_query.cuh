@@ -31,7 +31,9 @@ __device__ __forceinline__ int query_end(const QueryArgs& a, int T, int n, int i
 constexpr int kFewPass = 32;    // rows of the few-row kernel's widest pass
 constexpr int kFewPasses = 8;   // and passes of a launch
 constexpr int kFewSmallRows = 256;  // rows of a small call at most, in passes of 8
-constexpr int kFewUnits = 8192;  // its units beyond one per (sequence, kv-head, pass)
+// Its runs: four for each of the 1,824 warps that head_dim 128 fills a GPU with (records of 8 rows of that many
+// fit the fixed scratch array of kvq_decode_attention_noalloc).
+constexpr int kFewUnits = 7424;
 constexpr int kManyGrid = 160;  // CTAs of the many-row kernel at most (one per SM)
 
 bool few_small(const KvqView& v, int batch, long long rows, long long tokens);  // whether passes of 8 rows take it

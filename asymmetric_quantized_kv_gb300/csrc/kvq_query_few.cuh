@@ -1,6 +1,7 @@
 // Attention of few rows (query token x query head) per kv-head over a PER_BLOCK cache:
-// decode steps and drafts, bf16 sources, head_dim 64, 128 or 256.  The kernel takes 8, 16,
-// 24 or 32 rows a pass (16 at head_dim 256); more rows take several passes.
+// decode steps, drafts and short calls, bf16 sources, head_dim 64, 128 or 256.  The kernel
+// takes 8, 16, 24 or 32 rows a pass (16 at head_dim 256); more rows take several passes, side
+// by side in one launch.
 //
 // Mathematics, for a 16-token tile (it lies in one block of the cache, so one key scale ks
 // and one value scale vs = 2^e f, f in [1, 2)): with code matrices C_k, C_v,
@@ -20,9 +21,16 @@
 // never wait for one another.  Keys are the M operand of m16n8k16 (16 tokens x 8 rows),
 // values, transposed on the way from shared memory, that of the second product (16
 // channels x 8 rows); with more rows a converted operand serves up to four products.  p
-// crosses from one layout to the other with movmatrix.  The window's tokens (bf16) take the same path from registers, scaled by a power of two per tile.
-// All work lies in one row that is cut into equal runs, one a warp or up to four; a second
-// kernel merges a row's records.
+// crosses from one layout to the other with movmatrix.  The window's tokens (bf16) take the
+// same path from registers, scaled by a power of two per tile.  All work lies in one row
+// that is cut into equal runs, one a warp or up to four; a second kernel merges a row's
+// records.
+//
+// Measured (8 kv-heads of 128): 8 x 131,072 tokens with 8 rows 354 us, 6.1 TB/s (89% of the
+// measured copy bandwidth); 64 sequences of 1,024 to 65,536 tokens with 4 rows 367 us, 5.8
+// TB/s; 16 drafts of 5 tokens, 20 rows, 45 us, 1.9 TB/s, bound by the warps' issue (two a
+// scheduler at 254 registers); 1 x 4,101 tokens 12.5 us, bound by latency: 2.5 us to start
+// and plan, 6 for a unit, mostly instructions that no cache holds yet, 2.5 for the merge.
 #pragma once
 
 #include <math.h>

@@ -669,3 +669,26 @@ def test_passes_of_one_launch():
     for n in (4, 7, 32, 33, 75):
         check_queries(c, n, True)
         check_queries(c, n, False, [n - (b * n) // 3 for b in range(len(lens))])
+
+
+def test_decode_without_a_workspace_eight_heads_a_group():
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(64, 8, 128, E4, E4, 64, 64, 64)
+    c = Case(cfg, [100, 700, 64, 5], seed=3)
+    q = torch_src(c.queries(), cfg)
+    out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    K.kvq_decode_attention_noalloc(c.c_cfg, c.cache.c, q, out, 0.0)
+    assert torch.equal(out, c.cache.attention(q))
+
+
+@pytest.mark.parametrize("cfg,rot,halves", [
+    (cfg_of(8, 2, 128, E4, E4, 64, 64, 64), 128, True), (cfg_of(6, 3, 64, I8, I8, 32, 128, 32), 32, False),
+    (cfg_of(4, 2, 256, E5, E5, 32, 64, 64), 256, True), (cfg_of(4, 2, 128, E4, E4, 32, 64, 32, src=O.F32), 128, True),
+    (cfg_of(12, 9, 128, E4, E4, 64, 64, 16), 64, True)])
+def test_rope_append_of_17_to_32_rows(cfg, rot, halves):
+    """Chunks that fill a window, more than one of its rows behind it, and chunks that do not."""
+    for fused in (True, False):
+        c = rotated_case(cfg, [220, 131, 64, 20, 0], rot, halves, [20, 32, 31, 17], seed=rot, fused=fused)
+        c.check_pages()
+        c.check_lengths_and_window()
+        c.check_dequantize()
