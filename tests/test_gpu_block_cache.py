@@ -684,7 +684,7 @@ def test_decode_without_a_workspace_eight_heads_a_group():
 @pytest.mark.parametrize("cfg,rot,halves", [
     (cfg_of(8, 2, 128, E4, E4, 64, 64, 64), 128, True), (cfg_of(6, 3, 64, I8, I8, 32, 128, 32), 32, False),
     (cfg_of(4, 2, 256, E5, E5, 32, 64, 64), 256, True), (cfg_of(4, 2, 128, E4, E4, 32, 64, 32, src=O.F32), 128, True),
-    (cfg_of(12, 9, 128, E4, E4, 64, 64, 16), 64, True)])
+    (cfg_of(18, 9, 128, E4, E4, 64, 64, 16), 64, True)])
 def test_rope_append_of_17_to_32_rows(cfg, rot, halves):
     """Chunks that fill a window, more than one of its rows behind it, and chunks that do not."""
     for fused in (True, False):
