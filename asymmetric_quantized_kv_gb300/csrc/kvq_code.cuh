@@ -43,7 +43,23 @@ __device__ __forceinline__ uint32_t bf16x2_absmax(uint32_t m, uint32_t u) {  // 
   asm("max.u16x2 %0, %1, %2;\n" : "=r"(r) : "r"(m), "r"(a));
   return r;
 }
-__device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+// The same of finite magnitudes, as bits + 0x80: infinities and NaN wrap to the bottom (a token that a row does not see
+// then leaves the scaling of those it sees alone).
+__device__ __forceinline__ uint32_t bf16x2_finite_max(uint32_t m, uint32_t u) {
+  return bf16x2_absmax(m, (u & 0x7fff7fffu) + 0x00800080u);
+}
+__device__ __forceinline__ uint32_t finite_top(uint32_t m) {  // of the warp
+  return max(__reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16)), 0x80u) - 0x80u;
+}
+// Numbers that are not finite have all exponent bits set (E4M3: and all of the mantissa's): one more in the lowest of
+// these carries into the sign's place.
+struct FiniteTest {
+  uint32_t bits, one, sign;
+  __device__ __forceinline__ uint32_t carry(uint32_t w) const { return (w & bits) + one; }  // or'ed over words, then:
+  __device__ __forceinline__ bool fails(uint32_t carries) const { return (carries & sign) != 0u; }
+};
+constexpr FiniteTest kFiniteE4{0x7f7f7f7fu, 0x01010101u, 0x80808080u}, kFiniteE5{0x7c7c7c7cu, 0x04040404u, 0x80808080u};
+constexpr FiniteTest kFiniteBf16x2{0x7f807f80u, 0x00800080u, 0x80008000u}, kFiniteF16x2{0x7c007c00u, 0x04000400u, 0x80008000u};
 // Exponent k such that 2^-k brings values of largest magnitude `top` (bf16 bits) into [2^8, 2^9).
 __device__ __forceinline__ int norm_exponent(uint32_t top) {
   const int k = exponent_of(__uint_as_float(top << 16)) - 8;

@@ -151,6 +151,10 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity) {
 template <int D, int NB>
 constexpr bool query_in_smem() { return NB * (D / 16) > 16; }
 
+// CTAs an SM: with 128, 168 or 255 registers a thread.
+template <int D, int NB>
+constexpr int few_ctas() { return D == 64 && NB == 1 ? 4 : D * NB <= 128 ? 3 : 2; }
+
 template <int D, int NB>
 struct __align__(1024) FewSmem {
   uint8_t kv[kFWarps][kFStages][2][kTile * D];
@@ -162,8 +166,54 @@ struct __align__(1024) FewSmem {
 // Byte o of a 1024-byte aligned tile under the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swz(uint32_t o) { return o ^ (((o >> 7) & 7u) << 4); }
 
+// Rows of a 16-token value tile with a code that is not finite are zeroed, and the first such token noted.
+template <int D>
+__device__ __forceinline__ void drop_not_finite(uint8_t* vt, int lane, FiniteTest test, int tok, int& bad_from) {
+  const uint32_t at = (lane >> 1) * D + (lane & 1) * (D / 2);  // half a row a lane
+  uint32_t carries = 0u;
+#pragma unroll 1
+  for (int c = 0; c < D / 2; c += 16) {
+    const uint4 x = *reinterpret_cast<const uint4*>(vt + swz(at + c));
+    carries |= test.carry(x.x) | test.carry(x.y) | test.carry(x.z) | test.carry(x.w);
+  }
+  const uint32_t bad = __ballot_sync(0xffffffffu, test.fails(carries));
+  if (bad) {
+    bad_from = min(bad_from, tok + (__ffs(bad) - 1) / 2);
+    if ((bad >> (lane & ~1)) & 3u) {
+#pragma unroll 1
+      for (int c = 0; c < D / 2; c += 16) *reinterpret_cast<uint4*>(vt + swz(at + c)) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async();  // the slot's next copy comes after these
+    __syncwarp();
+  }
+}
+
+// The same for the second product's words of four window rows (tokens 2t, 2t + 1, 2t + 8, 2t + 9 of the tile).
+template <int W>
+__device__ __forceinline__ void drop_not_finite(uint32_t (&wv)[4][W], int tok, int& bad_from) {
+  constexpr FiniteTest test = kFiniteBf16x2;
+  const int t = threadIdx.x & 3;
+  uint32_t bad = 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t carries = 0u;
+#pragma unroll
+    for (int c = 0; c < W; ++c) carries |= test.carry(wv[j][c]);
+    if (test.fails(carries)) bad |= 1u << (2 * t + (j & 1) + 8 * (j >> 1));
+  }
+  bad = __reduce_or_sync(0xffffffffu, bad);
+  if (bad) {
+    bad_from = min(bad_from, tok + __ffs(bad) - 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if ((bad >> (2 * t + (j & 1) + 8 * (j >> 1))) & 1u)
+#pragma unroll
+        for (int c = 0; c < W; ++c) wv[j][c] = 0u;
+  }
+}
+
 template <int F, int D, int NB, bool kF32>
-__global__ void __launch_bounds__(kFThreads)
+__global__ void __launch_bounds__(kFThreads, few_ctas<D, NB>())
     query_few_kernel(KvqView v, QueryArgs a, int row_base, int passes, int sh, float* ws, int dynamic,
                      const __grid_constant__ CUtensorMap tmap) {
   constexpr int NS = D / 16;      // steps of the first product, and channel tiles of the second
@@ -229,6 +279,10 @@ __global__ void __launch_bounds__(kFThreads)
     const int nq = n_quantized(T, v.R), n = query_count(v, a, b), rows = n * v.n_rep - row0;
     // no token that the pass's last row does not see (the call's last row sees them all)
     const int seen = rows <= 0 ? 0 : rows <= 8 * NB ? T : query_end(a, T, n, (row0 + 8 * NB - 1) / v.n_rep);
+    // Tiles behind this hold tokens that some rows do not see.  A weight of zero would not keep such a row from a value
+    // that is not finite; so there those values are left out, and the rows that see one get NaN for their sum.
+    const int all_see = rows > 0 ? query_end(a, T, n, row0 / v.n_rep) : T;
+    int bad_from = 0x7fffffff;
     const int t0 = (int)(j0 << (4 + sh));
     const int t1 = max(t0, (int)min(min((unsigned)T, few_units(seen, 0) * kTile), j1 << (4 + sh)));
     const int tq = min(t1, nq);                                // tiles before tq come from the pages
@@ -432,7 +486,8 @@ __global__ void __launch_bounds__(kFThreads)
         cphase ^= 1u;
       }
       ++n_consumed;
-      const float kf = __shfl_sync(0xffffffffu, ks_l, blk), vf = __shfl_sync(0xffffffffu, vs_l, blk);
+      const float kf = __shfl_sync(0xffffffffu, ks_l, blk);
+      float vf = __shfl_sync(0xffffffffu, vs_l, blk);
       valid = valid && __shfl_sync(0xffffffffu, (int)sok_l, blk);
       if (--left == 0) {
         left = v.kgroup / kTile;
@@ -445,6 +500,14 @@ __global__ void __launch_bounds__(kFThreads)
       if (__all_sync(0xffffffffu, valid)) {  // a tile without its page, or its scales, takes no weight
         const uint8_t* kt = sm.kv[warp][stage][0];
         const uint8_t* vt = sm.kv[warp][stage][1];
+        if (__builtin_expect(tok + kTile > all_see, 0)) {
+          if constexpr (F != kI8)
+            drop_not_finite<D>(sm.kv[warp][stage][1], lane, F == kE4 ? kFiniteE4 : kFiniteE5, tok, bad_from);
+          if (!(vf < INFINITY)) {
+            bad_from = min(bad_from, tok);
+            vf = 0.f;
+          }
+        }
         float acc[NB][4], odd[4] = {0.f, 0.f, 0.f, 0.f};  // one block: two chains of half the length
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
@@ -533,8 +596,8 @@ __global__ void __launch_bounds__(kFThreads)
           x1[4 * c] = y1.x; x1[4 * c + 1] = y1.y; x1[4 * c + 2] = y1.z; x1[4 * c + 3] = y1.w;
         }
 #pragma unroll
-        for (int c = 0; c < LC / 2; ++c) m2 = bf16x2_absmax(bf16x2_absmax(m2, x0[c]), x1[c]);
-        norm_factors(warp_max(max(m2 & 0xffffu, m2 >> 16)), down, kf);
+        for (int c = 0; c < LC / 2; ++c) m2 = bf16x2_finite_max(bf16x2_finite_max(m2, x0[c]), x1[c]);
+        norm_factors(finite_top(m2), down, kf);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
           const uint32_t a0 = bf16x2_scaled(x0[2 * s], down), a1 = bf16x2_scaled(x1[2 * s], down);
@@ -557,9 +620,10 @@ __global__ void __launch_bounds__(kFThreads)
           wv[j][4 * c] = x.x; wv[j][4 * c + 1] = x.y; wv[j][4 * c + 2] = x.z; wv[j][4 * c + 3] = x.w;
         }
 #pragma unroll
-        for (int c = 0; c < W; ++c) m2 = bf16x2_absmax(m2, wv[j][c]);
+        for (int c = 0; c < W; ++c) m2 = bf16x2_finite_max(m2, wv[j][c]);
       }
-      norm_factors(warp_max(max(m2 & 0xffffu, m2 >> 16)), down, f);
+      if (__builtin_expect(tok + kTile > all_see, 0)) drop_not_finite(wv, tok, bad_from);
+      norm_factors(finite_top(m2), down, f);
       const int e = max(kMinExp, exponent_of(f));
       f *= pow2i(-e);
       uint32_t ph[NB][2], pl[NB][2];
@@ -590,7 +654,7 @@ __global__ void __launch_bounds__(kFThreads)
           float* rec = part + ((long long)(run + b * heads + (int)hp) * rows_max + row) * (D + 4);
           if (g == 0) {
             rec[0] = m_run[nb][r];
-            rec[1] = l_run[nb][r];
+            rec[1] = end[nb][r] > bad_from ? __int_as_float(0x7fffffff) : l_run[nb][r];
           }
 #pragma unroll
           for (int m = 0; m < NS; ++m)
@@ -691,7 +755,7 @@ __global__ void __launch_bounds__(kMWarps * 32)
   }
   const long long out0 = (((long long)b * a.n_q + i) * v.Hq + hq) * D;
   if (solo) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays
 #pragma unroll
     for (int c = 0; c < PER; c += 2) {
       const long long at = out0 + lane * PER + c;
@@ -717,7 +781,7 @@ __global__ void __launch_bounds__(kMWarps * 32)
   for (int w = 0; w < kMWarps; ++w) M = fmaxf(M, m_s[w]);
 #pragma unroll
   for (int w = 0; w < kMWarps; ++w) L = fmaf(l_s[w], exp2f(m_s[w] - M), L);
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
   for (int c = threadIdx.x; c < D; c += kMWarps * 32) {
     float s = 0.f;
 #pragma unroll

@@ -98,6 +98,7 @@ struct Misc {
   uint64_t s_full[2], p_full[2], o_full[2], q_full[2], turn[2];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   Seg seg[kSegs];
+  int bad_from[kSegs];          // of a segment: first token whose value is not finite, among those that some rows do not see
   float row_x[2][kRows];        // exchange between the two threads of a row
   uint32_t tmem;
   int abort;
@@ -392,9 +393,9 @@ __device__ __noinline__ int window_piece(const void* win, const KvqView& v, int 
     if (tok + r < T)
       x[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(win) +
                                              (((long long)b * v.R + (tok + r - nq)) * v.Hkv + h) * D + 8 * c);
-    m2 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(m2, x[i].x), x[i].y), x[i].z), x[i].w);
+    m2 = bf16x2_finite_max(bf16x2_finite_max(bf16x2_finite_max(bf16x2_finite_max(m2, x[i].x), x[i].y), x[i].z), x[i].w);
   }
-  const int k = max(kMinExp, norm_exponent(warp_max(max(m2 & 0xffffu, m2 >> 16))));
+  const int k = max(kMinExp, norm_exponent(finite_top(m2)));
   if (write) {
     const float down = pow2i(-k);
 #pragma unroll
@@ -406,6 +407,34 @@ __device__ __noinline__ int window_piece(const void* win, const KvqView& v, int 
     }
   }
   return k;
+}
+
+// A weight of zero would not keep a row from a value that is not finite.  So in tiles that some of the unit's rows do
+// not see whole, such tokens' rows of a piece are zeroed, and the first noted: rows that see it get NaN for their sum.
+template <int D>
+__device__ __noinline__ void drop_not_finite(uint8_t* dst, int piece, int lane, int tok, int* bad_from) {
+  constexpr int CPR = D / 8;
+  __syncwarp();
+  constexpr FiniteTest test = kFiniteF16x2;
+  uint32_t carries = 0u;
+#pragma unroll
+  for (int r0 = 0; r0 < 16; r0 += 32 / CPR) {
+    const uint4 x = *reinterpret_cast<const uint4*>(dst + tile_chunk(16 * piece + r0 + lane / CPR, lane % CPR));
+    carries |= test.carry(x.x) | test.carry(x.y) | test.carry(x.z) | test.carry(x.w);
+  }
+  if (!__any_sync(0xffffffffu, test.fails(carries))) return;
+#pragma unroll 1
+  for (int r0 = 0; r0 < 16; r0 += 32 / CPR) {
+    const int r = r0 + lane / CPR;
+    uint4* at = reinterpret_cast<uint4*>(dst + tile_chunk(16 * piece + r, lane % CPR));
+    const uint4 x = *at;
+    const bool bad = test.fails(test.carry(x.x) | test.carry(x.y) | test.carry(x.z) | test.carry(x.w));
+    const uint32_t mine = __ballot_sync(0xffffffffu, bad) >> (lane / CPR * CPR) & ((1u << CPR) - 1u);
+    if (mine) {
+      *at = make_uint4(0u, 0u, 0u, 0u);
+      if (lane % CPR == 0) atomicMin(bad_from, tok + r);
+    }
+  }
 }
 
 // Place of a row in q and out: rows follow one another head by head within a query, then to the next query's
@@ -589,6 +618,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
       j = run.j0;
       if (lane == 0) {
         const int i = w.qt * RT / v.n_rep;
+        mi.bad_from[k] = 0x7fffffff;
         mi.seg[k] = Seg{w.b, w.h, w.qt, w.T, nq, w.n, w.rows, run.j0, run.j1, run.j1 == w.tiles,
                         i, w.qt * RT - i * v.n_rep, run.last(), {0, 0, 0}};
         mbar_arrive(&mi.seg_full[k]);
@@ -695,6 +725,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         hand_over(&mi.k_full[st], lane);
         ok = wait(&mi.raw_v_full[rs], rp) && wait(&mi.v_empty[st], ph ^ 1);
         if (!ok) break;
+        const bool whole = t0 + kTok <= query_end(a, w.T, w.n, w.i);  // every row of the unit sees the tile
         if (plain && skip_v == 0) {
           convert_pieces<F, D>(sm + L::raw_v(rs), vd, warp - kConv0, lane);
         } else
@@ -708,6 +739,11 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           } else {
             window_piece<D>(v.v_win, v, w.b, w.h, tok, w.T, w.nq, vd, piece, lane, true);
           }
+        }
+        if (!whole && !(plain && F == kI8)) {
+#pragma unroll 1
+          for (int piece = warp - kConv0; piece < kPieces; piece += kConvWarps)
+            drop_not_finite<D>(vd, piece, lane, t0 + 16 * piece, &mi.bad_from[(nseg - 1) % kSegs]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&mi.raw_v_empty[rs]);
@@ -950,7 +986,8 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
       if (ok && (two || s == 0)) {
         const bool first = it0 == 0;
         const bool whole = begins && ends;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        if (end > mi.bad_from[(nseg - 1) % kSegs]) l = __int_as_float(0x7fffffff);
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays
         const int rs = (two ? s * kRows : 0) + row_l;
         float* rec = reinterpret_cast<float*>(ws + many_header_bytes(gridDim.x) +
                                               (2ull * blockIdx.x + (first ? 0 : 1)) * many_rec_bytes(D, RT)) +
@@ -1053,7 +1090,7 @@ __global__ void __launch_bounds__(kMergeRows * 32) many_merge_kernel(KvqView v, 
     k = (k / 2 + 1) * 2;  // the next CTA's first record
     if (k >= 2 * grid || !hdr[k].used) break;  // a run that gave up
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   const long long e = (((long long)u.b * a.n_q + row / v.n_rep) * v.Hq + u.h * v.n_rep + row % v.n_rep) * D + lane * PER;
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + e);
 #pragma unroll

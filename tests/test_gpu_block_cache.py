@@ -692,3 +692,55 @@ def test_rope_append_of_17_to_32_rows(cfg, rot, halves):
         c.check_pages()
         c.check_lengths_and_window()
         c.check_dequantize()
+
+
+# ----------------------------------------------------------- what a row does not see must not reach it
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("fmt", [E4, E5, I8])
+@pytest.mark.parametrize("D,Hq,H,n", [(128, 8, 2, 5), (64, 16, 16, 21), (128, 16, 4, 70), (64, 4, 4, 300), (256, 8, 2, 9),
+                                      (128, 2, 1, 140)])
+def test_masked_tokens_that_are_not_finite(fmt, D, Hq, H, n, wide):
+    """NaN and infinities in keys and values of tokens that only later queries see, in the window and in blocks
+    (as codes, and as an infinite scale): the earlier queries' outputs stay (each is within 2^-8 |out| + 2^-10 sum p |v| of
+    the exact one, |v| < 8, so two differ by 2^-7 |out| + 2^-6 at most); every row that sees a value of NaN is NaN."""
+    cfg = cfg_of(Hq, H, D, fmt, fmt, 64, 64, 64)
+    g, L = np.random.default_rng(5), O.layout(cfg)
+    for T, first in ((500, 497), (500, 460 if n > 45 else 498), (448, 446),
+                     (470 + n, (470 + n) // 64 * 64 - 20 if n > 30 else 470 + n - 2)):
+        if T - n > first:
+            continue
+        Ks = [[O.bf16(g.standard_normal((T, D))) for _ in range(H)]]
+        Vs = [[O.bf16(g.standard_normal((T, D))) for _ in range(H)]]
+        c = Case(cfg, [T], seed=1, streams=(Ks, Vs))
+        q = torch_src(O.bf16(g.standard_normal((1, n, Hq, D))), cfg)
+        cache = (widened(c, 1 << 21) if wide else c).cache
+        want = cache.query_attention(q)
+        seen = first - (T - n)                   # queries [0, seen) see no token from `first` on
+        nq = T // 64 * 64
+        for bad in (float("nan"), float("inf"), -float("inf")):
+            for b in range(max(first, nq), T):   # window rows
+                cache.k_win[0, b - nq, :, 3] = bad
+                cache.v_win[0, b - nq, :, D - 2] = bad
+            if first < nq and fmt != I8:         # codes of the tokens of the last block that are not seen
+                page = cache.page_view()[c.block_table[0, (nq - 1) // 64]]
+                code = 0x7F if fmt == E4 else (0x7E if np.isnan(bad) else 0x7C)
+                for h in range(H):
+                    hb = page[h * L["head"]:]
+                    for t in range(first, nq):
+                        hb[L["kc"] + (t % 64) * D + 1] = code
+                        hb[L["vc"] + (t % 64) * D + D - 1] = code
+            got = cache.query_attention(q)
+            assert torch.allclose(got[:, :seen].float(), want[:, :seen].float(), rtol=2.0 ** -7, atol=2.0 ** -6), (T, first, bad)
+            assert bool(torch.isfinite(got[:, :seen]).all())
+            if np.isnan(bad) and (first >= nq or fmt != I8):
+                assert bool(torch.isnan(got[:, seen:, :, D - 2 if first >= nq else D - 1]).all())
+        before = nq - 64 - (T - n)               # queries that see nothing of the last block
+        if before > 0:
+            page = cache.page_view()[c.block_table[0, (nq - 1) // 64]]
+            for h in range(H):
+                for at in (L["vm"], L["km"]):
+                    page[h * L["head"] + at:h * L["head"] + at + 4] = torch.tensor([0, 0, 0x80, 0x7F], dtype=torch.uint8)
+            got = cache.query_attention(q)
+            assert torch.allclose(got[:, :before].float(), want[:, :before].float(), rtol=2.0 ** -7, atol=2.0 ** -6)
+        assert int(cache.status.item()) == 0
