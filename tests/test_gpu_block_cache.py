@@ -744,3 +744,49 @@ def test_masked_tokens_that_are_not_finite(fmt, D, Hq, H, n, wide):
             got = cache.query_attention(q)
             assert torch.allclose(got[:, :before].float(), want[:, :before].float(), rtol=2.0 ** -7, atol=2.0 ** -6)
         assert int(cache.status.item()) == 0
+
+
+@pytest.mark.parametrize("n", [1, 6, 40])
+@pytest.mark.parametrize("Bn", [1000, 4096, 4097])
+def test_large_batches(Bn, n):
+    """Thousands of sequences over the same pages (4,097 exceed the split's table and take the plain kernel): every
+    one within the bound of the exact output, empty ones zeros."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(4, 2, 64, E4, E4, 32, 32, 32)
+    c = Case(cfg, [137], seed=3)
+    lens = torch.full((Bn,), 137, dtype=torch.int32, device="cuda")
+    lens[5::7] = 0
+    many = K.PagedKVCache.over(c.c_cfg, c.cache.pages, c.cache.block_table.repeat(Bn, 1), lens,
+                               c.cache.k_win.repeat(Bn, 1, 1, 1), c.cache.v_win.repeat(Bn, 1, 1, 1))
+    q = torch_src(O.bf16(np.random.default_rng(n).standard_normal((1, n, 4, 64))), cfg)
+    got = many.query_attention(q.repeat(Bn, 1, 1, 1)).double().cpu().numpy()
+    assert not got[5::7].any()
+    got = np.delete(got, np.s_[5::7], 0)
+    qs = q.double().cpu().numpy()[0]
+    for h in range(2):
+        Kd, Vd = O.dequantize_stream(cfg, c.states[0][h], c.k_scale[h], c.v_scale[h])
+        ref, size = O.query_attention(qs[:, 2 * h:2 * h + 2], Kd, Vd, True)
+        lim = 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * size + 2.0 ** -25 * np.abs(Vd).sum(0)
+        assert np.all(np.abs(got[:, :, 2 * h:2 * h + 2] - ref) <= lim)
+    assert int(many.status.item()) == 0
+
+
+def test_nothing_to_do():
+    """No new rows, no queries, no tokens."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(8, 2, 128, E4, E4, 64, 64, 64)
+    c = Case(cfg, [0, 0], seed=1, extra_pages=2).cache
+    rope = K.make_rope(rope_setup(256, 128)[1], 128)
+    x = torch.zeros(2, 0, 12, 128, device="cuda").bfloat16()
+    q = c.append_rope(rope, x[:, :, :8], x[:, :, 8:10], x[:, :, 10:])
+    assert q.shape == (2, 0, 8, 128) and c.seq_lens.tolist() == [0, 0]
+    assert c.query_attention(q).shape == (2, 0, 8, 128)
+    for n in (1, 5, 40, 300):
+        q = torch.ones(2, n, 8, 128, device="cuda").bfloat16()
+        for causal in (True, False):
+            assert not bool(c.query_attention(q, causal=causal).any())
+    assert not bool(c.attention(torch.ones(2, 8, 128, device="cuda").bfloat16()).any())
+    counts = torch.zeros(2, dtype=torch.int32, device="cuda")
+    out = torch.full((2, 5, 8, 128), 3.0, device="cuda").bfloat16()
+    assert bool((c.query_attention(torch.ones_like(out), n_q_per_seq=counts, out=out) == 3.0).all())
+    assert int(c.status.item()) == 0
