@@ -21,7 +21,7 @@
 // cluster barrier that follows every CTA's read of it.  Prompts take two: blocks and
 // queries over the whole GPU, then (a programmatic dependent) the window rows and lengths.
 //
-// Measured (8 kv-heads of 128): 8 prompts of 4,096 tokens with 64 query heads take 244 us, 5.3 TB/s (78% of the
+// Measured (8 kv-heads of 128): 8 prompts of 4,096 tokens with 64 query heads take 230 us, 5.6 TB/s (82% of the
 // measured copy bandwidth); a decode step of 64 sequences 5.5 us, 9 where a window fills.
 #include "kvq_host.h"
 #include "kvq_internal.cuh"
@@ -466,7 +466,9 @@ __global__ void __launch_bounds__(kThreads, 4) block_step_kernel(KvqView v, Bloc
   if (live && rank == 0 && threadIdx.x == 0) v.seq_lens[b] = T0 + n;
 }
 
-constexpr int kQTask = 8;  // heads a thread takes of a token in a prompt
+// Heads a thread takes of a token in a prompt.  8 prompts of 4,096 tokens with 64 query heads take 230 us with 2, 238
+// with 4, 340 with 8 (fewer threads with loads in flight), 272 with 1 (the angles are loaded again).
+constexpr int kQHeads = 2;
 
 // Blocks and queries of a prompt: CTAs [0, nfold) take one (sequence, block, head) each, the
 // rest q_tok tokens of a sequence's queries.
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 4) block_prompt_kernel(KvqView v, Bl
     const unsigned x = u - nfold;
     const int b = x / q_units, i0 = x % q_units * q_tok;
     if (!sequence_step(v, a, b, T0, n, &bad)) return;
-    if (i0 < n) rotate_queries<BF16, kThreads, kQTask / 2>(v, a, b, T0, i0, min(n, i0 + q_tok), 0, v.Hq);
+    if (i0 < n) rotate_queries<BF16, kThreads, kQHeads>(v, a, b, T0, i0, min(n, i0 + q_tok), 0, v.Hq);
   }
 }
 
@@ -502,9 +504,9 @@ __global__ void __launch_bounds__(kThreads) rope_query_kernel(KvqView v, BlockAp
   rotate_queries<BF16, kThreads, 1>(v, a, b, T0, i0, min(n, i0 + q_tok), 0, v.Hq);
 }
 
-// Tokens of queries a CTA takes: about 8 passes of its threads over groups of kQTask / 2 heads.
+// Tokens of queries a CTA takes: about two passes of its threads over groups of kQHeads heads.
 int query_tokens(const KvqView& v) {
-  const int slots = kThreads / (v.D / kCh), groups = (v.Hq + kQTask / 2 - 1) / (kQTask / 2);
+  const int slots = kThreads / (v.D / kCh), groups = (v.Hq + kQHeads - 1) / kQHeads;
   const int t = 2 * slots / groups;
   return t < 1 ? 1 : t;
 }
