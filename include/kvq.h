@@ -326,7 +326,8 @@ size_t kvq_query_workspace_bytes(const kvq_config* cfg, int32_t batch, int32_t n
  * out: [batch][n_q][Hq][D] device, src dtype (rounded once, to nearest even);
  * rows at or beyond n_q_per_seq[b] are left as they were.  A query that sees no
  * token (an empty cache, or more queries than tokens under the causal mask) gets
- * zeros.  softmax_scale: 0 means 1/sqrt(D).  workspace: as for
+ * zeros.  A key or value that is not finite makes NaN of the rows that see its token (of
+ * that channel or of all) and leaves the others as they are.  softmax_scale: 0 means 1/sqrt(D).  workspace: as for
  * kvq_decode_attention, kvq_query_workspace_bytes(cfg, batch, n_q) bytes.
  * Every configuration is taken.  PER_BLOCK caches with bf16 sources run on
  * tensor cores; every other configuration runs on a plain kernel of fp32
