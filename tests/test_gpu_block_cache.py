@@ -790,3 +790,48 @@ def test_nothing_to_do():
     out = torch.full((2, 5, 8, 128), 3.0, device="cuda").bfloat16()
     assert bool((c.query_attention(torch.ones_like(out), n_q_per_seq=counts, out=out) == 3.0).all())
     assert int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("n", [1, 6, 90])
+def test_two_streams_at_once(n):
+    """Two cache objects over the same pages, their calls interleaved on two streams: the results of one at a time."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg, lens = CASES["e4m3_p64"]
+    c = Case(cfg, lens, seed=12)
+    a, b = widened(c, 1 << 21).cache, widened(c, 1 << 21).cache
+    qs = [torch_src(O.bf16(np.random.default_rng(i).standard_normal((len(lens), n, 32, 128))), cfg) for i in range(2)]
+    want = [c.cache.query_attention(q, causal=False) if n <= 8 else a.query_attention(q, causal=False) for q in qs]
+    b.query_attention(qs[1], causal=False)  # its workspace
+    torch.cuda.synchronize()
+    s0, s1 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [[torch.empty_like(q) for _ in range(10)] for q in qs]
+    for i in range(10):
+        a.query_attention(qs[0], causal=False, out=outs[0][i], stream=s0)
+        b.query_attention(qs[1], causal=False, out=outs[1][i], stream=s1)
+    torch.cuda.synchronize()
+    for w, row in zip(want, outs):
+        for o in row:
+            assert torch.allclose(o.float(), w.float(), rtol=2.0 ** -7, atol=2.0 ** -6)
+            assert torch.equal(o, row[0])
+    assert int(c.cache.status.item()) == 0
+
+
+@pytest.mark.parametrize("n", [40, 200])
+def test_graph_of_many_rows(n):
+    """Many-row attention captured once: replays follow the lengths on the device, as eager calls do, bit for bit."""
+    cfg, _ = CASES["int8_p16"]
+    c = Case(cfg, [1500, 700, 64], seed=13)
+    cache = widened(c, 1 << 21).cache
+    q = torch_src(O.bf16(np.random.default_rng(n).standard_normal((3, n, 8, 128))), cfg)
+    out = torch.empty_like(q)
+    cache.query_attention(q, out=out)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        cache.query_attention(q, out=out)
+    for lens in ([1500, 700, 64], [1472, 0, 1], [64, 699, 64], [1, 1, 1]):
+        cache.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        out.fill_(7.0)
+        gr.replay()
+        assert torch.equal(out, cache.query_attention(q)), lens
+    assert int(cache.status.item()) == 0
