@@ -113,12 +113,25 @@ class PagedKVCache:
 
     # --- thin wrappers over the C ABI
     def append(self, k_new, v_new, n_new_per_seq=None, stream=None):
+        """k_new, v_new: [batch, n_new, Hkv, D], dense."""
         n = k_new.shape[1]
+        for name, t in (("k_new", k_new), ("v_new", v_new)):
+            if self._rows(name, t, n, self._H) != self._H * self._D and n:
+                raise ValueError(f"{name} must be contiguous")
+        if n_new_per_seq is not None:
+            self._counts("n_new_per_seq", n_new_per_seq)
         B.kvq_quantize_append(self.cfg, self.c, k_new, v_new, n, n_new_per_seq, stream)
 
     def attention(self, q, out=None, softmax_scale=0.0, stream=None):
+        if q.numel() != self.batch * self._Hq * self._D or q.dtype != self._src or not q.is_contiguous():
+            raise ValueError(f"q must be contiguous {self._src} of shape {(self.batch, self._Hq, self._D)}")
+        self._beside("q", q)
         if out is None:
             out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        elif out.numel() != q.numel() or out.dtype != torch.float32 or not out.is_contiguous():
+            raise ValueError("out must be contiguous float32 of q's shape")
+        else:
+            self._beside("out", out)
         B.kvq_decode_attention(self.cfg, self.c, q, out, softmax_scale, self.workspace, stream)
         return out
 
@@ -139,7 +152,8 @@ class PagedKVCache:
             raise ValueError(f"{name} must be {self._src} of shape {(self.batch, n, heads, D)}")
         sb, sn, sh, sd = t.stride()
         row = sn if n > 1 else sb if self.batch > 1 else heads * D
-        if sd != 1 or (heads > 1 and sh != D) or (self.batch > 1 and n > 1 and sb != n * row):
+        # a row below heads * D: a broadcast view, whose storage holds fewer rows than the kernels would read
+        if sd != 1 or (heads > 1 and sh != D) or (self.batch > 1 and n > 1 and sb != n * row) or (n and row < heads * D):
             raise ValueError(f"{name}: a token's row must be contiguous and the tokens evenly spaced")
         self._beside(name, t)
         return row

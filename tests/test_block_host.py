@@ -209,3 +209,46 @@ def test_query_attention_refusals(K):
     assert call(cache=_cache(K, None, status=None)) == E
     assert K.kvq_query_workspace_bytes(_cfg(K), 0, 1) == 0 and K.kvq_query_workspace_bytes(_cfg(K), 1, 0) == 0
     assert K.kvq_query_workspace_bytes(_cfg(K, head_dim=96), 1, 1) == 0
+
+
+# ------------------------------------------------------------------ the cache object's checks
+
+def _object(K, batch=4, heads=2, D=64):
+    """A cache object with what its checks of arguments read, and no device."""
+    c = K.PagedKVCache.__new__(K.PagedKVCache)
+    c.batch, c._D, c._H, c._Hq, c._src = batch, D, heads, 3 * heads, K.src_torch_dtype(_cfg(K))
+    c._beside = lambda name, t: None
+    return c
+
+
+def test_broadcast_rows_are_refused(K):
+    """A row stride of 0 (or below a row) would be read as dense rows, past the end of the tensor's storage."""
+    import torch
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    c, one = _object(K), _object(K, batch=1)
+    for obj, x in ((c, z(1, 1, 2, 64).expand(4, 1, 2, 64)),      # a decode step, one row for all sequences
+                   (one, z(1, 1, 2, 64).expand(1, 9, 2, 64)),    # a prompt, one row for all tokens
+                   (c, z(1, 1, 2, 64).expand(4, 9, 2, 64)),
+                   (c, z(4, 1, 2, 64).expand(4, 9, 2, 64)),
+                   (c, z(1, 9, 2, 64).expand(4, 9, 2, 64)),
+                   (c, z(4, 9, 1, 64).expand(4, 9, 2, 64)),
+                   (c, z(4, 9, 2, 1).expand(4, 9, 2, 64)),
+                   (one, z(20 * 64).as_strided((1, 9, 2, 64), (9 * 64, 64, 64, 1)))):
+        n = x.shape[1]
+        with pytest.raises(ValueError, match="evenly spaced"):
+            obj._rows("k_new", x, n, 2)
+        fine = torch.zeros_like(x, memory_format=torch.contiguous_format)
+        for k, v in ((x, fine), (fine, x)):
+            with pytest.raises(ValueError, match="evenly spaced"):
+                obj.append(k, v)
+    assert c._rows("k", z(4, 9, 2, 64), 9, 2) == 128
+    assert c._rows("k", z(4, 9, 8, 64)[:, :, 3:5], 9, 2) == 512
+    assert c._rows("k", z(4, 1, 8, 64)[:, :, 3:5], 1, 2) == 512
+    assert one._rows("k", z(1, 9, 8, 64)[:, ::3, 3:5], 3, 2) == 3 * 512
+    assert one._rows("k", z(1, 1, 2, 64), 1, 2) == 128
+    assert c._rows("k", z(4, 0, 8, 64)[:, :, 3:5], 0, 2) >= 0
+    # kvq_quantize_append takes dense rows alone
+    for k, v in ((z(4, 9, 8, 64)[:, :, :2], z(4, 9, 2, 64)), (z(4, 9, 2, 64), z(4, 9, 8, 64)[:, :, :2]),
+                 (z(4, 9, 2, 64), z(4, 8, 2, 64)), (z(4, 9, 2, 64).float(), z(4, 9, 2, 64)), (z(3, 9, 2, 64), z(3, 9, 2, 64))):
+        with pytest.raises(ValueError):
+            c.append(k, v)
