@@ -589,16 +589,19 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
   const uint32_t tmem = mi.tmem;
   const Waiter wait{mi, v.status};
 
-  // The next segment (every warp but the copying one): it is read whole and its place given back.
+  // The next segment (every warp but the copying one), read whole.  Its place is given back when the warp reads and
+  // writes it no more: the softmax warps read bad_from at the segment's end.
   uint32_t nseg = 0;
   auto segment = [&](Seg& g) -> bool {
     const uint32_t k = nseg % kSegs;
     const bool ok = wait(&mi.seg_full[k], (nseg / kSegs) & 1);
     g = mi.seg[k];
     ++nseg;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&mi.seg_empty[k]);
     return __all_sync(0xffffffffu, ok);
+  };
+  auto leave_segment = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&mi.seg_empty[(nseg - 1) % kSegs]);
   };
 
   if (warp == kLoadWarp) {
@@ -749,6 +752,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         if (lane == 0) mbar_arrive(&mi.raw_v_empty[rs]);
         hand_over(&mi.v_full[st], lane);
       }
+      leave_segment();
     } while (ok && !w.last);
   } else if (warp >= kMmaWarp) {
     // A warp a stream, so that one's waits do not hold up the other's products (issuing blocks until the
@@ -768,6 +772,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
     Seg w;
     do {
       if (!segment(w) || w.j0 == w.j1) break;
+      leave_segment();
       const int nt = __shfl_sync(0xffffffffu, w.j1 - w.j0, 0);
       const int i0 = two ? 0 : s;  // the stream's tiles: i0, i0 + by, ...
       ok = __all_sync(0xffffffffu, wait(&mi.q_full[two ? s : 0], (nseg - 1) & 1));
@@ -1033,6 +1038,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         }
       }
       tc::fence_before();
+      leave_segment();
       it0 += nt;
     } while (ok && !w.last);
   }

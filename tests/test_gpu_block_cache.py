@@ -835,3 +835,28 @@ def test_graph_of_many_rows(n):
         gr.replay()
         assert torch.equal(out, cache.query_attention(q)), lens
     assert int(cache.status.item()) == 0
+
+
+@pytest.mark.parametrize("n_rep,n,D", [(4, 10, 128), (5, 7, 64), (2, 64, 128), (4, 64, 128)])
+def test_not_finite_in_hundreds_of_one_tile_units(n_rep, n, D):
+    """A CTA of the many-row kernel has many units of one tile each in flight; what one notes of a value that is not
+    finite stays until its outputs have left.  The last token's value is NaN in every other sequence: of those the last
+    query alone is NaN, in all channels or in that one, and every other row is as without it."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(8 * n_rep, 8, D, E4, E4, 64, 64, 64)
+    c = Case(cfg, [97], seed=3)
+    Bn = 600
+    many = K.PagedKVCache.over(c.c_cfg, c.cache.pages, c.cache.block_table.repeat(Bn, 1), c.cache.seq_lens.repeat(Bn),
+                               c.cache.k_win.repeat(Bn, 1, 1, 1), c.cache.v_win.repeat(Bn, 1, 1, 1))
+    wide = widened(c, 1 << 21).cache
+    q = torch_src(O.bf16(np.random.default_rng(n).standard_normal((1, n, 8 * n_rep, D))), cfg)
+    want = wide.query_attention(q)
+    assert bool(torch.isfinite(want).all())
+    many.v_win[::2, 96 - 64, :, 5] = float("nan")
+    for _ in range(4):
+        got = many.query_attention(q.repeat(Bn, 1, 1, 1))
+        assert bool(torch.isnan(got[::2, n - 1, :, 5]).all())
+        # each within 2^-8 |out| + 2^-10 sum p |v| of the exact output, |v| < 8
+        for part, ref in ((got[::2, :n - 1], want[:, :n - 1]), (got[1::2], want)):
+            assert torch.allclose(part.float(), ref.float().expand_as(part), rtol=2.0 ** -7, atol=2.0 ** -6)
+    assert int(many.status.item()) == 0
