@@ -259,6 +259,7 @@ static __device__ __noinline__ bool plan_run(const KvqView& v, const QueryArgs& 
     if (b < v.batch) wb[b] = s;
     total += s;
   }
+  __syncwarp();  // wb is read by other lanes than wrote it
   total = sum64(total) * v.Hkv;
   // no CTA between two others is left without a place: the merge walks from one to the next
   const unsigned long long runs = min((unsigned long long)gridDim.x, total), me = blockIdx.x;
@@ -703,8 +704,8 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         const int rs = two ? 0 : st;
         uint8_t* kd = sm + L::kK + st * L::kTileB;
         uint8_t* vd = sm + L::kV + st * L::kTileB;
-        ok = wait(&mi.raw_k_full[rs], rp) && wait(&mi.k_empty[st], ph ^ 1);
-        if (!ok) break;
+        ok = __all_sync(0xffffffffu, wait(&mi.raw_k_full[rs], rp) && wait(&mi.k_empty[st], ph ^ 1));
+        if (!ok) break;  // the warp as one: what follows has barriers of the warp
         const uint32_t skip_k = mi.skip_k[slot], skip_v = mi.skip_v[slot];
         const bool plain = t0 + kTok <= w.nq;  // every piece is a page's
         if (plain && skip_k == 0) {
@@ -726,7 +727,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         __syncwarp();
         if (lane == 0) mbar_arrive(&mi.raw_k_empty[rs]);
         hand_over(&mi.k_full[st], lane);
-        ok = wait(&mi.raw_v_full[rs], rp) && wait(&mi.v_empty[st], ph ^ 1);
+        ok = __all_sync(0xffffffffu, wait(&mi.raw_v_full[rs], rp) && wait(&mi.v_empty[st], ph ^ 1));
         if (!ok) break;
         const bool whole = t0 + kTok <= query_end(a, w.T, w.n, w.i);  // every row of the unit sees the tile
         if (plain && skip_v == 0) {
@@ -829,9 +830,9 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
     uint8_t* const qd = sm + L::kQ + (two ? s : 0) * L::kTileB;
     Seg w;
     do {
-      // (threads that share barriers give up together)
+      // (threads that share barriers give up together: with 128 rows both streams, which are joined at the end)
       ok = segment(w);
-      if (any_of<2 * kRows>(kBarStream + s, !ok) || w.j0 == w.j1) break;
+      if ((two ? any_of<2 * kRows>(kBarStream + s, !ok) : any_of<4 * kRows>(kBarJoin, !ok)) || w.j0 == w.j1) break;
       const int j0 = w.j0, nt = w.j1 - w.j0;
       const int off = two ? s * kRows : 0;                     // the stream's first row in the unit
       const bool live = w.qt * RT + off + row_l < w.rows;
