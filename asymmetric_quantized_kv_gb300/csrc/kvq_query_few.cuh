@@ -698,9 +698,10 @@ __global__ void __launch_bounds__(kMWarps * 32)
     row += (hp - h * passes) * rows_max;
   }
   const int i = row / v.n_rep, hq = h * v.n_rep + (row - i * v.n_rep);
-  if (b >= v.batch || i >= query_count(v, a, b)) return;
-  const unsigned units = few_units(seq_tokens(v, b), sh);
-  grid_dep_wait();
+  const bool some = b < v.batch && i < query_count(v, a, b);
+  const unsigned units = some ? few_units(seq_tokens(v, b), sh) : 0;
+  grid_dep_wait();  // every CTA: where no row has a query, the end of this grid still follows the first kernel's
+  if (!some) return;
   const FewPlan plan = *reinterpret_cast<const FewPlan*>(ws);
   const unsigned* pref =
       reinterpret_cast<const unsigned*>(reinterpret_cast<const char*>(ws) + sizeof(FewPlan));

@@ -860,3 +860,20 @@ def test_not_finite_in_hundreds_of_one_tile_units(n_rep, n, D):
         for part, ref in ((got[::2, :n - 1], want[:, :n - 1]), (got[1::2], want)):
             assert torch.allclose(part.float(), ref.float().expand_as(part), rtol=2.0 ** -7, atol=2.0 ** -6)
     assert int(many.status.item()) == 0
+
+
+def test_calls_without_queries_between_others():
+    """Calls in which no sequence has a query write their plan to the same workspace as the calls around them."""
+    cfg, lens = CASES["e4m3_p64"]
+    c = Case(cfg, lens, seed=4)
+    q = torch_src(O.bf16(np.random.default_rng(1).standard_normal((len(lens), 3, 32, 128))), cfg)
+    none = torch.zeros(len(lens), dtype=torch.int32, device="cuda")
+    cache = widened(c, 1 << 21).cache
+    want, keep = cache.query_attention(q), torch.full_like(q, 7.0)
+    outs = [torch.empty_like(q) for _ in range(40)]
+    for o in outs:
+        cache.query_attention(q, n_q_per_seq=none, out=keep)
+        cache.query_attention(q, out=o)
+        cache.query_attention(q, n_q_per_seq=none, out=keep)
+    assert all(torch.equal(o, want) for o in outs) and bool((keep == 7.0).all())
+    assert int(cache.status.item()) == 0
