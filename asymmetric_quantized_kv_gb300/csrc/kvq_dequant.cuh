@@ -10,12 +10,15 @@ namespace kvq {
 // Scale slot of PER_CHANNEL / PER_BLOCK group g0 / G inside its page (the page of token g0).
 __device__ __forceinline__ int group_slot(int g0, int P, int G) { return (g0 % P) / G; }
 
-// Scale of the PER_BLOCK block that holds token t of sequence b (0 when its page is missing).
+// Scale of the PER_BLOCK block that holds token t of sequence b (0, and *ok cleared, when its page is missing).
 // off_meta: v.off_km or v.off_vm.
-__device__ __forceinline__ float block_scale(const KvqView& v, int b, int h, int t, int off_meta) {
+__device__ __forceinline__ float block_scale(const KvqView& v, int b, int h, int t, int off_meta, bool* ok) {
   const int g0 = t / v.kgroup * v.kgroup;  // keys and values share one group
   const uint8_t* page = page_of(v, b, g0);
-  if (!page) return 0.f;
+  if (!page) {
+    *ok = false;
+    return 0.f;
+  }
   return load_meta(page + (long long)h * v.head_bytes + off_meta, group_slot(g0, v.P, v.kgroup), v.meta16);
 }
 
@@ -25,7 +28,7 @@ __device__ __forceinline__ float block_code_value(unsigned u, int fmt) {
 }
 
 // Channel c of the key of token t < T (nq = n_quantized(T, R)) of sequence b, kv-head h.
-// *ok is cleared when a page is missing.
+// *ok is cleared when its page is missing, or the page that holds its group's scale.
 __device__ inline float cache_key(const KvqView& v, int b, int h, int t, int c, int nq, bool* ok) {
   if (t >= nq) return load_src(v.k_win, (((long long)b * v.R + (t - nq)) * v.Hkv + h) * v.D + c, v.src_bf16);
   const uint8_t* page = page_of(v, b, t);
@@ -36,7 +39,7 @@ __device__ inline float cache_key(const KvqView& v, int b, int h, int t, int c, 
   const uint8_t* hb = page + (long long)h * v.head_bytes;
   const int slot = t % v.P;
   const unsigned ku = get_code(hb + (long long)slot * v.krow, c, v.kbits);
-  if (v.kaxis == KVQ_PER_BLOCK) return __fmul_rn(block_code_value(ku, v.kfmt), block_scale(v, b, h, t, v.off_km));
+  if (v.kaxis == KVQ_PER_BLOCK) return __fmul_rn(block_code_value(ku, v.kfmt), block_scale(v, b, h, t, v.off_km, ok));
   if (is_fp8(v.kfmt)) return __fmul_rn(fp8_to_float(ku, v.kfmt), v.k_scale[h]);
   if (v.kaxis == KVQ_PER_TENSOR) return dequant_sym(signed_code(ku, v.kbits, KVQ_SYM_ABSMAX), v.k_scale[h]);
   const uint8_t* meta;
@@ -68,7 +71,10 @@ __device__ inline float cache_value(const KvqView& v, int b, int h, int t, int c
   const uint8_t* hb = page + (long long)h * v.head_bytes;
   const int slot = t % v.P;
   const unsigned vu = get_code(hb + v.off_vc + (long long)slot * v.vrow, c, v.vbits);
-  if (v.vaxis == KVQ_PER_BLOCK) return __fmul_rn(block_code_value(vu, v.vfmt), block_scale(v, b, h, t, v.off_vm));
+  if (v.vaxis == KVQ_PER_BLOCK) {
+    bool ok;  // as its key's
+    return __fmul_rn(block_code_value(vu, v.vfmt), block_scale(v, b, h, t, v.off_vm, &ok));
+  }
   if (is_fp8(v.vfmt)) return __fmul_rn(fp8_to_float(vu, v.vfmt), v.v_scale[h]);
   if (v.vaxis == KVQ_PER_TENSOR) return dequant_sym(signed_code(vu, v.vbits, KVQ_SYM_ABSMAX), v.v_scale[h]);
   const uint8_t* meta = hb + v.off_vm + (long long)slot * v.v_ng * v.v_nmeta * v.mb;

@@ -877,3 +877,28 @@ def test_calls_without_queries_between_others():
         cache.query_attention(q, n_q_per_seq=none, out=keep)
     assert all(torch.equal(o, want) for o in outs) and bool((keep == 7.0).all())
     assert int(cache.status.item()) == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "mixed"])
+def test_missing_page_of_a_blocks_scales(kind):
+    """Blocks over several pages.  A missing page's tokens get no weight, and where it holds the block's scales the
+    whole block gets none: on the tensor-core kernels (bf16) and on the plain one (fp32 sources, differing formats)."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(8, 2, 128, E4, I8 if kind == "mixed" else E4, 64, 64, 16, src=O.F32 if kind == "f32" else O.BF16)
+    T = 300
+    c = Case(cfg, [T], seed=6)
+    c.cache.block_table[0, 4] = c.cache.n_pages + 3   # tokens 64 .. 79, and the scales of 64 .. 127
+    c.cache.block_table[0, 9] = -1                    # tokens 144 .. 159 alone
+    keep = np.ones(T, bool)
+    keep[64:128] = keep[144:160] = False
+    half = 2.0 ** -24 if kind == "f32" else 2.0 ** -8
+    for n in (1, 6, 40):
+        q = O.bf16(np.random.default_rng(n).standard_normal((1, n, 8, 128)))
+        for cache in (c.cache, widened(c, 1 << 21).cache):
+            got = cache.query_attention(torch_src(q, cfg), causal=False).double().cpu().numpy()
+            assert int(c.cache.status.item()) | int(cache.status.item()) == K.KVQ_DEV_BAD_PAGE
+            for h in range(2):
+                Kd, Vd = O.dequantize_stream(cfg, c.states[0][h], c.k_scale[h], c.v_scale[h])
+                ref, size = O.query_attention(q[0, :, 4 * h:4 * h + 4], Kd[keep], Vd[keep], False)
+                lim = half * np.abs(ref) + 2.0 ** -10 * size + 2.0 ** -25 * np.abs(Vd).sum(0)
+                assert np.all(np.abs(got[0, :, 4 * h:4 * h + 4] - ref) <= lim), (n, h)
