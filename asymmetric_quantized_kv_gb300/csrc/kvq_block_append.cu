@@ -211,14 +211,16 @@ __device__ __forceinline__ void load_item(const KvqView& v, const BlockAppend& a
   }
 }
 
+// Largest magnitude of an item, as bits: ordered like the magnitudes, infinities and then NaN above them (a maximum of
+// floats would pass over NaN).
 template <bool BF16>
-__device__ __forceinline__ float item_absmax(const Item<BF16>& it) {
+__device__ __forceinline__ uint32_t item_absmax(const Item<BF16>& it) {
   float x[kCh];
   it.get(x);
-  float m[4] = {0.f, 0.f, 0.f, 0.f};
+  uint32_t m[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int i = 0; i < kCh; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(x[i]));
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+  for (int i = 0; i < kCh; ++i) m[i & 3] = max(m[i & 3], __float_as_uint(x[i]) & 0x7fffffffu);
+  return max(max(m[0], m[1]), max(m[2], m[3]));
 }
 
 // Two FP8 bytes (a in the low one): nearest, ties to even, saturating.
@@ -238,7 +240,7 @@ __device__ __forceinline__ uint32_t fp8x2(float a, float b) {
 // 2^-20 |q| of one (over five times the distance of the two quotients) and values that are not finite take the
 // IEEE division.  FP8: the quotient lies between q (1 - 2^-20) and q (1 + 2^-20), and rounding is monotone: where
 // both ends give the same byte it is the quotient's, elsewhere the division decides.  (r is exact enough only
-// while 1 / s is a normal number: smaller or larger scales divide.)
+// while 1 / s is a normal number: smaller or larger scales divide.)  Scales of 0 and NaN give codes 0.
 template <int F>  // 0 INT8, 1 E4M3, 2 E5M2
 __device__ __forceinline__ uint2 codes8(const float* x, float s, float r) {
   uint32_t w[2] = {0u, 0u};
@@ -249,7 +251,7 @@ __device__ __forceinline__ uint2 codes8(const float* x, float s, float r) {
       float c = rintf(q);
       if (!(fabsf(__fsub_rn(fabsf(__fsub_rn(q, c)), 0.5f)) > __fmul_rn(9.5367431640625e-07f, fabsf(q))))
         c = rintf(__fdiv_rn(x[i], s));
-      const uint32_t u = s == 0.f ? 0u : static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(c, -127.f), 127.f))) & 0xFFu;
+      const uint32_t u = !(s > 0.f) ? 0u : static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(c, -127.f), 127.f))) & 0xFFu;
       w[i >> 2] |= u << (8 * (i & 3));
     }
   } else {
@@ -260,7 +262,7 @@ __device__ __forceinline__ uint2 codes8(const float* x, float s, float r) {
       const float a = __fmul_rn(x[i], r), b = __fmul_rn(x[i + 1], r);
       uint32_t u = fp8x2<F == 2>(__fmul_rn(a, kLo), __fmul_rn(b, kLo));
       if (!near || u != fp8x2<F == 2>(__fmul_rn(a, kHi), __fmul_rn(b, kHi)))
-        u = s == 0.f ? 0u : fp8x2<F == 2>(__fdiv_rn(x[i], s), __fdiv_rn(x[i + 1], s));
+        u = !(s > 0.f) ? 0u : fp8x2<F == 2>(__fdiv_rn(x[i], s), __fdiv_rn(x[i + 1], s));
       w[i >> 2] |= u << (8 * (i & 2));
     }
   }
@@ -294,12 +296,18 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int cl, int ch, const 
   *reinterpret_cast<uint2*>(row + ch) = make_uint2(c.z, c.w);
 }
 
+// Scale of a block whose largest magnitude has the bits m; NaN where an element is not finite.
+__device__ __forceinline__ float block_scale_of(uint32_t m, float rqmax, int meta16) {
+  const float s = __fmul_rn(__uint_as_float(m), rqmax);
+  return m >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : meta16 ? f16_up(s) : s;
+}
+
 __device__ __forceinline__ float block_rqmax(int fmt) {  // the fp32 numbers nearest to 1 / qmax
   return fmt == KVQ_FP8_E4M3 ? 1.f / 448.f : fmt == KVQ_FP8_E5M2 ? 1.f / 57344.f : 1.f / 127.f;
 }
 
 struct FoldSmem {
-  float mk[kThreads / 32], mv[kThreads / 32];  // of either kernel's warps
+  uint32_t mk[kThreads / 32], mv[kThreads / 32];  // of either kernel's warps
 };
 
 // Quantize block [t0, t0 + G) of one head.  Whole CTA; ends with a barrier, so the window
@@ -310,7 +318,7 @@ __device__ void fold_block(const KvqView& v, const BlockAppend& a, FoldSmem& sm,
   const int np = v.D / kCh, lp = __ffs(np) - 1, G = v.kgroup, items = G << lp;
   const bool held = items <= N * NT;
   Item<BF16> k[N], w[N];
-  float mk = 0.f, mv = 0.f;
+  uint32_t mk = 0u, mv = 0u;
   for (int base = 0; base < items; base += N * NT) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -324,15 +332,12 @@ __device__ void fold_block(const KvqView& v, const BlockAppend& a, FoldSmem& sm,
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      mk = fmaxf(mk, item_absmax<BF16>(k[j]));
-      mv = fmaxf(mv, item_absmax<BF16>(w[j]));
+      mk = max(mk, item_absmax<BF16>(k[j]));
+      mv = max(mv, item_absmax<BF16>(w[j]));
     }
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-  }
+  mk = __reduce_max_sync(0xffffffffu, mk);
+  mv = __reduce_max_sync(0xffffffffu, mv);
   if ((threadIdx.x & 31) == 0) {
     sm.mk[threadIdx.x >> 5] = mk;
     sm.mv[threadIdx.x >> 5] = mv;
@@ -340,14 +345,10 @@ __device__ void fold_block(const KvqView& v, const BlockAppend& a, FoldSmem& sm,
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NT / 32; ++i) {
-    mk = fmaxf(mk, sm.mk[i]);
-    mv = fmaxf(mv, sm.mv[i]);
+    mk = max(mk, sm.mk[i]);
+    mv = max(mv, sm.mv[i]);
   }
-  float ks = __fmul_rn(mk, block_rqmax(v.kfmt)), vs = __fmul_rn(mv, block_rqmax(v.vfmt));
-  if (v.meta16) {
-    ks = f16_up(ks);
-    vs = f16_up(vs);
-  }
+  const float ks = block_scale_of(mk, block_rqmax(v.kfmt), v.meta16), vs = block_scale_of(mv, block_rqmax(v.vfmt), v.meta16);
   const float kr = ks > 0.f ? __frcp_rn(ks) : 0.f, vr = vs > 0.f ? __frcp_rn(vs) : 0.f;
   if (threadIdx.x == 0) {
     uint8_t* page = page_of(v, b, t0);

@@ -95,12 +95,13 @@ __global__ void __launch_bounds__(kPT) query_plain_kernel(KvqView v, QueryArgs a
       float mx = s;
       for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
       const float m = fmaxf(ms[r], mx);
+      const bool seen = lane < nt && okt[lane] && t0 + lane < ends[r];
       const float p = s == -INFINITY ? 0.f : exp2f(s - m);
       float sum = p;
       for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
       const float alpha = m == -INFINITY ? 1.f : exp2f(ms[r] - m);
       __syncwarp();
-      ps[r][lane] = p;
+      ps[r][lane] = seen ? p : -1.f;
       if (lane == 0) {
         al[r] = alpha;
         ls[r] = ls[r] * alpha + sum;
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(kPT) query_plain_kernel(KvqView v, QueryArgs a
         float s = o[r][j] * alpha;
         for (int tt = 0; tt < nt; ++tt) {
           const float p = ps[r][tt];
-          if (p != 0.f) s = fmaf(p, kv[tt][c], s);  // a token without weight adds nothing, whatever it holds
+          if (!(p < 0.f)) s = fmaf(p, kv[tt][c], s);  // a token that the row does not see adds nothing, whatever it holds
         }
         o[r][j] = s;
       }
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kPT) query_plain_kernel(KvqView v, QueryArgs a
 #pragma unroll
   for (int r = 0; r < kPRows; ++r) {
     if (r >= rows) break;
-    const float inv = ls[r] > 0.f ? 1.f / ls[r] : 0.f;
+    const float inv = ls[r] == 0.f ? 0.f : 1.f / ls[r];  // NaN stays
 #pragma unroll
     for (int j = 0; j < kMaxHeadDim / kPT; ++j) {
       const int c = threadIdx.x + j * kPT;

@@ -91,9 +91,8 @@
  *               1/57344 (E5M2).  Keys and values
  *               are PER_BLOCK together, with one `group`; their formats may
  *               differ.  Source tensors and windows are 16-byte aligned.
- *               A non-finite key or value makes its block's scale, and with it
- *               the outputs of the queries that see the block, meaningless; the
- *               queries of the same call that do not see it may be affected too.
+ *               A block with an element that is not finite has the scale NaN and
+ *               codes 0: all of its tokens read as NaN (x^ = c*s).
  *
  * Residual window (`residual` = R tokens, per sequence and kv-head): new
  * tokens are written unquantized (source dtype) into the window; when an
@@ -326,8 +325,11 @@ size_t kvq_query_workspace_bytes(const kvq_config* cfg, int32_t batch, int32_t n
  * out: [batch][n_q][Hq][D] device, src dtype (rounded once, to nearest even);
  * rows at or beyond n_q_per_seq[b] are left as they were.  A query that sees no
  * token (an empty cache, or more queries than tokens under the causal mask) gets
- * zeros.  A key or value that is not finite makes NaN of the rows that see its token (of
- * that channel or of all) and leaves the others as they are.  softmax_scale: 0 means 1/sqrt(D).  workspace: as for
+ * zeros.  A key or value that is not finite enters the softmax and the sums of the
+ * queries that see its token as it is: NaN, and an infinite value, make their outputs
+ * NaN or infinite, in that channel or in all; an infinite key has the weight of its
+ * logit (none for -inf).  Queries that do not see the token are not affected by it.
+ * softmax_scale: 0 means 1/sqrt(D).  workspace: as for
  * kvq_decode_attention, kvq_query_workspace_bytes(cfg, batch, n_q) bytes.
  * Every configuration is taken.  PER_BLOCK caches with bf16 sources run on
  * tensor cores; every other configuration runs on a plain kernel of fp32

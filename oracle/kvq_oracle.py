@@ -428,6 +428,7 @@ def _quant_k_channel(x, spec: QSpec, meta16=False):
 def _quant_block(x, spec: QSpec, meta16=False):
     """One scale per block of G consecutive tokens: x [n, D], n % G == 0.
 
+    A block with an element that is not finite has the scale NaN and codes 0.
     Returns (codes [n, D] (FP8: bytes), scales [n/G], None)."""
     n, D = x.shape
     xg = x.reshape(n // spec.group, spec.group * D)
@@ -435,12 +436,14 @@ def _quant_block(x, spec: QSpec, meta16=False):
     s = fl32(a * fl32(1.0 / (fp8_max(spec.fmt) if is_fp8(spec.fmt) else 127.0)))
     if meta16:
         s = f16_up(s)
+    bad = ~np.isfinite(a)
+    xg, s = np.where(bad, 0.0, xg), np.where(bad, 1.0, s)
     if is_fp8(spec.fmt):
         c = quant_fp8(xg, s, spec.fmt)
     else:
         with np.errstate(divide="ignore", invalid="ignore"):
             c = np.where(s == 0.0, 0.0, np.clip(np.rint(fl32(xg / s)), -127, 127)).astype(np.int64)
-    return c.reshape(n, D), s[:, 0], None
+    return c.reshape(n, D), np.where(bad, np.nan, s)[:, 0], None
 
 
 def _dequant_block(c, s, spec: QSpec):

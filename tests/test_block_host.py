@@ -252,3 +252,19 @@ def test_broadcast_rows_are_refused(K):
                  (z(4, 9, 2, 64), z(4, 8, 2, 64)), (z(4, 9, 2, 64).float(), z(4, 9, 2, 64)), (z(3, 9, 2, 64), z(3, 9, 2, 64))):
         with pytest.raises(ValueError):
             c.append(k, v)
+
+
+@pytest.mark.parametrize("fmt", [O.INT8, O.FP8_E4M3, O.FP8_E5M2])
+@pytest.mark.parametrize("m16", [False, True])
+def test_block_quantizer_of_values_that_are_not_finite(fmt, m16):
+    x = np.random.default_rng(5).standard_normal((64, 64))
+    spec = O.QSpec(fmt, S, BLK, 16)
+    want, ws, _ = O._quant_block(x, spec, m16)
+    for bad in (np.nan, np.inf, -np.inf):
+        y = x.copy()
+        y[20, 3], y[63, 63] = bad, bad
+        c, s, _ = O._quant_block(y, spec, m16)
+        assert np.isnan(s).tolist() == [False, True, False, True] and s[0] == ws[0] and s[2] == ws[2]
+        assert not c[16:32].any() and not c[48:].any()
+        assert np.array_equal(c[:16], want[:16]) and np.array_equal(c[32:48], want[32:48])
+        assert np.isnan(O._dequant_block(c, s, spec)).reshape(4, -1).all(1).tolist() == [False, True, False, True]

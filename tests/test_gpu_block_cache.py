@@ -902,3 +902,53 @@ def test_missing_page_of_a_blocks_scales(kind):
                 ref, size = O.query_attention(q[0, :, 4 * h:4 * h + 4], Kd[keep], Vd[keep], False)
                 lim = half * np.abs(ref) + 2.0 ** -10 * size + 2.0 ** -25 * np.abs(Vd).sum(0)
                 assert np.all(np.abs(got[0, :, 4 * h:4 * h + 4] - ref) <= lim), (n, h)
+
+
+@pytest.mark.parametrize("bad", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("kind", [I8, E4, E5, "f32", "meta16"])
+def test_not_finite_through_an_append(kind, bad):
+    """A block that gets a value that is not finite reads as NaN, every other block as without it; queries that see a
+    token of the block are NaN, those that do not are within the bound of the exact output: on the plain kernel (fp32
+    sources), the few-row and the many-row one."""
+    fmt = kind if kind in (I8, E4, E5) else I8
+    cfg = cfg_of(8, 2, 128, fmt, fmt, 32, 64, 32, src=O.F32 if kind == "f32" else O.BF16,
+                 meta_dtype=O.F16 if kind == "meta16" else O.F32)
+    T, x, half = 300, float(bad), 2.0 ** -24 if kind == "f32" else 2.0 ** -8
+    g = np.random.default_rng(3)
+    rows = lambda: [[O.bf16(g.standard_normal((T, 128))) for _ in range(2)] for _ in range(3)]
+    Ks, Vs = rows(), rows()
+    Ks[0][1][250, 7] = x          # a key in tokens 224 .. 255: sequence 0, head 1
+    Vs[1][0][131, 100] = x        # a value in tokens 128 .. 159: sequence 1, head 0
+    Vs[2][1][290, 9] = x          # a value in the window: sequence 2, head 1
+    c = Case(cfg, [T] * 3, seed=1, streams=(Ks, Vs))
+    block = {(0, 1): (224, 256), (1, 0): (128, 160)}
+    deq = []
+    for b in range(3):
+        k, v = (t.double().cpu().numpy() for t in c.cache.dequantize(b, 0, T))
+        for h in range(2):
+            Kd, Vd = O.dequantize_stream(cfg, c.states[b][h])
+            np.testing.assert_array_equal(k[:, h], Kd)
+            np.testing.assert_array_equal(v[:, h], Vd)
+            deq.append((b, h, Kd, Vd))
+            if (b, h) in block:
+                lo, hi = block[b, h]
+                assert np.isnan((Kd if b == 0 else Vd)[lo:hi]).all()
+                assert np.isfinite(np.delete(Kd if b == 0 else Vd, np.s_[lo:hi], 0)).all()
+    for n in (1, 5, 200):
+        q = O.bf16(g.standard_normal((3, n, 8, 128)))
+        for cache in (c.cache, widened(c, 1 << 21).cache):
+            got = cache.query_attention(torch_src(q, cfg)).double().cpu().numpy()
+            for b, h, Kd, Vd in deq:
+                y, end = got[b, :, 4 * h:4 * h + 4], T - n + 1 + np.arange(n)
+                first = block[b, h][0] if (b, h) in block else 290 if (b, h) == (2, 1) else T
+                sees = end > first
+                if (b, h) == (2, 1):
+                    assert not np.isfinite(y[sees, :, 9]).any()
+                else:
+                    assert np.isnan(y[sees]).all(), (b, h, n)
+                if not sees.all():
+                    m = int((~sees).sum())
+                    ref, size = O.query_attention(q[b, :m, 4 * h:4 * h + 4], Kd[:end[m - 1]], Vd[:end[m - 1]], True)
+                    lim = half * np.abs(ref) + 2.0 ** -10 * size + 2.0 ** -25 * np.abs(Vd[:end[m - 1]]).sum(0)
+                    assert np.all(np.abs(y[:m] - ref) <= lim), (b, h, n)
+    assert int(c.cache.status.item()) == 0
