@@ -43,13 +43,21 @@ __device__ __forceinline__ uint32_t bf16x2_absmax(uint32_t m, uint32_t u) {  // 
   asm("max.u16x2 %0, %1, %2;\n" : "=r"(r) : "r"(m), "r"(a));
   return r;
 }
+__device__ __forceinline__ uint32_t bf16x2_min(uint32_t a, uint32_t b) {  // of magnitudes, as bits
+  uint32_t r;
+  asm("min.u16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // The same of finite magnitudes, as bits + 0x80: infinities and NaN wrap to the bottom (a token that a row does not see
 // then leaves the scaling of those it sees alone).
 __device__ __forceinline__ uint32_t bf16x2_finite_max(uint32_t m, uint32_t u) {
   return bf16x2_absmax(m, (u & 0x7fff7fffu) + 0x00800080u);
 }
-__device__ __forceinline__ uint32_t finite_top(uint32_t m) {  // of the warp
-  return max(__reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16)), 0x80u) - 0x80u;
+__device__ __forceinline__ uint32_t finite_top(uint32_t m) {  // the larger of the two
+  return max(max(m & 0xffffu, m >> 16), 0x80u) - 0x80u;
+}
+__device__ __forceinline__ uint32_t chunk_top(const uint4& x) {  // largest finite magnitude of 8 values
+  return finite_top(bf16x2_finite_max(bf16x2_finite_max(bf16x2_finite_max(bf16x2_finite_max(0u, x.x), x.y), x.z), x.w));
 }
 // Numbers that are not finite have all exponent bits set (E4M3: and all of the mantissa's): one more in the lowest of
 // these carries into the sign's place.
@@ -65,6 +73,8 @@ __device__ __forceinline__ int norm_exponent(uint32_t top) {
   const int k = exponent_of(__uint_as_float(top << 16)) - 8;
   return top == 0 ? 0 : max(-126, min(k, 119));
 }
+// The same for values, whose exponent rides in the softmax's.
+__device__ __forceinline__ int value_exponent(uint32_t top) { return max(kMinExp, norm_exponent(top)); }
 __device__ __forceinline__ void norm_factors(uint32_t top, float& down, float& up) {
   const int k = norm_exponent(top);
   down = pow2i(-k);

@@ -11,7 +11,7 @@
 // the products that enter the tensor cores stay near 1 whatever the scales are; M is
 // raised only when a tile exceeds it by 2^8 (p f then stays below 2^9, inside f16).
 // The operands are exact: every code is an f16 number, and a bf16 query row is one after
-// scaling by a power of two (elements more than 2^-32 below the row's largest drop bits).
+// scaling by a power of two (elements more than 2^25 below the row's largest drop bits).
 // p f is rounded to f16 once (bf16 output: 2^-11 against the output's own 2^-8), or split
 // in two f16 terms for fp32 output.
 //
@@ -22,7 +22,8 @@
 // values, transposed on the way from shared memory, that of the second product (16
 // channels x 8 rows); with more rows a converted operand serves up to four products.  p
 // crosses from one layout to the other with movmatrix.  The window's tokens (bf16) take the
-// same path from registers, scaled by a power of two per tile.  All work lies in one row
+// same path from registers, each scaled by a power of two of its own: a shared one would let
+// a large token take bits from tokens whose queries do not see it.  All work lies in one row
 // that is cut into equal runs, one a warp or up to four; a second kernel merges a row's
 // records.
 //
@@ -413,19 +414,18 @@ __global__ void __launch_bounds__(kFThreads, few_ctas<D, NB>())
     }
 
     // logits of the tile at token tok (acc: token g / g + 8 x row 2t / 2t + 1) -> B operands of the second
-    // product; kf, vf: scale of the keys, and of the values as 2^e f
-    auto softmax = [&](const float (&acc)[NB][4], int tok, float kf, int e, float f, uint32_t (&ph)[NB][2],
+    // product; scale of the keys, and of the values as 2^e f, of tokens g (kf0, e0) and g + 8
+    auto softmax = [&](const float (&acc)[NB][4], int tok, float kf0, float kf1, int e0, int e1, float f, uint32_t (&ph)[NB][2],
                        uint32_t (&pl)[NB][2]) {
-      const float fe = (float)e, ie = pow2i(-e);
+      const float fe0 = (float)e0, fe1 = (float)e1, ie0 = pow2i(-e0), ie1 = pow2i(-e1);
       float x[NB][2][2];  // [block][token g / g + 8][row]
       bool need = false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float c = kf * fct[nb][r];
-          x[nb][0][r] = tok + g < end[nb][r] ? fmaf(acc[nb][r], c, fe) : -INFINITY;
-          x[nb][1][r] = tok + g + 8 < end[nb][r] ? fmaf(acc[nb][2 + r], c, fe) : -INFINITY;
+          x[nb][0][r] = tok + g < end[nb][r] ? fmaf(acc[nb][r], kf0 * fct[nb][r], fe0) : -INFINITY;
+          x[nb][1][r] = tok + g + 8 < end[nb][r] ? fmaf(acc[nb][2 + r], kf1 * fct[nb][r], fe1) : -INFINITY;
           need = need || fmaxf(x[nb][0][r], x[nb][1][r]) > m_run[nb][r] + kLazy;
         }
       if (__any_sync(0xffffffffu, need)) {
@@ -454,7 +454,8 @@ __global__ void __launch_bounds__(kFThreads, few_ctas<D, NB>())
         for (int r = 0; r < 2; ++r) {
           p[0][r] = ex2(x[nb][0][r] - m_run[nb][r]);
           p[1][r] = ex2(x[nb][1][r] - m_run[nb][r]);
-          l_run[nb][r] = fmaf(p[0][r] + p[1][r], ie, l_run[nb][r]);
+          l_run[nb][r] = e0 == e1 ? fmaf(p[0][r] + p[1][r], ie0, l_run[nb][r])
+                                  : fmaf(p[0][r], ie0, fmaf(p[1][r], ie1, l_run[nb][r]));
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(kFThreads, few_ctas<D, NB>())
         const int e = vf == 0.f ? 0 : min(126, max(kMinExp, exponent_of(vf)));
         const float f = vf * pow2i(-e);  // in [1, 2), or less below 2^kMinExp
         uint32_t ph[NB][2], pl[NB][2];
-        softmax(acc, tok, kf, e, f, ph, pl);
+        softmax(acc, tok, kf, kf, e, e, f, ph, pl);
         // ---- second product: rows g / g + 8 of channel tile m = channels g GC + 2m / + 1,
         //      k-slots = tokens 2t, 2t + 1, 2t + 8, 2t + 9
         constexpr int W = GC / 4;  // words of a value row a lane holds
@@ -576,18 +577,18 @@ __global__ void __launch_bounds__(kFThreads, few_ctas<D, NB>())
       }
     }
 
-    // ---- the window's tokens: bf16 rows, a power of two per tile in place of the scales
+    // ---- the window's tokens: bf16 rows, a power of two per token in place of the scales
     for (int i = qtiles; i < tiles; ++i) {
       const int tok = t0 + i * kTile;
       const uint16_t* kw = static_cast<const uint16_t*>(v.k_win) + (((long long)b * v.R + (tok - nq)) * v.Hkv + h) * D;
       const uint16_t* vw = static_cast<const uint16_t*>(v.v_win) + (((long long)b * v.R + (tok - nq)) * v.Hkv + h) * D;
       const long long pitch = (long long)v.Hkv * D;
       const uint4 z4 = make_uint4(0u, 0u, 0u, 0u);
-      float acc[NB][4], down, kf, f;
+      float acc[NB][4], kf0, kf1;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
       {
-        uint32_t x0[LC / 2], x1[LC / 2], m2 = 0u;
+        uint32_t x0[LC / 2], x1[LC / 2], m0 = 0u, m1 = 0u;
 #pragma unroll
         for (int c = 0; c < LC / 8; ++c) {
           const uint4 y0 = tok + g < t1 ? *reinterpret_cast<const uint4*>(kw + g * pitch + t * LC + 8 * c) : z4;
@@ -596,12 +597,24 @@ __global__ void __launch_bounds__(kFThreads, few_ctas<D, NB>())
           x1[4 * c] = y1.x; x1[4 * c + 1] = y1.y; x1[4 * c + 2] = y1.z; x1[4 * c + 3] = y1.w;
         }
 #pragma unroll
-        for (int c = 0; c < LC / 2; ++c) m2 = bf16x2_finite_max(bf16x2_finite_max(m2, x0[c]), x1[c]);
-        norm_factors(finite_top(m2), down, kf);
+        for (int c = 0; c < LC / 2; ++c) {
+          m0 = bf16x2_finite_max(m0, x0[c]);
+          m1 = bf16x2_finite_max(m1, x1[c]);
+        }
+        m0 = finite_top(m0);
+        m1 = finite_top(m1);
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {  // over the four lanes of a row
+          m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+          m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+        }
+        float down0, down1;
+        norm_factors(m0, down0, kf0);
+        norm_factors(m1, down1, kf1);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          const uint32_t a0 = bf16x2_scaled(x0[2 * s], down), a1 = bf16x2_scaled(x1[2 * s], down);
-          const uint32_t a2 = bf16x2_scaled(x0[2 * s + 1], down), a3 = bf16x2_scaled(x1[2 * s + 1], down);
+          const uint32_t a0 = bf16x2_scaled(x0[2 * s], down0), a1 = bf16x2_scaled(x1[2 * s], down1);
+          const uint32_t a2 = bf16x2_scaled(x0[2 * s + 1], down0), a3 = bf16x2_scaled(x1[2 * s + 1], down1);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
             const uint2 b2 = query(nb, s);
@@ -610,7 +623,7 @@ __global__ void __launch_bounds__(kFThreads, few_ctas<D, NB>())
         }
       }
       constexpr int W = GC / 2;  // bf16 pairs of a value row a lane holds
-      uint32_t wv[4][W], m2 = 0u;
+      uint32_t wv[4][W], exps = 0u;  // exponents of the four rows, a byte each
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int r = 2 * t + (j & 1) + 8 * (j >> 1);
@@ -619,19 +632,25 @@ __global__ void __launch_bounds__(kFThreads, few_ctas<D, NB>())
           const uint4 x = tok + r < t1 ? *reinterpret_cast<const uint4*>(vw + r * pitch + g * GC + 8 * c) : z4;
           wv[j][4 * c] = x.x; wv[j][4 * c + 1] = x.y; wv[j][4 * c + 2] = x.z; wv[j][4 * c + 3] = x.w;
         }
+        uint32_t m2 = 0u;
 #pragma unroll
         for (int c = 0; c < W; ++c) m2 = bf16x2_finite_max(m2, wv[j][c]);
+        m2 = finite_top(m2);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) m2 = max(m2, __shfl_xor_sync(0xffffffffu, m2, o));  // over the row's eight lanes
+        exps |= (uint32_t)(value_exponent(m2) & 0xff) << (8 * j);
       }
       if (__builtin_expect(tok + kTile > all_see, 0)) drop_not_finite(wv, tok, bad_from);
-      norm_factors(finite_top(m2), down, f);
-      const int e = max(kMinExp, exponent_of(f));
-      f *= pow2i(-e);
+      const uint32_t mine = __shfl_sync(0xffffffffu, exps, g >> 1) >> (8 * (g & 1));  // of tokens g, g + 8
       uint32_t ph[NB][2], pl[NB][2];
-      softmax(acc, tok, kf, e, f, ph, pl);
+      softmax(acc, tok, kf0, kf1, (int8_t)mine, (int8_t)(mine >> 16), 1.f, ph, pl);
+      float down[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) down[j] = pow2i(-(int8_t)(exps >> (8 * j)));
 #pragma unroll
       for (int m = 0; m < NS; ++m) {  // channels g GC + 2m, + 1 are pair m of each row
-        const uint32_t y0 = bf16x2_scaled(wv[0][m], down), y1 = bf16x2_scaled(wv[1][m], down);
-        const uint32_t y2 = bf16x2_scaled(wv[2][m], down), y3 = bf16x2_scaled(wv[3][m], down);
+        const uint32_t y0 = bf16x2_scaled(wv[0][m], down[0]), y1 = bf16x2_scaled(wv[1][m], down[1]);
+        const uint32_t y2 = bf16x2_scaled(wv[2][m], down[2]), y3 = bf16x2_scaled(wv[3][m], down[3]);
         const uint32_t a0 = prmt(y0, y1, 0x5410u), a1 = prmt(y0, y1, 0x7632u);
         const uint32_t a2 = prmt(y2, y3, 0x5410u), a3 = prmt(y2, y3, 0x7632u);
 #pragma unroll

@@ -24,6 +24,11 @@
 // With more than 128 rows a unit is 256 rows, one half a stream, over the same tiles;
 // with fewer the streams take every other tile of one half and are joined at the end.
 //
+// A 16-token piece of the window has one power of two for its keys and one for its values, as long as its tokens lie
+// within 2^12 of one another.  Where they may not, a shared one would take bits from the smaller tokens, and so let a
+// token change the outputs of queries that do not see it: each token then has its own, in a table of the workspace that
+// the softmax reads.  It comes to know of it by an infinite scale, which sends the tile the way of a new maximum.
+//
 // Work split: units (sequence, kv-head, 256 or 128 rows) laid end to end as tiles; every CTA
 // takes an equal run of them, whatever the lengths are, so that all SMs finish together.
 // A unit cut by such a boundary leaves fp32 partial records, which a second kernel merges.
@@ -52,6 +57,8 @@ constexpr int kConv0 = kSoftWarps, kConvWarps = 4, kLoadWarp = kConv0 + kConvWar
 constexpr int kMThreads = (kMmaWarp + 2) * 32;
 constexpr int kBarStream = 1, kBarJoin = 3;  // named barriers: of the streams (and the next), of both
 constexpr int kSlots = 8;     // tiles whose scales are kept
+constexpr int kFarSlots = 4;  // tiles whose tokens' exponents are kept (the converters are two ahead of the softmax at most)
+constexpr int kFarSpan = 12;  // exponents that a piece's tokens may span with one power of two (2^-21 of a token's largest lost)
 constexpr int kSegs = 8;      // segments that are told of
 constexpr float kLazyM = 256.f;  // a piece's weights may sum to this before the maximum is raised
 constexpr float kMinitM = -1e30f;
@@ -91,7 +98,7 @@ struct Seg {
 struct Misc {
   // of each piece: key scale, log2 of the value scale (-inf: it has no tokens to see), 1 / value scale
   float4 scale[kSlots][kPieces];
-  uint32_t skip_k[kSlots];      // pieces to fill with zeros
+  uint32_t skip_k[kSlots];      // pieces to fill with zeros; from bit 8: pieces whose tokens have exponents of their own
   uint32_t skip_v[kSlots];
   uint64_t raw_k_full[2], raw_v_full[2], raw_k_empty[2], raw_v_empty[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
@@ -336,6 +343,16 @@ __device__ __forceinline__ uint32_t tile_chunk(int r, int c) {
   return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+__host__ __device__ inline size_t many_rec_bytes(int D, int RT) { return (size_t)RT * (D + 4) * sizeof(float); }
+// The workspace: the CTAs' record headers, their tables of exponents, their records.
+__host__ __device__ inline size_t many_far_bytes() { return (size_t)kFarSlots * kTok * sizeof(int2); }  // of a CTA
+__host__ __device__ inline size_t many_far_offset(int grid) { return ((size_t)grid * 2 * sizeof(RecHeader) + 255) / 256 * 256; }
+__host__ __device__ inline size_t many_header_bytes(int grid) { return many_far_offset(grid) + (size_t)grid * many_far_bytes(); }
+// Table of a tile's exponents.
+__device__ __forceinline__ int2* far_table(unsigned char* ws, uint32_t it) {
+  return reinterpret_cast<int2*>(ws + many_far_offset(gridDim.x) + blockIdx.x * many_far_bytes()) + it % kFarSlots * kTok;
+}
+
 // ---- converter: K pieces of 16 tokens of a raw tile, 4 pieces apart, -> f16 (whole warp).  A lane takes 8 codes
 // of a row, one 16-byte chunk of the tile: eight lanes' loads and stores then meet no bank twice.
 template <int F, int D, int K>
@@ -379,35 +396,119 @@ __device__ __noinline__ void zero_piece(uint8_t* dst, int piece, int lane) {
   for (int i = lane; i < 16 * (D / 8); i += 32)
     *reinterpret_cast<uint4*>(dst + tile_chunk(16 * piece + i / (D / 8), i % (D / 8))) = make_uint4(0u, 0u, 0u, 0u);
 }
-// 16 window rows from token tok (those before T; zeros behind), scaled by 2^-k with k their common exponent.
-// write == false: only the exponent.
+// Window rows of a piece of 16 tokens from tok on, those before T (the last one in place of those behind, so that loads
+// need no branch and are in flight together).  A lane has the same chunk of every RPI-th row.
+template <int D>
+struct WindowRows {
+  static constexpr int CPR = D / 8, RPI = 32 / CPR, N = 16 / RPI;
+  const uint16_t* src;
+  long long pitch;
+  int r0, n;
+  __device__ __forceinline__ WindowRows(const void* win, const KvqView& v, int b, int h, int tok, int T, int nq, int lane)
+      : pitch((long long)v.Hkv * D), r0(lane / CPR), n(T - tok) {
+    src = static_cast<const uint16_t*>(win) + (((long long)b * v.R + (tok - nq)) * v.Hkv + h) * D + 8 * (lane % CPR);
+  }
+  __device__ __forceinline__ uint4 load(int i) const {
+    return *reinterpret_cast<const uint4*>(src + min(r0 + i * RPI, n - 1) * pitch);
+  }
+  __device__ __forceinline__ bool has(int i) const { return r0 + i * RPI < n; }
+};
+// Loops over them are short code, with four loads in flight: what a unit's few window pieces wait for is instructions
+// that no cache holds.
+
+// Whether two of the rows lie further apart than one power of two serves (top: the largest magnitude).
+template <int D>
+__device__ __noinline__ bool rows_apart(const WindowRows<D> w, uint32_t top) {
+  bool apart = false;
+#pragma unroll 1
+  for (int i = 0; i < w.N; ++i) {
+    uint32_t m = chunk_top(w.load(i));
+#pragma unroll
+    for (int o = w.CPR / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    apart = apart || (m && value_exponent(m) < value_exponent(top) - kFarSpan);  // zeros go with any
+  }
+  return __any_sync(0xffffffffu, apart);
+}
+// The rows scaled by 2^-k with k their common exponent (zeros behind the last).  write == false: only the exponent.
+// kFarBit is added to it where rows are too far apart for that.
+constexpr int kFarBit = 1024;
 template <int D>
 __device__ __noinline__ int window_piece(const void* win, const KvqView& v, int b, int h, int tok, int T, int nq, uint8_t* dst,
                                             int piece, int lane, bool write) {
-  constexpr int CPR = D / 8, RPI = 32 / CPR, N = 16 / RPI;
-  uint4 x[N];
-  uint32_t m2 = 0u;
+  const WindowRows<D> w(win, v, b, h, tok, T, nq, lane);
+  uint32_t top = 0u, low = 0x7fff7fffu;
+#pragma unroll 1
+  for (int i = 0; i < w.N; i += 4) {
+    uint4 x[4];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int r = i * RPI + lane / CPR, c = lane % CPR;
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (tok + r < T)
-      x[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(win) +
-                                             (((long long)b * v.R + (tok + r - nq)) * v.Hkv + h) * D + 8 * c);
-    m2 = bf16x2_finite_max(bf16x2_finite_max(bf16x2_finite_max(bf16x2_finite_max(m2, x[i].x), x[i].y), x[i].z), x[i].w);
-  }
-  const int k = max(kMinExp, norm_exponent(finite_top(m2)));
-  if (write) {
-    const float down = pow2i(-k);
+    for (int j = 0; j < 4; ++j) x[j] = w.load(i + j);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int r = i * RPI + lane / CPR, c = lane % CPR;
-      *reinterpret_cast<uint4*>(dst + tile_chunk(16 * piece + r, c)) =
-          make_uint4(bf16x2_scaled(x[i].x, down), bf16x2_scaled(x[i].y, down), bf16x2_scaled(x[i].z, down),
-                     bf16x2_scaled(x[i].w, down));
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t m = bf16x2_finite_max(bf16x2_finite_max(bf16x2_finite_max(bf16x2_finite_max(0u, x[j].x), x[j].y), x[j].z), x[j].w);
+      top = bf16x2_absmax(top, m);
+      low = bf16x2_min(low, m);  // of some of a row: no more than the row's largest
     }
   }
-  return k;
+  top = finite_top(__reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)));
+  low = __reduce_min_sync(0xffffffffu, min(low & 0xffffu, low >> 16));
+  const int k = value_exponent(top);
+  if (write) {
+    const float down = pow2i(-k);
+#pragma unroll 1
+    for (int i = 0; i < w.N; i += 4) {
+      uint4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = w.load(i + j);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!w.has(i + j)) x[j] = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(dst + tile_chunk(16 * piece + w.r0 + (i + j) * w.RPI, lane % w.CPR)) =
+            make_uint4(bf16x2_scaled(x[j].x, down), bf16x2_scaled(x[j].y, down), bf16x2_scaled(x[j].z, down),
+                       bf16x2_scaled(x[j].w, down));
+      }
+    }
+  }
+  const bool near = low > 0x80u && value_exponent(low - 0x80u) >= k - kFarSpan;
+  return k + (top && !near && rows_apart<D>(w, top) ? kFarBit : 0);
+}
+// The same with a power of two for each row, whose exponents go to exps, two ints apart.  Seldom called.
+template <int D>
+__device__ __noinline__ void far_piece(const void* win, const KvqView& v, int b, int h, int tok, int T, int nq, uint8_t* dst,
+                                       int piece, int lane, bool write, int* exps) {
+  const WindowRows<D> w(win, v, b, h, tok, T, nq, lane);
+#pragma unroll 1
+  for (int i = 0; i < w.N; ++i) {
+    const int r = w.r0 + i * w.RPI, c = lane % w.CPR;
+    const uint4 x = w.has(i) ? w.load(i) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t top = chunk_top(x);
+#pragma unroll
+    for (int o = w.CPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int k = value_exponent(top);
+    const float down = pow2i(-k);
+    if (c == 0) exps[2 * r] = k;
+    if (write)
+      *reinterpret_cast<uint4*>(dst + tile_chunk(16 * piece + r, c)) =
+          make_uint4(bf16x2_scaled(x.x, down), bf16x2_scaled(x.y, down), bf16x2_scaled(x.z, down), bf16x2_scaled(x.w, down));
+  }
+}
+
+// Such a piece's keys, exponents and scale, and its values.
+template <int D>
+__device__ __noinline__ void far_keys(const KvqView& v, Misc& mi, const Seg& g, unsigned char* ws, uint32_t it, int tok, int piece,
+                                      uint8_t* dst) {
+  const int lane = threadIdx.x & 31, slot = it % kSlots;
+  int* tab = reinterpret_cast<int*>(far_table(ws, it) + 16 * piece);
+  far_piece<D>(v.k_win, v, g.b, g.h, tok, g.T, g.nq, dst, piece, lane, true, tab);
+  far_piece<D>(v.v_win, v, g.b, g.h, tok, g.T, g.nq, dst, piece, lane, false, tab + 1);
+  if (lane == 0) {
+    atomicOr(&mi.skip_k[slot], 1u << (8 + piece));
+    mi.scale[slot][piece] = make_float4(0.f, INFINITY, 0.f, 0.f);
+  }
+}
+template <int D>
+__device__ __noinline__ void far_values(const KvqView& v, const Seg& g, unsigned char* ws, uint32_t it, int tok, int piece, uint8_t* dst) {
+  far_piece<D>(v.v_win, v, g.b, g.h, tok, g.T, g.nq, dst, piece, threadIdx.x & 31, true,
+               reinterpret_cast<int*>(far_table(ws, it) + 16 * piece) + 1);
 }
 
 // A weight of zero would not keep a row from a value that is not finite.  So in tiles that some of the unit's rows do
@@ -529,6 +630,62 @@ __device__ __forceinline__ float half_weights(uint32_t tS, const float4* sc, flo
   return l;
 }
 
+// The same two steps for a tile with pieces (the bits of far) whose tokens have exponents of their own, in tab (of the
+// keys, of the values): the largest x, which takes the place of the logits, and then the weights, written over the first
+// 32 of the columns they come from; returns the sum of weight / value scale.  Seldom called.
+static __device__ __noinline__ float far_max(uint32_t tS, const Misc& mi, unsigned char* ws, uint32_t it, float fct, int lim) {
+  const int hf = (threadIdx.x >> 7) & 1, slot = it % kSlots;
+  const float4* sc = mi.scale[slot] + 4 * hf;
+  const int2* tab = far_table(ws, it) + 64 * hf;
+  const uint32_t far = mi.skip_k[slot] >> (8 + 4 * hf);
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[16];
+    tc::tmem_ld16(tS + 16 * c, r);
+    tc::wait_ld(r);
+    const float4 k = sc[c];
+    const bool own = (far >> c) & 1u;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int2 t = own ? tab[16 * c + e] : make_int2(0, 0);
+      const float kx = (own ? pow2i(t.x) : k.x) * fct, ky = own ? (float)t.y : k.y;
+      const float x = 16 * c + e < lim ? fmaf(__uint_as_float(r[e]), kx, ky) : -INFINITY;
+      mx = fmaxf(mx, x);
+      r[e] = __float_as_uint(x);
+    }
+    tc::tmem_st16(tS + 16 * c, r);
+  }
+  tc::wait_st();
+  return mx;
+}
+static __device__ __noinline__ float far_weights(uint32_t tS, const Misc& mi, unsigned char* ws, uint32_t it, float M) {
+  const int hf = (threadIdx.x >> 7) & 1, slot = it % kSlots;
+  const float4* sc = mi.scale[slot] + 4 * hf;
+  const int2* tab = far_table(ws, it) + 64 * hf;
+  const uint32_t far = mi.skip_k[slot] >> (8 + 4 * hf);
+  float l = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[16], pk[8];
+    tc::tmem_ld16(tS + 16 * c, r);
+    tc::wait_ld(r);
+    const float z = sc[c].z;
+    const bool own = (far >> c) & 1u;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float p = ex2(__uint_as_float(r[e]) - M);
+      l = fmaf(p, own ? pow2i(-tab[16 * c + e].y) : z, l);
+      r[e] = __float_as_uint(p);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) pk[e] = pack_f16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+    tc::tmem_st8(tS + 8 * c, pk);
+  }
+  tc::wait_st();
+  return l;
+}
+
 // Barrier of kThreads threads that also says whether any of them asks.
 template <int kThreads>
 __device__ __forceinline__ bool any_of(int bar, bool ask) {
@@ -540,9 +697,6 @@ __device__ __forceinline__ bool any_of(int bar, bool ask) {
       : "memory");
   return r != 0;
 }
-
-__host__ __device__ inline size_t many_rec_bytes(int D, int RT) { return (size_t)RT * (D + 4) * sizeof(float); }
-__host__ __device__ inline size_t many_header_bytes(int grid) { return ((size_t)grid * 2 * sizeof(RecHeader) + 255) / 256 * 256; }
 
 template <int F, int D>
 __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, QueryArgs a, unsigned char* ws, int RT) {
@@ -722,7 +876,11 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
           } else {
             const int kk = window_piece<D>(v.k_win, v, w.b, w.h, tok, w.T, w.nq, kd, piece, lane, true);
             const int kv = window_piece<D>(v.v_win, v, w.b, w.h, tok, w.T, w.nq, vd, piece, lane, false);
-            if (lane == 0) mi.scale[slot][piece] = make_float4(pow2i(kk), (float)kv, pow2i(-kv), 0.f);
+            if (max(kk, kv) >= kFarBit / 2) {
+              far_keys<D>(v, mi, mi.seg[(nseg - 1) % kSegs], ws, it, tok, piece, kd);
+            } else if (lane == 0) {
+              mi.scale[slot][piece] = make_float4(pow2i(kk), (float)kv, pow2i(-kv), 0.f);
+            }
           }
         }
         __syncwarp();
@@ -741,6 +899,8 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
             zero_piece<D>(vd, piece, lane);
           } else if (tok < w.nq) {
             convert_piece<F, D>(sm + L::raw_v(rs), vd, piece, lane);
+          } else if ((mi.skip_k[slot] >> (8 + piece)) & 1u) {
+            far_values<D>(v, mi.seg[(nseg - 1) % kSegs], ws, it, tok, piece, vd);
           } else {
             window_piece<D>(v.v_win, v, w.b, w.h, tok, w.T, w.nq, vd, piece, lane, true);
           }
@@ -897,7 +1057,9 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
             ok = false;
             break;
           }
-          const float mx = masked ? half_max<true>(tS, sc, fct, lim) : half_max<false>(tS, sc, fct, lim);
+          const uint32_t far = mi.skip_k[slot] >> 8;  // the same for the whole stream
+          const float mx = far ? far_max(tS, mi, ws, it0 + i, fct, lim)
+                           : masked ? half_max<true>(tS, sc, fct, lim) : half_max<false>(tS, sc, fct, lim);
           if (hf) *rx = mx;
           named_bar_sync(kBarStream + s, 2 * kRows);
           float mn = M;
@@ -921,7 +1083,13 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
               tc::tmem_st16(tO + c, r);
             }
           }
-          sum = masked ? half_weights<true>(tS, sc, fct, M, lim, pk, top) : half_weights<false>(tS, sc, fct, M, lim, pk, top);
+          if (far) {
+            sum = far_weights(tS, mi, ws, it0 + i, M);
+            tc::tmem_ld32(tS, pk);
+            tc::wait_ld(pk);
+          } else {
+            sum = masked ? half_weights<true>(tS, sc, fct, M, lim, pk, top) : half_weights<false>(tS, sc, fct, M, lim, pk, top);
+          }
         }
         any = true;
         l += sum;

@@ -952,3 +952,58 @@ def test_not_finite_through_an_append(kind, bad):
                     lim = half * np.abs(ref) + 2.0 ** -10 * size + 2.0 ** -25 * np.abs(Vd[:end[m - 1]]).sum(0)
                     assert np.all(np.abs(y[:m] - ref) <= lim), (b, h, n)
     assert int(c.cache.status.item()) == 0
+
+
+def oracle_limits(cfg, state, q, h, causal=True):
+    """Exact outputs of kv-head h's queries, and the bound of the file's head for each element."""
+    Kd, Vd = O.dequantize_stream(cfg, state)
+    heads = slice(h * cfg.n_rep, (h + 1) * cfg.n_rep)
+    ref, size = O.query_attention(q[:, heads].astype(np.float64), Kd, Vd, causal)
+    return ref, 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * size + 2.0 ** -25 * np.abs(Vd).sum(0)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("D,Hq,H,n", [(128, 8, 2, 5), (64, 16, 16, 21), (128, 16, 4, 70), (64, 4, 4, 300), (256, 8, 2, 9),
+                                      (128, 2, 1, 140)])
+def test_window_tokens_far_apart(D, Hq, H, n, wide):
+    """Finite keys and values of any size in the window.  Those of tokens that only later queries see leave the earlier
+    ones within the bound of the exact output; rows 2^40 and 2^45 times the others leave every query within it (a logit
+    2^40 times the others is off by more than they are large, but its weight is 0 or 1 whatever it is off by)."""
+    cfg = cfg_of(Hq, H, D, E4, E4, 64, 64, 64)
+    g, T = np.random.default_rng(6), 500          # 52 tokens in the window
+    big = float(np.frombuffer(np.uint32(0x7F7F0000).tobytes(), np.float32)[0])   # the largest bf16
+    q = O.bf16(g.standard_normal((1, n, Hq, D)))
+
+    def outputs(Ks, Vs):
+        c = Case(cfg, [T], seed=1, streams=([Ks], [Vs]))
+        got = (widened(c, 1 << 21) if wide else c).cache.query_attention(torch_src(q, cfg)).double().cpu().numpy()[0]
+        assert int(c.cache.status.item()) == 0
+        return c, got
+
+    def streams():
+        return tuple([O.bf16(g.standard_normal((T, D))) for _ in range(H)] for _ in range(2))
+    for large in (2.0 ** 40, big):
+        for first in (T - 2, T - 20):
+            if n <= T - first:
+                continue
+            Ks, Vs = streams()
+            for X, ch in ((Ks, 3), (Vs, D - 2)):
+                for x in X:
+                    x[first:, ch] = np.where(np.arange(T - first) % 2, large, -large)
+            c, got = outputs(Ks, Vs)
+            m = n - (T - first)                   # queries that see none of them
+            for h in range(H):
+                st = O.quantize_stream(cfg, Ks[h][:first], Vs[h][:first])
+                ref, lim = oracle_limits(cfg, st, q[0, :m], h)
+                assert np.all(np.abs(got[:m, h * cfg.n_rep:(h + 1) * cfg.n_rep] - ref) <= lim), (large, first, h)
+    for rows, which in (((470, 471), 0), ((475, 490), 1)):
+        for at in ((rows[0],), rows):
+            KV = streams()
+            for x in KV[which]:
+                for i, r in enumerate(at):
+                    x[r] *= 2.0 ** (40 + 5 * i)
+            c, got = outputs(*KV)
+            for h in range(H):
+                ref, lim = oracle_limits(cfg, c.states[0][h], q[0], h)
+                assert np.all(np.abs(got[:, h * cfg.n_rep:(h + 1) * cfg.n_rep] - ref) <= lim), (which, at, h)
+            c.check_attention()
