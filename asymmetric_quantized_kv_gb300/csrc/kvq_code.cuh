@@ -11,6 +11,8 @@ constexpr int kI8 = 0, kE4 = 1, kE5 = 2;  // formats as template arguments
 constexpr int fmt_index(int fmt) { return fmt == KVQ_INT8 ? kI8 : fmt == KVQ_FP8_E4M3 ? kE4 : kE5; }
 
 constexpr int kMinExp = -100;  // smallest value-scale exponent that rides in a softmax's (2^100 x 2^27 tokens stays finite)
+// Exponent of values that are all zero: far below that of any others, whose weights would lose bits to theirs.
+constexpr int kZeroExp = -32;
 
 // The four 8-bit codes of a word as two f16x2 (bytes 0, 1 and 2, 3).
 template <int F>
@@ -74,7 +76,7 @@ __device__ __forceinline__ int norm_exponent(uint32_t top) {
   return top == 0 ? 0 : max(-126, min(k, 119));
 }
 // The same for values, whose exponent rides in the softmax's.
-__device__ __forceinline__ int value_exponent(uint32_t top) { return max(kMinExp, norm_exponent(top)); }
+__device__ __forceinline__ int value_exponent(uint32_t top) { return top == 0 ? kZeroExp : max(kMinExp, norm_exponent(top)); }
 __device__ __forceinline__ void norm_factors(uint32_t top, float& down, float& up) {
   const int k = norm_exponent(top);
   down = pow2i(-k);

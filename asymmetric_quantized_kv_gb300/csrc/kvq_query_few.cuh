@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kFThreads, few_ctas<D, NB>())
 #pragma unroll
           for (int i4 = 0; i4 < 4; ++i4) acc[0][i4] += odd[i4];
         }
-        const int e = vf == 0.f ? 0 : min(126, max(kMinExp, exponent_of(vf)));
+        const int e = vf == 0.f ? kZeroExp : min(126, max(kMinExp, exponent_of(vf)));
         const float f = vf * pow2i(-e);  // in [1, 2), or less below 2^kMinExp
         uint32_t ph[NB][2], pl[NB][2];
         softmax(acc, tok, kf, kf, e, e, f, ph, pl);

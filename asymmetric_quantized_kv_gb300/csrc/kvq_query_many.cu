@@ -818,9 +818,9 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         uint32_t bad = p0.missing;
         if (lane < kPieces && p0.t0 + 16 * lane < p0.t1) {
           if (p0.scaled && !((bad >> lane) & 1u)) {
-            drop_v = p0.vs < pow2i(kMinExp);  // values below 2^-91: read as 0, weight 1
+            drop_v = p0.vs < pow2i(kMinExp);  // values below 2^-91: read as 0
             // (the third is finite for a scale of NaN too: rows that do not see the piece multiply it by 0)
-            sc = make_float4(p0.ks, drop_v ? 0.f : __log2f(p0.vs), drop_v ? 1.f : p0.vs > 0.f ? __frcp_rn(p0.vs) : 0.f, 0.f);
+            sc = make_float4(p0.ks, drop_v ? (float)kZeroExp : __log2f(p0.vs), drop_v ? pow2i(-kZeroExp) : p0.vs > 0.f ? __frcp_rn(p0.vs) : 0.f, 0.f);
           } else {
             bad |= 1u << lane;
           }

@@ -1007,3 +1007,26 @@ def test_window_tokens_far_apart(D, Hq, H, n, wide):
                 ref, lim = oracle_limits(cfg, c.states[0][h], q[0], h)
                 assert np.all(np.abs(got[:, h * cfg.n_rep:(h + 1) * cfg.n_rep] - ref) <= lim), (which, at, h)
             c.check_attention()
+
+
+@pytest.mark.parametrize("fmt", [E4, I8])
+def test_heavy_tokens_without_values(fmt):
+    """A token with most of the weight whose block's values are all zero (padding, a sink) leaves the others' weights
+    their bits: they all have 2^-17.5 of its weight, so that a rounding would go the same way in all of them."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(4, 2, 64, fmt, fmt, 32, 32, 32)
+    T, Bn = 970, 600                      # long runs: a warp's, and a unit's, hold the token and many others
+    Ks, Vs = ([np.zeros((T, 64)) for _ in range(2)] for _ in range(2))
+    for h in range(2):
+        Ks[h][5, 0] = 1.0
+        Vs[h][32:] = O.bf16(1.0 + np.random.default_rng(h).random((T - 32, 64)))
+    c = Case(cfg, [T], seed=3, streams=([Ks], [Vs]))
+    many = K.PagedKVCache.over(c.c_cfg, c.cache.pages, c.cache.block_table.repeat(Bn, 1), c.cache.seq_lens.repeat(Bn),
+                               c.cache.k_win.repeat(Bn, 1, 1, 1), c.cache.v_win.repeat(Bn, 1, 1, 1))
+    for n in (1, 6, 40):
+        q = np.zeros((1, n, 4, 64))
+        q[..., 0] = O.bf16(np.full((1, n, 4), 17.5 * np.log(2.0) * 8.0))
+        got = many.query_attention(torch_src(q, cfg).repeat(Bn, 1, 1, 1), causal=False).double().cpu().numpy()
+        for h in range(2):
+            ref, lim = oracle_limits(cfg, c.states[0][h], q[0], h, False)
+            assert np.all(np.abs(got[:, :, 2 * h:2 * h + 2] - ref) <= lim), (n, h)
