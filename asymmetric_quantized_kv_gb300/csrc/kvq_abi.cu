@@ -326,7 +326,7 @@ kvq_status kvq_query_attention(const kvq_config* c, const kvq_cache* cache, cons
   if (!q || !out || ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15))
     return KVQ_ERR_INVALID_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return KVQ_ERR_WORKSPACE;
-  if (ws_bytes < kvq::query_workspace_bytes(v, cache->batch, n_q)) return KVQ_ERR_WORKSPACE;
+  if (ws_bytes < kvq::query_call_bytes(v, cache->batch, n_q)) return KVQ_ERR_WORKSPACE;
   kvq::QueryArgs a;
   a.q = q;
   a.out = out;

@@ -82,7 +82,8 @@ kvq_status launch_block_append(const KvqView& v, const RopeView& r, const void* 
 kvq_status launch_rope_queries(const KvqView& v, const RopeView& r, const void* q, long long qs, int n_new,
                                const int32_t* n_new_per_seq, void* q_out, cudaStream_t st);
 // Attention of n_q queries per sequence.
-size_t query_workspace_bytes(const KvqView& v, int batch, int n_q);
+size_t query_workspace_bytes(const KvqView& v, int batch, int n_q);  // of calls of at most n_q queries
+size_t query_call_bytes(const KvqView& v, int batch, int n_q);       // of a call of n_q queries
 size_t decode_workspace_bytes(const KvqView& v, int batch);  // kvq_decode_attention over a PER_BLOCK cache
 kvq_status launch_query(const KvqView& v, const QueryArgs& a, void* ws, cudaStream_t st);
 kvq_status launch_dequantize(const KvqView& v, int seq, int t0, int t1, float* k_out,

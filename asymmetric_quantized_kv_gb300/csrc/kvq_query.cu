@@ -203,7 +203,8 @@ static size_t few_bytes(const KvqView& v, int batch, long long rows, int out_f32
   return few_header_bytes(batch) + (size_t)records * (v.D + 4) * sizeof(float);
 }
 
-size_t query_workspace_bytes(const KvqView& v, int batch, int n_q) {
+// What a call of n_q queries needs.
+size_t query_call_bytes(const KvqView& v, int batch, int n_q) {
   KvqView b = v;
   b.batch = batch;
   if (!query_tc_shape(b)) return 256;
@@ -212,6 +213,19 @@ size_t query_workspace_bytes(const KvqView& v, int batch, int n_q) {
   if (takes_few(v, batch, rows, 0, 1LL << 62)) return few;
   const size_t many = query_many_workspace_bytes(v, batch, n_q);
   return few > many ? few : many;
+}
+
+// What any call of at most n_q queries needs: the few-row kernel's records can take more than the many-row kernel's, and
+// up to kFewSmallRows rows may be the former's.
+size_t query_workspace_bytes(const KvqView& v, int batch, int n_q) {
+  size_t most = query_call_bytes(v, batch, n_q);
+  const int few = (kFewSmallRows + v.n_rep - 1) / v.n_rep;
+  static_assert(kFewPass * kFewPasses <= kFewSmallRows, "the most rows of the few-row kernel");
+  for (int n = 1; n < n_q && n <= few; ++n) {
+    const size_t x = query_call_bytes(v, batch, n);
+    if (x > most) most = x;
+  }
+  return most;
 }
 
 // A decode call's (fp32 output, in passes of 16 rows).

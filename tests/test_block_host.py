@@ -268,3 +268,12 @@ def test_block_quantizer_of_values_that_are_not_finite(fmt, m16):
         assert not c[16:32].any() and not c[48:].any()
         assert np.array_equal(c[:16], want[:16]) and np.array_equal(c[32:48], want[32:48])
         assert np.isnan(O._dequant_block(c, s, spec)).reshape(4, -1).all(1).tolist() == [False, True, False, True]
+
+
+@pytest.mark.parametrize("batch", [1, 3, 64, 600])
+@pytest.mark.parametrize("D,Hq,H", [(128, 32, 8), (64, 16, 16), (256, 8, 2), (128, 7, 1), (128, 64, 1)])
+def test_workspace_of_more_queries_serves_fewer(K, D, Hq, H, batch):
+    """The size is for calls of at most n_q queries, whichever kernel they take."""
+    cfg = _cfg(K, num_q_heads=Hq, num_kv_heads=H, head_dim=D)
+    sizes = [K.kvq_query_workspace_bytes(cfg, batch, n) for n in list(range(1, 300)) + [1000, 10000, 1 << 20]]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
