@@ -111,6 +111,18 @@ class PagedKVCache:
                              p(self.k_scale), p(self.v_scale), batch, max_pages_per_seq, self.n_pages,
                              p(self.status), p(self.rope_table), self.rope_positions)
 
+    def _empty(self, shape, dtype, stream):
+        """A new tensor, of the allocator's pool of the stream that is to write it: memory of the current stream's pool
+        may still be in use there."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self._device)
+        if not isinstance(stream, torch.cuda.Stream):
+            at = int(getattr(stream, "cuda_stream", stream))
+            stream = (torch.cuda.default_stream(self._device) if at < 2  # no stream, or the legacy one by name
+                      else torch.cuda.ExternalStream(at, device=self._device))
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self._device)
+
     # --- thin wrappers over the C ABI
     def append(self, k_new, v_new, n_new_per_seq=None, stream=None):
         """k_new, v_new: [batch, n_new, Hkv, D], dense."""
@@ -127,7 +139,7 @@ class PagedKVCache:
             raise ValueError(f"q must be contiguous {self._src} of shape {(self.batch, self._Hq, self._D)}")
         self._beside("q", q)
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+            out = self._empty(q.shape, torch.float32, stream)
         elif out.numel() != q.numel() or out.dtype != torch.float32 or not out.is_contiguous():
             raise ValueError("out must be contiguous float32 of q's shape")
         else:
@@ -169,7 +181,7 @@ class PagedKVCache:
         if q is not None:
             qs = self._rows("q", q, n, self._Hq)
             if q_out is None:
-                q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+                q_out = self._empty(q.shape, q.dtype, stream)
             elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous():
                 raise ValueError("q_out must be contiguous, of q's shape and dtype")
             else:
@@ -183,13 +195,14 @@ class PagedKVCache:
     def query_attention(self, q, causal=True, n_q_per_seq=None, out=None, softmax_scale=0.0, stream=None):
         """Attention of n_q queries per sequence, q [batch, n_q, Hq, D]: the sequence's newest n_q tokens over its
         own cache (causal), or a decoder's tokens over an encoder's states (causal=False).  The workspace grows
-        with n_q on first use and is kept; calls on several streams at once need a cache object each."""
+        with n_q on first use and is kept; calls on several streams at once need a cache object each, and an object
+        outlives the calls on other streams than its own."""
         cfg, n = self.cfg, q.shape[1]
         if q.shape != (self.batch, n, self._Hq, self._D) or q.dtype != self._src or not q.is_contiguous():
             raise ValueError(f"q must be contiguous {self._src} of shape {(self.batch, n, cfg.num_q_heads, cfg.head_dim)}")
         self._beside("q", q)
         if out is None:
-            out = torch.empty_like(q)
+            out = self._empty(q.shape, q.dtype, stream)
         elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
             raise ValueError("out must be contiguous, of q's shape and dtype")
         else:
@@ -201,7 +214,7 @@ class PagedKVCache:
             need = self._query_bytes[n] = B.kvq_query_workspace_bytes(cfg, self.batch, max(n, 1))
         if self.workspace.numel() < need:
             self._outgrown.append(self.workspace)  # a captured graph may still use it
-            self.workspace = torch.empty(need, dtype=torch.uint8, device=self.pages.device)
+            self.workspace = self._empty(need, torch.uint8, stream)
         if stream is None:
             stream = torch._C._cuda_getCurrentRawStream(self._index)
         B.kvq_query_attention(cfg, self.c, q, n, n_q_per_seq, B.KVQ_MASK_CAUSAL if causal else B.KVQ_MASK_NONE, out,
@@ -214,8 +227,7 @@ class PagedKVCache:
 
     def dequantize(self, seq, tok_begin, tok_end, stream=None):
         n = tok_end - tok_begin
-        k = torch.empty(n, self.cfg.num_kv_heads, self.cfg.head_dim, dtype=torch.float32, device=self.pages.device)
-        v = torch.empty_like(k)
+        k, v = (self._empty((n, self.cfg.num_kv_heads, self.cfg.head_dim), torch.float32, stream) for _ in range(2))
         B.kvq_dequantize(self.cfg, self.c, seq, tok_begin, tok_end, k, v, stream)
         return k, v
 

@@ -1030,3 +1030,28 @@ def test_heavy_tokens_without_values(fmt):
         for h in range(2):
             ref, lim = oracle_limits(cfg, c.states[0][h], q[0], h, False)
             assert np.all(np.abs(got[:, :, 2 * h:2 * h + 2] - ref) <= lim), (n, h)
+
+
+def test_new_tensors_belong_to_the_stream_that_writes_them():
+    """With a stream named, what a call allocates comes from that stream's pool, not from the current stream's, where
+    the memory may still be in use."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(8, 2, 128, E4, E4, 64, 64, 64)
+    _, tt = rope_setup(512, 128)
+    rope = K.make_rope(tt, 128)
+    cache = Case(cfg, [100, 70], seed=6, extra_pages=4).cache
+    x = torch.randn(2, 5, 12, 128, device="cuda").bfloat16()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream):
+        q = cache.append_rope(rope, x[:, :, :8], x[:, :, 8:10], x[:, :, 10:], stream=stream)
+        made = [q, cache.query_attention(q, stream=stream), cache.attention(q[:, 0].contiguous(), stream=stream),
+                *cache.dequantize(0, 0, 90, stream=stream)]
+        side.synchronize()
+        made.append(cache.workspace)          # grown by the first query_attention
+        where = [next(s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= t.data_ptr() < s["address"] + s["total_size"])
+                 for t in made]
+        assert where == [side.cuda_stream] * len(made)
+    assert cache.query_attention(q, stream=0).data_ptr() != 0
+    torch.cuda.synchronize()
+    assert int(cache.status.item()) == 0
