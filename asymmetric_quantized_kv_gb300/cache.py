@@ -214,7 +214,8 @@ class PagedKVCache:
             need = self._query_bytes[n] = B.kvq_query_workspace_bytes(cfg, self.batch, max(n, 1))
         if self.workspace.numel() < need:
             self._outgrown.append(self.workspace)  # a captured graph may still use it
-            self.workspace = self._empty(need, torch.uint8, stream)
+            # at least doubled, so that all of them together stay below the one in use
+            self.workspace = self._empty(max(need, 2 * self.workspace.numel()), torch.uint8, stream)
         if stream is None:
             stream = torch._C._cuda_getCurrentRawStream(self._index)
         B.kvq_query_attention(cfg, self.c, q, n, n_q_per_seq, B.KVQ_MASK_CAUSAL if causal else B.KVQ_MASK_NONE, out,

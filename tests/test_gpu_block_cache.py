@@ -1055,3 +1055,11 @@ def test_new_tensors_belong_to_the_stream_that_writes_them():
     assert cache.query_attention(q, stream=0).data_ptr() != 0
     torch.cuda.synchronize()
     assert int(cache.status.item()) == 0
+
+
+def test_outgrown_workspaces_stay_below_the_one_in_use():
+    cfg = cfg_of(2, 2, 128, E4, E4, 64, 64, 64)
+    cache = Case(cfg, [100], seed=6).cache
+    for n in range(1, 80):
+        cache.query_attention(torch.zeros(1, n, 2, 128, device="cuda").bfloat16())
+        assert sum(w.numel() for w in cache._outgrown) <= cache.workspace.numel()
