@@ -62,6 +62,8 @@ class PagedKVCache:
         """A cache over buffers that the caller owns: pages (n_pages * kvq_page_bytes bytes), block_table
         [batch, max_pages_per_seq] and seq_lens [batch] int32, and the residual windows [batch, R, Hkv, D] in
         the source dtype (None when R is 0).  All contiguous, on one device."""
+        if not pages.is_cuda:
+            raise ValueError("a cache's buffers are CUDA tensors")
         page = B.kvq_page_bytes(cfg)
         if pages.dtype != torch.uint8 or not pages.is_contiguous() or pages.numel() == 0 or pages.numel() % page:
             raise ValueError(f"pages must be contiguous uint8 of a multiple of {page} bytes")
@@ -175,6 +177,8 @@ class PagedKVCache:
         [batch, n_new, Hq, D] (or None) may be slices of one fused projection (rows of one token contiguous,
         tokens evenly spaced).  Returns the rotated queries."""
         n = k_new.shape[1]
+        if getattr(rope, "tensor", None) is not None:  # make_rope's
+            self._beside("cos_sin", rope.tensor)
         if n_new_per_seq is not None:
             self._counts("n_new_per_seq", n_new_per_seq)
         qs = 0
@@ -227,6 +231,7 @@ class PagedKVCache:
         return B.kvq_decode_kernel(self.cfg, self.c)
 
     def dequantize(self, seq, tok_begin, tok_end, stream=None):
+        self._beside("the cache", self.pages)
         n = tok_end - tok_begin
         k, v = (self._empty((n, self.cfg.num_kv_heads, self.cfg.head_dim), torch.float32, stream) for _ in range(2))
         B.kvq_dequantize(self.cfg, self.c, seq, tok_begin, tok_end, k, v, stream)
@@ -234,6 +239,8 @@ class PagedKVCache:
 
     def calibrate(self, k_src, v_src, k_qmax, v_qmax, stream=None):
         """Set the static per-head scales from [N, Hkv, D] source tensors."""
+        for name, t in (("k_src", k_src), ("v_src", v_src)):
+            self._beside(name, t)
         B.kvq_calibrate_absmax(self.cfg, k_src, k_src.shape[0], k_qmax, self.k_scale, stream)
         B.kvq_calibrate_absmax(self.cfg, v_src, v_src.shape[0], v_qmax, self.v_scale, stream)
 

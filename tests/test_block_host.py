@@ -277,3 +277,21 @@ def test_workspace_of_more_queries_serves_fewer(K, D, Hq, H, batch):
     cfg = _cfg(K, num_q_heads=Hq, num_kv_heads=H, head_dim=D)
     sizes = [K.kvq_query_workspace_bytes(cfg, batch, n) for n in list(range(1, 300)) + [1000, 10000, 1 << 20]]
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+def test_tables_and_buffers_off_the_device_are_refused(K):
+    """Host memory never reaches a kernel: the rotation's table, and the buffers of a cache."""
+    import torch
+    c = _object(K)
+    del c._beside
+    c._index, c._device = 0, torch.device("cuda:0")
+    k = torch.zeros(4, 1, 2, 64, dtype=torch.bfloat16)
+    rope = K.make_rope(torch.zeros(32, 64), 64)
+    with pytest.raises(ValueError, match="cos_sin must be on the cache's device"):
+        c.append_rope(rope, None, k, k)
+    cfg = _cfg(K)
+    buffers = dict(pages=torch.zeros(K.kvq_page_bytes(cfg), dtype=torch.uint8), block_table=torch.zeros(1, 1, dtype=torch.int32),
+                   seq_lens=torch.zeros(1, dtype=torch.int32))
+    buffers["k_win"], buffers["v_win"] = (torch.zeros(1, 64, 8, 128, dtype=torch.bfloat16) for _ in range(2))
+    with pytest.raises(ValueError, match="CUDA"):
+        K.PagedKVCache.over(cfg, **buffers)
