@@ -55,7 +55,7 @@ constexpr int kMaxUnits = kFewUnits;
 constexpr int kUnitTokens = 512;    // a warp takes several units only if they are this long
 constexpr int kMinUnit = 64;        // tokens of the smallest chunk
 constexpr float kLazy = 8.f;
-constexpr float kMinit = -1e30f;
+constexpr float kMinit = -3e38f;  // below any logit
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t r;

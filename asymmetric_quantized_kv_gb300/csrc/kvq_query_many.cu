@@ -61,7 +61,8 @@ constexpr int kFarSlots = 4;  // tiles whose tokens' exponents are kept (the con
 constexpr int kFarSpan = 12;  // exponents that a piece's tokens may span with one power of two (2^-21 of a token's largest lost)
 constexpr int kSegs = 8;      // segments that are told of
 constexpr float kLazyM = 256.f;  // a piece's weights may sum to this before the maximum is raised
-constexpr float kMinitM = -1e30f;
+constexpr float kMinitM = -3e38f;  // below any logit
+constexpr float kWideM = 1048576.f;  // x - M is one multiply-add, exact, where M is an x that was rounded: up to this, by 2^-4 at most
 
 // A CTA's partial records: that of its first unit and that of its last, where they are cut.
 struct RecHeader {
@@ -631,7 +632,7 @@ __device__ __forceinline__ float half_weights(uint32_t tS, const float4* sc, flo
 }
 
 // The same two steps for a tile with pieces (the bits of far) whose tokens have exponents of their own, in tab (of the
-// keys, of the values): the largest x, which takes the place of the logits, and then the weights, written over the first
+// keys, of the values), or with logits whose rounding is not small: the largest x, which takes the place of the logits, and then the weights, written over the first
 // 32 of the columns they come from; returns the sum of weight / value scale.  Seldom called.
 static __device__ __noinline__ float far_max(uint32_t tS, const Misc& mi, unsigned char* ws, uint32_t it, float fct, int lim) {
   const int hf = (threadIdx.x >> 7) & 1, slot = it % kSlots;
@@ -1038,6 +1039,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
       const int warp_end = __reduce_min_sync(0xffffffffu, end);
       float M = kMinitM, l = 0.f;
       bool any = false;  // this stream has had a tile of this segment
+      bool wide = false;  // its maxima are too large for that: every tile then goes the way of far ones
       for (int i = two ? 0 : s; i < nt; i += two ? 1 : 2) {
         const int t0 = (j0 + i) * kTok + 64 * hf, slot = (it0 + i) % kSlots;
         ok = wait(&mi.s_full[s], ns & 1);
@@ -1052,7 +1054,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
         float top = INFINITY, sum = 0.f;  // nothing stands before the first tile
         if (any) sum = masked ? half_weights<true>(tS, sc, fct, M, lim, pk, top) : half_weights<false>(tS, sc, fct, M, lim, pk, top);
         // (a stream whose wait gave up stops as one: the barrier carries that too)
-        if (any_of<2 * kRows>(kBarStream + s, top > kLazyM || !ok)) {
+        if (any_of<2 * kRows>(kBarStream + s, top > kLazyM || wide || !ok)) {
           if (any_of<2 * kRows>(kBarStream + s, !ok)) {
             ok = false;
             break;
@@ -1067,7 +1069,7 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
             mn = fmaxf(M, fmaxf(mx, *rx));
             *rx = mn;
           }
-          named_bar_sync(kBarStream + s, 2 * kRows);
+          wide = any_of<2 * kRows>(kBarStream + s, !hf && fabsf(mn) > kWideM && mn > kMinitM);
           if (hf) mn = *rx;
           const float al = ex2(M - mn);
           M = mn;
@@ -1083,7 +1085,8 @@ __global__ void __launch_bounds__(kMThreads, 1) query_many_kernel(KvqView v, Que
               tc::tmem_st16(tO + c, r);
             }
           }
-          if (far) {
+          if (wide && !far) far_max(tS, mi, ws, it0 + i, fct, lim);
+          if (far || wide) {
             sum = far_weights(tS, mi, ws, it0 + i, M);
             tc::tmem_ld32(tS, pk);
             tc::wait_ld(pk);

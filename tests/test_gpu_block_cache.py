@@ -1063,3 +1063,24 @@ def test_outgrown_workspaces_stay_below_the_one_in_use():
     for n in range(1, 80):
         cache.query_attention(torch.zeros(1, n, 2, 128, device="cuda").bfloat16())
         assert sum(w.numel() for w in cache._outgrown) <= cache.workspace.numel()
+
+
+def test_logits_far_below_zero():
+    """Every logit below -10^31: the largest still has the weight 1."""
+    cfg = cfg_of(8, 2, 128, E4, E4, 32, 32, 32)
+    T = 330
+    for heavy in (7, 328):                       # in a block, in the window
+        Ks, Vs = ([O.bf16(np.random.default_rng(h).standard_normal((T, 128))) for h in range(2)] for _ in range(2))
+        for x in Ks:
+            x[:] = 0.0
+            x[:, 0] = -2.0 ** 57
+            x[heavy, 0] = -2.0 ** 56
+        c = Case(cfg, [T], seed=3, streams=([Ks], [Vs]))
+        for n in (1, 5, 70):
+            q = np.zeros((1, n, 8, 128))
+            q[..., 0] = 2.0 ** 50
+            for cache in (c.cache, widened(c, 1 << 21).cache):
+                got = cache.query_attention(torch_src(q, cfg), causal=False).double().cpu().numpy()[0]
+                for h in range(2):
+                    Kd, Vd = O.dequantize_stream(cfg, c.states[0][h])
+                    assert np.all(np.abs(got[:, 4 * h:4 * h + 4] - Vd[heavy]) <= 2.0 ** -8 * np.abs(Vd[heavy])), (heavy, n, h)
