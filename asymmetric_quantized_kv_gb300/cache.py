@@ -49,7 +49,7 @@ class PagedKVCache:
         pages = torch.zeros(n_pages * B.kvq_page_bytes(cfg), dtype=torch.uint8, device=dev)
         if block_table is None:
             block_table = torch.arange(batch * max_pages_per_seq, dtype=torch.int32).reshape(batch, -1)
-        block_table = torch.as_tensor(block_table, dtype=torch.int32).reshape(batch, max_pages_per_seq).to(dev)
+        block_table = torch.as_tensor(block_table, dtype=torch.int32).reshape(batch, max_pages_per_seq).to(dev).contiguous()
         seq_lens = torch.zeros(batch, dtype=torch.int32, device=dev)
         R, H, D = cfg.residual, cfg.num_kv_heads, cfg.head_dim
         dt = src_torch_dtype(cfg)

@@ -295,3 +295,13 @@ def test_tables_and_buffers_off_the_device_are_refused(K):
     buffers["k_win"], buffers["v_win"] = (torch.zeros(1, 64, 8, 128, dtype=torch.bfloat16) for _ in range(2))
     with pytest.raises(ValueError, match="CUDA"):
         K.PagedKVCache.over(cfg, **buffers)
+
+
+def test_broadcast_block_table_is_laid_out(K):
+    """A table that is a broadcast view (all sequences over the same pages) is copied to whole rows."""
+    import torch
+    spec = (K.KVQ_FP8_E4M3, 0, K.KVQ_PER_BLOCK, 64)
+    cfg = K.make_config(8, 2, 64, spec, spec, 64, 64, src_dtype=K.KVQ_BF16)
+    table = torch.tensor([[1, 0, 2]], dtype=torch.int32).expand(4, 3)
+    c = K.PagedKVCache(cfg, 4, 3, n_pages=3, block_table=table, device="cpu")
+    assert c.block_table.is_contiguous() and c.block_table.tolist() == [[1, 0, 2]] * 4
