@@ -192,12 +192,24 @@ static bool takes_few(const KvqView& v, int batch, long long rows, int out_f32, 
                      : passes <= kFewPasses && pairs * passes <= 1024.0 && products <= 536870912.0;
 }
 
+// Decode calls (fp32 output) take as many runs as their records fit the fixed scratch array of
+// kvq_decode_attention_noalloc with, so that both entry points run the same plan and the latter takes wide groups too;
+// where pairs alone fill it, all.
+int few_runs(const KvqView& v, int batch, long long rows, int out_f32) {
+  if (!out_f32) return kFewUnits;
+  const long long passes = rows < 16 * kFewPasses ? (rows + 15) / 16 : kFewPasses, most = rows < 16 ? rows : 16;
+  const long long fit = (long long)((KVQ_NOALLOC_SCRATCH_BYTES - few_header_bytes(batch)) / (most * (v.D + 4) * sizeof(float))) -
+                        (long long)batch * v.Hkv * passes;
+  return fit < kFewLeast || fit > kFewUnits ? kFewUnits : (int)fit;
+}
+
 static size_t few_bytes(const KvqView& v, int batch, long long rows, int out_f32) {
   const long long pass = v.D > 128 || out_f32 ? 16 : kFewPass, pairs = (long long)batch * v.Hkv;
   const long long passes = rows < pass * kFewPasses ? (rows + pass - 1) / pass : kFewPasses;
-  long long records = (kFewUnits + pairs * passes) * (rows < pass ? rows : pass);
+  const long long runs = few_runs(v, batch, rows, out_f32);
+  long long records = (runs + pairs * passes) * (rows < pass ? rows : pass);
   if (few_small(v, batch, rows, v.P)) {  // as it may be, with the narrowest table
-    const long long by8 = (kFewUnits + pairs * ((rows + 7) / 8)) * (rows < 8 ? rows : 8);
+    const long long by8 = (runs + pairs * ((rows + 7) / 8)) * (rows < 8 ? rows : 8);
     if (by8 > records) records = by8;
   }
   return few_header_bytes(batch) + (size_t)records * (v.D + 4) * sizeof(float);

@@ -31,9 +31,9 @@ __device__ __forceinline__ int query_end(const QueryArgs& a, int T, int n, int i
 constexpr int kFewPass = 32;    // rows of the few-row kernel's widest pass
 constexpr int kFewPasses = 8;   // and passes of a launch
 constexpr int kFewSmallRows = 256;  // rows of a small call at most, in passes of 8
-// Its runs: four for each of the 1,824 warps that head_dim 128 fills a GPU with (records of 8 rows of that many
-// fit the fixed scratch array of kvq_decode_attention_noalloc).
-constexpr int kFewUnits = 7424;
+constexpr int kFewUnits = 7424;  // its runs at most: four for each of the 1,824 warps that head_dim 128 fills a GPU with
+constexpr int kFewLeast = 1216;  // and the fewest that a call is cut down to: one for each warp at two CTAs an SM
+int few_runs(const KvqView& v, int batch, long long rows, int out_f32);  // a call's
 constexpr int kManyGrid = 160;  // CTAs of the many-row kernel at most (one per SM)
 
 bool few_small(const KvqView& v, int batch, long long rows, long long tokens);  // whether passes of 8 rows take it

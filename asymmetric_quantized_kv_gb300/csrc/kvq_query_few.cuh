@@ -51,7 +51,6 @@ constexpr int kFWarps = 4;
 constexpr int kFThreads = kFWarps * 32;
 constexpr int kFStages = 3;
 constexpr int kRounds = 4;          // units per warp at most
-constexpr int kMaxUnits = kFewUnits;
 constexpr int kUnitTokens = 512;    // a warp takes several units only if they are this long
 constexpr int kMinUnit = 64;        // tokens of the smallest chunk
 constexpr float kLazy = 8.f;
@@ -82,9 +81,10 @@ __device__ __forceinline__ unsigned few_places(const FewPlan& p, unsigned n) {
   return p.aligned ? (n + p.run - 1) / p.run * p.run : n + kUnitCost;
 }
 
-// One warp; pref: B + 1 ints of shared memory, the places before a sequence.  workers: warps of the grid.  Lanes over
-// the sequences, whose lengths are read once (a decode step's time is a chain of such latencies).
-__device__ inline void few_plan(const KvqView& v, int heads, int sh, int workers, unsigned* pref, FewPlan* plan) {
+// One warp; pref: B + 1 ints of shared memory, the places before a sequence.  workers: warps of the grid; max_runs: the
+// call's, one a warp at least.  Lanes over the sequences, whose lengths are read once (a decode step's time is a chain of
+// such latencies).
+__device__ inline void few_plan(const KvqView& v, int heads, int sh, int workers, int max_runs, unsigned* pref, FewPlan* plan) {
   const int B = v.batch, lane = threadIdx.x & 31;
   unsigned sum = 0, some = 0;
 #pragma unroll 1
@@ -96,8 +96,8 @@ __device__ inline void few_plan(const KvqView& v, int heads, int sh, int workers
   }
   const unsigned work = __reduce_add_sync(0xffffffffu, sum) * heads;
   const unsigned rounds = min(max(work / workers / (unsigned)max(1, kUnitTokens >> (4 + sh)), 1u),
-                              (unsigned)min(kRounds, max(1, kMaxUnits / workers)));
-  const unsigned most = min(rounds * (unsigned)workers, (unsigned)kMaxUnits);
+                              (unsigned)min(kRounds, max(1, max_runs / workers)));
+  const unsigned most = min(rounds * (unsigned)workers, (unsigned)max_runs);
   FewPlan p;
   p.run = max((work + most - 1) / most, (unsigned)(kMinUnit / kTile));
   p.aligned = rounds == 1;
@@ -215,7 +215,7 @@ __device__ __forceinline__ void drop_not_finite(uint32_t (&wv)[4][W], int tok, i
 
 template <int F, int D, int NB, bool kF32>
 __global__ void __launch_bounds__(kFThreads, few_ctas<D, NB>())
-    query_few_kernel(KvqView v, QueryArgs a, int row_base, int passes, int sh, float* ws, int dynamic,
+    query_few_kernel(KvqView v, QueryArgs a, int row_base, int passes, int sh, int max_runs, float* ws, int dynamic,
                      const __grid_constant__ CUtensorMap tmap) {
   constexpr int NS = D / 16;      // steps of the first product, and channel tiles of the second
   constexpr int LC = D / 4;       // channels a lane holds of a key row
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kFThreads, few_ctas<D, NB>())
   __shared__ FewPlan s_plan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int workers = gridDim.x * kFWarps, heads = v.Hkv * passes;
-  if (warp == 0) few_plan(v, heads, sh, workers, pref, &s_plan);
+  if (warp == 0) few_plan(v, heads, sh, workers, max_runs, pref, &s_plan);
   __syncthreads();
   if (blockIdx.x == 0) {
     if (threadIdx.x == 0) *reinterpret_cast<FewPlan*>(ws) = s_plan;
@@ -828,7 +828,8 @@ kvq_status launch_few_t(const KvqView& v, const QueryArgs& a, int row0, int pass
                                        sizeof(FewSmem<D, NB>) + 1024 + sizeof(int) * (kMaxBatch + 1), &occ);
   if (so != KVQ_OK) return so;
   int grid = num_sms() * occ;
-  if (grid > kMaxUnits / kFWarps) grid = kMaxUnits / kFWarps;
+  const int max_runs = few_runs(v, v.batch, (long long)a.n_q * v.n_rep, a.out_f32);
+  if (grid > max_runs / kFWarps) grid = max_runs / kFWarps;
   // warps take their next unit from a counter where one may come (workers run at unequal speed);
   // a call too small for that saves the counter's clearing
   const long long pairs = (long long)v.batch * v.Hkv * passes;
@@ -838,7 +839,7 @@ kvq_status launch_few_t(const KvqView& v, const QueryArgs& a, int row0, int pass
   const int dynamic = most > (long long)grid * kFWarps * kUnitTokens;
   if (dynamic && cudaMemsetAsync(reinterpret_cast<char*>(ws) + few_counter_offset(v.batch), 0, 8, st) != cudaSuccess)
     return KVQ_ERR_CUDA;
-  kern<<<grid, kFThreads, smem, st>>>(v, a, row0, passes, sh, ws, dynamic, tmap);
+  kern<<<grid, kFThreads, smem, st>>>(v, a, row0, passes, sh, max_runs, ws, dynamic, tmap);
   if (cudaGetLastError() != cudaSuccess) return KVQ_ERR_CUDA;
   const long long rows = (long long)a.n_q * v.n_rep - row0;
   const int rows_max = (int)(rows < 8 * NB ? rows : 8 * NB);

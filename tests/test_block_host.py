@@ -305,3 +305,11 @@ def test_broadcast_block_table_is_laid_out(K):
     table = torch.tensor([[1, 0, 2]], dtype=torch.int32).expand(4, 3)
     c = K.PagedKVCache(cfg, 4, 3, n_pages=3, block_table=table, device="cpu")
     assert c.block_table.is_contiguous() and c.block_table.tolist() == [[1, 0, 2]] * 4
+
+
+@pytest.mark.parametrize("D,Hq,H,batch", [(128, 16, 1, 1), (128, 9, 1, 1), (128, 64, 8, 200), (256, 8, 1, 1), (256, 32, 2, 300),
+                                          (128, 128, 1, 64), (64, 64, 8, 1000), (256, 128, 8, 20)])
+def test_decode_workspaces_fit_the_library_s_own(K, D, Hq, H, batch):
+    """kvq_decode_attention_noalloc takes wide groups: their calls are cut into fewer runs."""
+    cfg = _cfg(K, num_q_heads=Hq, num_kv_heads=H, head_dim=D)
+    assert 0 < K.kvq_workspace_bytes(cfg, batch, 4096) <= K.KVQ_NOALLOC_SCRATCH_BYTES

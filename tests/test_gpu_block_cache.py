@@ -1084,3 +1084,17 @@ def test_logits_far_below_zero():
                 for h in range(2):
                     Kd, Vd = O.dequantize_stream(cfg, c.states[0][h])
                     assert np.all(np.abs(got[:, 4 * h:4 * h + 4] - Vd[heavy]) <= 2.0 ** -8 * np.abs(Vd[heavy])), (heavy, n, h)
+
+
+@pytest.mark.parametrize("D,Hq,H,Bn", [(128, 16, 1, 2), (256, 32, 2, 5), (128, 64, 8, 100), (128, 128, 1, 3), (256, 16, 1, 1)])
+def test_decode_without_a_workspace_wide_groups(D, Hq, H, Bn):
+    """Calls whose records would not fit the fixed array with all runs: the same bits as with a workspace, and the
+    oracle's outputs."""
+    import asymmetric_quantized_kv_gb300 as K
+    cfg = cfg_of(Hq, H, D, E4, E4, 64, 64, 64)
+    c = Case(cfg, [3000 if b == 0 else 100 + 37 * b for b in range(Bn)], seed=3)
+    q = torch_src(c.queries(), cfg)
+    out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    K.kvq_decode_attention_noalloc(c.c_cfg, c.cache.c, q, out, 0.0)
+    assert torch.equal(out, c.cache.attention(q))
+    c.check_attention()
