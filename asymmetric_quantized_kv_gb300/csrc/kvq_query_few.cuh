@@ -29,7 +29,7 @@
 //
 // Measured (8 kv-heads of 128): 8 x 131,072 tokens with 8 rows 354 us, 6.1 TB/s (89% of the
 // measured copy bandwidth); 64 sequences of 1,024 to 65,536 tokens, 1.10M in all, with 4
-// rows 367 us, 6.1 TB/s; 16 drafts of 5 tokens, 20 rows, 45 us, 1.9 TB/s, bound by the warps' issue (two a
+// rows 368 us, 6.1 TB/s; 16 drafts of 5 tokens, 20 rows, 46 us, 1.9 TB/s, bound by the warps' issue (two a
 // scheduler at 255 registers); 1 x 4,101 tokens 11 us, bound by latency: 2.5 us to start
 // and plan, 6 for a unit, mostly instructions that no cache holds yet, 2.5 for the merge.
 #pragma once

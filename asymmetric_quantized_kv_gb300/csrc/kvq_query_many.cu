@@ -33,11 +33,12 @@
 // takes an equal run of them, whatever the lengths are, so that all SMs finish together.
 // A unit cut by such a boundary leaves fp32 partial records, which a second kernel merges.
 //
-// Measured, 32 query heads on 8 kv-heads of 128: a causal prompt of 8,192 tokens takes 500 us, 1.1 PFLOP/s (56% of the
-// measured matrix rate); 4 x 1,000 queries over 30,011 tokens 1.58 ms, 1.24 PFLOP/s (63%).  A tile of 256 rows and
+// Measured, 32 query heads on 8 kv-heads of 128: a causal prompt of 8,192 tokens takes 485 us, 1.1 PFLOP/s (58% of the
+// measured matrix rate); 4 x 1,000 queries over 30,011 tokens 1.61 ms, 1.22 PFLOP/s (62%).  A tile of 256 rows and
 // 128 tokens takes about 3,500 cycles, 2,048 of them products; the rest is handshakes that the two streams overlap only
 // in part.  A unit's start and end take the time of 5 tiles, which bounds calls of short units: 16 x 448 queries on 16
-// heads of 64 over up to 1,500 tokens take 78 us, 0.16 PFLOP/s.
+// heads of 64 over up to 1,500 tokens take 84 us, 0.15 PFLOP/s.  (Two percent either way is where the code lies in the
+// instruction caches: changes to parts that a call does not run move its time by as much.)
 #include <math.h>
 
 #include "kvq_code.cuh"
