@@ -330,8 +330,11 @@ size_t kvq_query_workspace_bytes(const kvq_config* cfg, int32_t batch, int32_t n
  * NaN or infinite, in that channel or in all; an infinite key has the weight of its
  * logit (none for -inf).  Queries that do not see the token are not affected by it,
  * finite or not.  (A block's tokens share a scale, so a token's codes do depend on the
- * later tokens of its block once it is quantized.)  The tensor-core kernels want the
- * magnitudes of the values that a query sees within a factor of 2^90 of one another.
+ * later tokens of its block once it is quantized.)  On the tensor-core kernels an
+ * output is off by up to 2^-25 of the sum, over the tokens it sees, of the largest
+ * magnitude among the values of the token's block (of the token, in the window): a
+ * value 2^17 times the others costs the queries that see its block bits of those, in
+ * all channels.  Magnitudes may lie 2^90 apart at most.
  * softmax_scale: 0 means 1/sqrt(D).  workspace: as for
  * kvq_decode_attention, kvq_query_workspace_bytes(cfg, batch, n_q) bytes.
  * Every configuration is taken.  PER_BLOCK caches with bf16 sources run on

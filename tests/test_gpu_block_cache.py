@@ -1098,3 +1098,68 @@ def test_decode_without_a_workspace_wide_groups(D, Hq, H, Bn):
     K.kvq_decode_attention_noalloc(c.c_cfg, c.cache.c, q, out, 0.0)
     assert torch.equal(out, c.cache.attention(q))
     c.check_attention()
+
+
+def odd_values(g, Ks, Vs, lens, R, D):
+    """A few tokens, most of them in the window, with NaN, an infinity, zeros or a row far larger than the others."""
+    for _ in range(int(g.integers(0, 4))):
+        b, h = int(g.integers(0, len(lens))), int(g.integers(0, len(Ks[0])))
+        if lens[b] == 0:
+            continue
+        t = int(g.integers(0, lens[b])) if g.random() < 0.3 else lens[b] - 1 - int(g.integers(0, min(lens[b], R)))
+        X, kind = (Ks, Vs)[int(g.integers(0, 2))], int(g.integers(0, 4))
+        if kind == 0:
+            X[b][h][t, int(g.integers(0, D))] = np.nan
+        elif kind == 1:
+            X[b][h][t, int(g.integers(0, D))] = -np.inf
+        elif kind == 2:
+            X[b][h][t] = 0.0
+        else:
+            X[b][h][t] *= 2.0 ** (36 if X is Ks else 20)
+
+
+@pytest.mark.parametrize("copies", [1, 120])
+@pytest.mark.parametrize("first", range(0, 100, 20))
+def test_random_calls_with_odd_values(first, copies):
+    """Random shapes, formats, lengths and masks over tokens of any kind, alone and as many copies over shared pages
+    (many units of every kernel's split): finite rows within the bound, with 2^-25 of the largest magnitude of each
+    token's block (in the window, of the token) in place of the channel's, rows that see NaN not finite."""
+    import asymmetric_quantized_kv_gb300 as K
+    for seed in range(first, first + 20):
+        g = np.random.default_rng(1000 * copies + seed)
+        D, H, rep = int(g.choice([64, 128, 128, 256])), int(g.choice([1, 2, 3])), int(g.choice([1, 2, 4, 5, 8]))
+        G, P, fmt = int(g.choice([16, 32, 64])), int(g.choice([16, 64, 128])), int(g.choice([E4, E5, I8]))
+        R = G * int(g.choice([1, 2, 3]))
+        n, causal = int(g.choice([1, 2, 5, 9, 17, 33, 70, 140])), bool(g.random() < 0.7)
+        lens = [int(g.choice([int(g.integers(0, 130)), int(g.integers(0, 3 * R + 300))])) for _ in range(int(g.integers(1, 4)))]
+        cfg = cfg_of(H * rep, H, D, fmt, fmt, G, R, P, meta_dtype=O.F16 if seed % 5 == 0 else O.F32)
+        Ks, Vs = ([[O.bf16(g.standard_normal((T, D))) for _ in range(H)] for T in lens] for _ in range(2))
+        odd_values(g, Ks, Vs, lens, R, D)
+        with np.errstate(all="ignore"):
+            c = Case(cfg, lens, seed=1, streams=(Ks, Vs))
+        q = O.bf16(g.standard_normal((len(lens), n, H * rep, D)))
+        m = c.cache
+        caches = [m, widened(c, 1 << 21).cache] if copies == 1 else [K.PagedKVCache.over(
+            c.c_cfg, m.pages, m.block_table.repeat(copies, 1), m.seq_lens.repeat(copies), m.k_win.repeat(copies, 1, 1, 1),
+            m.v_win.repeat(copies, 1, 1, 1))]
+        got = [x.query_attention(torch_src(q, cfg).repeat(copies, 1, 1, 1), causal=causal).double().cpu().numpy()
+               .reshape(copies, *q.shape) for x in caches]
+        got = np.concatenate(got)
+        assert all(int(x.status.item()) == 0 for x in caches)
+        for b, T in enumerate(lens):
+            nq = T // R * R
+            for h in range(H):
+                Kd, Vd = O.dequantize_stream(cfg, c.states[b][h])
+                a = np.abs(Vd).max(1, initial=0.0)
+                a[:nq] = np.repeat(a[:nq].reshape(-1, G).max(1, initial=0.0), G)
+                for i in range(n):
+                    end = max(0, T - n + i + 1) if causal else T
+                    y, k, v = got[:, b, i, h * rep:(h + 1) * rep], Kd[:end], Vd[:end]
+                    if np.isfinite(k).all() and np.isfinite(v).all():
+                        ref, size = O.query_attention(q[b, i:i + 1, h * rep:(h + 1) * rep], k, v, False)
+                        lim = 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * size + 2.0 ** -25 * a[:end].sum()
+                        assert np.all(np.abs(y - ref[0]) <= lim[0]), (seed, b, h, i)
+                    elif np.isnan(k).any():
+                        assert np.isnan(y).all(), (seed, b, h, i)
+                    elif np.isfinite(k).all():
+                        assert not np.isfinite(y[..., np.isnan(v).any(0)]).any(), (seed, b, h, i)
